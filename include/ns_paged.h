@@ -88,6 +88,7 @@ typedef enum ns_dtype { NS_F16 = 0, NS_BF16 = 1 } ns_dtype;
 #define NS_DEV_FUSED_SLOT 0x10u      /* fused append: slot is not the slot of position L-1 */
 #define NS_DEV_BAD_QUERY_SPAN 0x20u  /* prefill: query span longer than the context, or negative */
 #define NS_DEV_MERGE_QUEUE 0x40u     /* decode: a CTA's merge queue overflowed (a merge was skipped) */
+#define NS_DEV_BAD_TOKEN 0x80u       /* verification: a drafted token outside [0, vocab_size) */
 
 /* Human-readable name of a status code (static string). */
 const char *ns_status_string(ns_status status);
@@ -443,6 +444,150 @@ ns_status ns_kv_append_paged_attn_decode_q8_0(const void *q, const void *k_new, 
                                              ns_stream_t stream, int max_blocks_per_seq,
                                              int64_t num_blocks, ns_dtype dtype, void *workspace,
                                              size_t workspace_bytes);
+
+/*
+ * Workspace of the span attention calls (ns_prompt_attn and
+ * ns_paged_attn_prefill_q8_0): partial rows of the query tiles that were cut
+ * across CTAs.  Its size depends on head_dim alone (64 or 128; 0 for others),
+ * its contents need no initialisation and carry nothing from one call to the
+ * next.  Two calls that share a workspace must not run concurrently, nor may
+ * two captured graphs that share one.
+ */
+size_t ns_span_attn_workspace_bytes(int head_dim);
+
+/*
+ * ns_prompt_attn -- causal attention of whole prompts, straight from the
+ * projection's rows (no cache): packed sequences of different lengths.
+ *
+ * Sequence s owns query rows query_start_loc[s] .. query_start_loc[s+1]-1 and
+ * key rows key_start_loc[s] .. key_start_loc[s+1]-1 of k and v.  With n query
+ * rows and L key rows, query row i sits at position L-n+i and sees the keys
+ * p <= L-n+i; with h = j / (num_q_heads/num_kv_heads):
+ *   z_p = scale * sum_d q[i][j][d] * k[p][h][d],  p = 0 .. L-n+i
+ *   out[i][j][:] = sum_p softmax(z)_p * v[p][h][:]
+ * key_start_loc NULL means query_start_loc (every token sees itself and the
+ * tokens before it).  More keys than queries put a prefix in front (rows read
+ * back with ns_kv_gather); with fewer, the first n-L rows see no key and get
+ * 0.  Rows of q behind the last sequence are not read, their rows of out not
+ * written.
+ *
+ *   q       [total_q_tokens][num_q_heads][head_dim], rows q_row_stride
+ *           elements apart (read)
+ *   k, v    [total_k_tokens][num_kv_heads][head_dim], rows k_row_stride and
+ *           v_row_stride elements apart (read): the slices of a fused
+ *           projection need no copy
+ *   query_start_loc, key_start_loc  int32 [num_seqs+1], nondecreasing, first
+ *           entry >= 0, last <= the tensor's rows (read).  A sequence whose
+ *           entries break that is skipped and sets NS_DEV_BAD_QUERY_SPAN.
+ *   out     [total_q_tokens][num_q_heads][head_dim], dense (written)
+ * Strides are multiples of 8 and at least the heads' width.  head_dim is 64
+ * or 128; num_q_heads / num_kv_heads is any whole number up to 64.  A value
+ * that is infinite or NaN in k or v may reach every row of its own sequence,
+ * and no other sequence.
+ */
+ns_status ns_prompt_attn(const void *q, const void *k, const void *v, const int32_t *query_start_loc,
+                         const int32_t *key_start_loc, int num_seqs, int total_q_tokens,
+                         int total_k_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                         int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride, float scale,
+                         void *out, ns_stream_t stream, ns_dtype dtype, void *workspace,
+                         size_t workspace_bytes);
+
+/*
+ * ns_paged_attn_prefill_q8_0 -- ns_paged_attn_prefill over a q8_0 pool: the
+ * attention of the query spans query_start_loc (prompt chunks, drafted
+ * tokens, decode rows) over everything in the cache up to each token's own
+ * position, K_s[p] and V_s[p] being the dequantised rows (fp16(d) * code).
+ * The span's own tokens must already be in the pool (ns_kv_append_q8_0).
+ * head_dim 64, block_size 16; num_q_heads / num_kv_heads any whole number up
+ * to 64.  A span longer than its context, negative or outside the query rows
+ * is skipped (NS_DEV_BAD_QUERY_SPAN), as is a sequence whose context exceeds
+ * its table row (NS_DEV_BAD_CONTEXT_LEN); a block id outside the pool sets
+ * NS_DEV_BAD_BLOCK_ID and its tokens are left out.  workspace:
+ * ns_span_attn_workspace_bytes(64).
+ */
+ns_status ns_paged_attn_prefill_q8_0(const void *q, const int32_t *query_start_loc, const void *k_codes,
+                                     const void *k_scales, const void *v_codes, const void *v_scales,
+                                     const int32_t *block_tables, const int32_t *context_lens,
+                                     int num_seqs, int total_q_tokens, int num_q_heads,
+                                     int num_kv_heads, int head_dim, int block_size, float scale,
+                                     void *out, ns_stream_t stream, int max_blocks_per_seq,
+                                     int64_t num_blocks, ns_dtype dtype, void *workspace,
+                                     size_t workspace_bytes);
+
+/*
+ * ns_kv_gather -- read sequences back from the pool into packed rows:
+ *   k_out[start_loc[s] + p][h][:] = K_s[p][h][:]   (same for v)
+ * for p = 0 .. start_loc[s+1]-start_loc[s]-1, the first tokens of sequence s.
+ * A bit-exact copy; the inverse of ns_kv_append.  The rows feed
+ * ns_prompt_attn as a prefix, leave the GPU, or return through ns_kv_append.
+ *
+ *   start_loc    int32 [num_seqs+1], nondecreasing, first entry >= 0, last <=
+ *                total_tokens (read); rows outside every sequence are left as
+ *                they were
+ *   k_out, v_out [total_tokens][num_kv_heads][head_dim], dense (written)
+ * A sequence whose entries break that order is skipped
+ * (NS_DEV_BAD_QUERY_SPAN), one with more tokens than its table row holds too
+ * (NS_DEV_BAD_CONTEXT_LEN); the rows of a block id outside the pool are left
+ * as they were (NS_DEV_BAD_BLOCK_ID).
+ */
+ns_status ns_kv_gather(const void *k_pool, const void *v_pool, const int32_t *block_tables,
+                       const int32_t *start_loc, int num_seqs, int total_tokens, int num_kv_heads,
+                       int head_dim, int block_size, void *k_out, void *v_out, ns_stream_t stream,
+                       int max_blocks_per_seq, int64_t num_blocks, ns_dtype dtype);
+
+/*
+ * ns_kv_gather_q8_0 -- ns_kv_gather from a q8_0 pool (head_dim 64, block_size
+ * 4, 8, 16 or 32): each value is fp16(d) * code rounded once to dtype (fp16
+ * saturates nowhere: a product beyond its range becomes infinite).
+ */
+ns_status ns_kv_gather_q8_0(const void *k_codes, const void *k_scales, const void *v_codes,
+                            const void *v_scales, const int32_t *block_tables, const int32_t *start_loc,
+                            int num_seqs, int total_tokens, int num_kv_heads, int head_dim,
+                            int block_size, void *k_out, void *v_out, ns_stream_t stream,
+                            int max_blocks_per_seq, int64_t num_blocks, ns_dtype dtype);
+
+/*
+ * ns_verify_drafts -- verification of drafted tokens against the target's
+ * probabilities, from given random numbers (speculative sampling).
+ *
+ * Sequence s drafted n = draft_start_loc[s+1]-draft_start_loc[s] tokens x_0 ..
+ * x_{n-1}; its n+1 target rows p_0 .. p_n start at row draft_start_loc[s]+s of
+ * target_probs (row i is the distribution that judges draft i, row n that of
+ * the token after all of them), its draft rows q_0 .. q_{n-1} at row
+ * draft_start_loc[s] of draft_probs.
+ *   draft i is accepted when accept_uniforms[draft_start_loc[s]+i] * q_i(x_i)
+ *     < p_i(x_i); a = the number accepted before the first that is not
+ *   w(v) = max(p_a(v) - q_a(v), 0) when a < n (p_a(v) where all of these are
+ *     0), p_n(v) when a == n
+ *   y = the smallest v with w(0) + .. + w(v) > sample_uniforms[s] * sum w
+ * The packed rows draft_start_loc[s]+s .. +n of out_tokens get x_0 .. x_{a-1},
+ * y, then -1; num_accepted[s] = a.  The tokens then follow the target's
+ * distribution whatever the drafts were.  Products, sums and comparisons are
+ * exact or carry at least 45 bits, so that a value next to a border decides
+ * as it does in fp64.  A NaN probability counts as 0; without any positive
+ * weight y = -1.
+ *
+ *   target_probs  float [total_drafts+num_seqs][vocab_size], rows
+ *                 target_row_stride elements apart (read)
+ *   draft_probs   float [total_drafts][vocab_size], rows draft_row_stride
+ *                 elements apart (read), or NULL: every draft was certain
+ *                 (q_i is 1 at x_i and 0 elsewhere, as for drafts looked up)
+ *   draft_tokens  int32 [total_drafts] (read); out_tokens int32
+ *                 [total_drafts+num_seqs], num_accepted int32 [num_seqs]
+ *                 (written)
+ *   draft_start_loc  int32 [num_seqs+1], nondecreasing, first entry >= 0, last
+ *                 <= total_drafts (read)
+ *   accept_uniforms, sample_uniforms  float [total_drafts], [num_seqs], in
+ *                 [0, 1) (read)
+ * A sequence whose entries of draft_start_loc break that is skipped
+ * (NS_DEV_BAD_QUERY_SPAN); one with a drafted token outside the vocabulary
+ * gets -1 everywhere (NS_DEV_BAD_TOKEN).
+ */
+ns_status ns_verify_drafts(const float *target_probs, const float *draft_probs, const int32_t *draft_tokens,
+                           const int32_t *draft_start_loc, const float *accept_uniforms,
+                           const float *sample_uniforms, int num_seqs, int total_drafts, int vocab_size,
+                           int64_t target_row_stride, int64_t draft_row_stride, int32_t *out_tokens,
+                           int32_t *num_accepted, ns_stream_t stream);
 
 /*
  * Device status word of the current device: OR of NS_DEV_* bits raised by

@@ -31,6 +31,7 @@ DEV_BITS = {
     0x10: "NS_DEV_FUSED_SLOT",
     0x20: "NS_DEV_BAD_QUERY_SPAN",
     0x40: "NS_DEV_MERGE_QUEUE",
+    0x80: "NS_DEV_BAD_TOKEN",
 }
 
 
@@ -86,6 +87,12 @@ _SIGNATURES = {
     "ns_paged_attn_decode_q8_0": (I, [P, P, P, P, P, P, P, I, I, I, I, I, F, P, P, I, I64, I, P, SZ]),
     "ns_kv_append_paged_attn_decode_q8_0": (I, [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, F, P, P, I,
                                                 I64, I, P, SZ]),
+    "ns_span_attn_workspace_bytes": (SZ, [I]),
+    "ns_prompt_attn": (I, [P, P, P, P, P, I, I, I, I, I, I, I64, I64, I64, F, P, P, I, P, SZ]),
+    "ns_paged_attn_prefill_q8_0": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, I, I64, I, P, SZ]),
+    "ns_kv_gather": (I, [P, P, P, P, I, I, I, I, I, P, P, P, I, I64, I]),
+    "ns_kv_gather_q8_0": (I, [P, P, P, P, P, P, I, I, I, I, I, P, P, P, I, I64, I]),
+    "ns_verify_drafts": (I, [P, P, P, P, P, P, I, I, I, I64, I64, P, P, P]),
 }
 
 
@@ -188,8 +195,8 @@ class PreparedCall:
 
 def prepare(fn, *args, **kwargs) -> PreparedCall:
     """``fn`` (a launching entry point of this module: ns_kv_append,
-    ns_paged_attn_decode, ns_kv_append_paged_attn_decode, ns_paged_attn_prefill
-    or a q8_0 one) with these arguments, checked now and run by calling the
+    ns_paged_attn_decode, ns_kv_append_paged_attn_decode, ns_paged_attn_prefill,
+    a q8_0 one, ns_prompt_attn, ns_kv_gather or ns_verify_drafts) with these arguments, checked now and run by calling the
     returned object.  It is what a serving loop that calls the same step on the
     same buffers every iteration uses, so that a call costs the host one
     foreign call."""
@@ -385,6 +392,149 @@ def ns_kv_append_paged_attn_decode_q8_0(q, k_new, v_new, slot_mapping, k_codes, 
         hkv, d, bs, float(scale), _dev(out, "out", q.dtype), _stream(stream), block_tables.shape[1], nb,
         _dtype_code(q), _dev(workspace, "workspace", torch.uint8), workspace.numel())
     _check(st, "ns_kv_append_paged_attn_decode_q8_0")
+
+
+def _rows(t: torch.Tensor, name: str, dtype) -> int:
+    """Pointer of [T, H, D] rows that are dense themselves and any stride apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() and ((t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1)):
+        raise ValueError(f"the rows of {name} must be dense [heads, head_dim]")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements from one row to the next; with no next row, the row's own width."""
+    return t.stride(0) if t.shape[0] > 1 else t[0].numel() if t.shape[0] else t.shape[1] * t.shape[2]
+
+
+def ns_span_attn_workspace_bytes(head_dim: int = 64) -> int:
+    return int(lib().ns_span_attn_workspace_bytes(head_dim))
+
+
+def alloc_span_workspace(head_dim: int = 64, device=None) -> torch.Tensor:
+    """A workspace for ns_prompt_attn and ns_paged_attn_prefill_q8_0 (its contents need no initialisation)."""
+    return torch.empty(ns_span_attn_workspace_bytes(head_dim), dtype=torch.uint8, device=device or "cuda")
+
+
+def ns_prompt_attn(q, k, v, query_start_loc, scale, out, workspace, key_start_loc=None, stream=None):
+    """Causal attention of packed prompts: q [T, Hq, D] over k and v [T', Hkv, D] (rows any stride
+    apart); sequence s owns the rows query_start_loc[s]..[s+1] (int32 [S+1]) of q, and of k and v
+    unless key_start_loc says otherwise."""
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [T, Hq, D], k and v [T', Hkv, D]")
+    T, hq, d = q.shape
+    Tk, hkv, _ = k.shape
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    S = query_start_loc.shape[0] - 1
+    if query_start_loc.dim() != 1 or S < 0:
+        raise ValueError("query_start_loc must be [num_seqs + 1]")
+    if key_start_loc is None:
+        if Tk != T:
+            raise ValueError("k and v must have q's rows when key_start_loc is not given")
+    elif key_start_loc.shape != query_start_loc.shape:
+        raise ValueError("key_start_loc must be [num_seqs + 1]")
+    dt = _dtype_code(q)
+    st = _invoke("ns_prompt_attn", _rows(q, "q", q.dtype), _rows(k, "k", q.dtype), _rows(v, "v", q.dtype),
+                 _dev(query_start_loc, "query_start_loc", torch.int32),
+                 None if key_start_loc is None else _dev(key_start_loc, "key_start_loc", torch.int32),
+                 S, T, Tk, hq, hkv, d, _row_stride(q), _row_stride(k), _row_stride(v), float(scale),
+                 _dev(out, "out", q.dtype), _stream(stream), dt, _dev(workspace, "workspace", torch.uint8),
+                 workspace.numel())
+    _check(st, "ns_prompt_attn")
+
+
+def ns_paged_attn_prefill_q8_0(q, query_start_loc, k_codes, k_scales, v_codes, v_scales, block_tables,
+                               context_lens, scale, out, workspace, stream=None):
+    """Attention of the query spans ``query_start_loc`` over a q8_0 pool (block size 16); the workspace
+    is alloc_span_workspace's."""
+    T, hq, d = q.shape
+    nb, hkv, bs, d2, kc, ks, vc, vs = _q8_pools(k_codes, k_scales, v_codes, v_scales)
+    S = context_lens.shape[0]
+    if d2 != d or out.shape != q.shape or query_start_loc.shape != (S + 1,) or block_tables.dim() != 2 \
+            or block_tables.shape[0] != S:
+        raise ValueError("shape mismatch")
+    st = _invoke("ns_paged_attn_prefill_q8_0",
+                 _dev(q, "q"), _dev(query_start_loc, "query_start_loc", torch.int32), kc, ks, vc, vs,
+                 _dev(block_tables, "block_tables", torch.int32), _dev(context_lens, "context_lens", torch.int32),
+                 S, T, hq, hkv, d, bs, float(scale), _dev(out, "out", q.dtype), _stream(stream),
+                 block_tables.shape[1], nb, _dtype_code(q), _dev(workspace, "workspace", torch.uint8),
+                 workspace.numel())
+    _check(st, "ns_paged_attn_prefill_q8_0")
+
+
+def _gather_shapes(nb, hkv, d, block_tables, start_loc, k_out, v_out):
+    if k_out.dim() != 3 or k_out.shape[1:] != (hkv, d) or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+        raise ValueError("k_out and v_out must be [total_tokens, Hkv, D]")
+    if block_tables.dim() != 2 or start_loc.shape != (block_tables.shape[0] + 1,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq], start_loc [num_seqs + 1]")
+
+
+def ns_kv_gather(k_pool, v_pool, block_tables, start_loc, k_out, v_out, stream=None):
+    """Read the first start_loc[s+1]-start_loc[s] tokens of each sequence from the pools into the
+    packed rows k_out/v_out [T, Hkv, D]."""
+    nb, hkv, bs, d = k_pool.shape
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("shape mismatch")
+    _gather_shapes(nb, hkv, d, block_tables, start_loc, k_out, v_out)
+    st = _invoke("ns_kv_gather", _dev(k_pool, "k_pool", k_out.dtype), _dev(v_pool, "v_pool", k_out.dtype),
+                 _dev(block_tables, "block_tables", torch.int32), _dev(start_loc, "start_loc", torch.int32),
+                 block_tables.shape[0], k_out.shape[0], hkv, d, bs, _dev(k_out, "k_out"),
+                 _dev(v_out, "v_out"), _stream(stream), block_tables.shape[1], nb, _dtype_code(k_out))
+    _check(st, "ns_kv_gather")
+
+
+def ns_kv_gather_q8_0(k_codes, k_scales, v_codes, v_scales, block_tables, start_loc, k_out, v_out, stream=None):
+    """ns_kv_gather from a q8_0 pool: the dequantised rows, rounded to k_out's type."""
+    nb, hkv, bs, d, kc, ks, vc, vs = _q8_pools(k_codes, k_scales, v_codes, v_scales)
+    _gather_shapes(nb, hkv, d, block_tables, start_loc, k_out, v_out)
+    st = _invoke("ns_kv_gather_q8_0", kc, ks, vc, vs, _dev(block_tables, "block_tables", torch.int32),
+                 _dev(start_loc, "start_loc", torch.int32), block_tables.shape[0], k_out.shape[0], hkv, d, bs,
+                 _dev(k_out, "k_out"), _dev(v_out, "v_out"), _stream(stream), block_tables.shape[1], nb,
+                 _dtype_code(k_out))
+    _check(st, "ns_kv_gather_q8_0")
+
+
+def _prob_rows(t, name):
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be dense")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def ns_verify_drafts(target_probs, draft_probs, draft_tokens, draft_start_loc, accept_uniforms, sample_uniforms,
+                     out_tokens, num_accepted, stream=None):
+    """Verify the drafted tokens of each sequence against the target's probabilities.
+
+    target_probs float32 [T + S, V] (a sequence of n drafts has n + 1 rows), draft_probs [T, V] or
+    None (certain drafts), draft_tokens int32 [T], draft_start_loc int32 [S + 1], uniforms in [0, 1).
+    Writes out_tokens int32 [T + S] (accepted drafts, the drawn token, then -1) and num_accepted [S].
+    """
+    T, S = draft_tokens.shape[0], num_accepted.shape[0]
+    if target_probs.dim() != 2 or target_probs.shape[0] != T + S or out_tokens.shape != (T + S,):
+        raise ValueError("target_probs must be [num_drafts + num_seqs, V], out_tokens [num_drafts + num_seqs]")
+    V = target_probs.shape[1]
+    if draft_probs is not None and draft_probs.shape != (T, V):
+        raise ValueError("draft_probs must be [num_drafts, V]")
+    if draft_start_loc.shape != (S + 1,) or accept_uniforms.shape != (T,) or sample_uniforms.shape != (S,):
+        raise ValueError("draft_start_loc must be [S + 1], accept_uniforms [num_drafts], sample_uniforms [S]")
+    p, ps = _prob_rows(target_probs, "target_probs")
+    q, qs = (None, 0) if draft_probs is None else _prob_rows(draft_probs, "draft_probs")
+    st = _invoke("ns_verify_drafts", p, q, _dev(draft_tokens, "draft_tokens", torch.int32),
+                 _dev(draft_start_loc, "draft_start_loc", torch.int32),
+                 _dev(accept_uniforms, "accept_uniforms", torch.float32),
+                 _dev(sample_uniforms, "sample_uniforms", torch.float32), S, T, V, ps, qs,
+                 _dev(out_tokens, "out_tokens", torch.int32), _dev(num_accepted, "num_accepted", torch.int32),
+                 _stream(stream))
+    _check(st, "ns_verify_drafts")
 
 
 def ns_read_decode_plan(workspace, stream=None) -> dict:

@@ -47,4 +47,55 @@ cudaError_t launch_tc_prefill(const void *q, const int32_t *query_start_loc, con
                               int min_span, int head_dim, unsigned *status, bool after_walk,
                               cudaStream_t stream);
 
+// Attention of query spans over contiguous K/V rows (ns_prompt_attn) or a
+// q8_0 pool (ns_paged_attn_prefill_q8_0).
+struct SpanAttnArgs {
+    const void *q;
+    const int32_t *query_start_loc;
+    int num_seqs, total_q_tokens, num_q_heads, num_kv_heads, head_dim;
+    long long q_row_stride;  // elements
+    float scale;
+    void *out;
+    ns_dtype dtype;
+    void *workspace;
+    unsigned *status;
+    // contiguous rows
+    const void *k, *v;
+    const int32_t *key_start_loc;
+    int total_k_tokens;
+    long long k_row_stride, v_row_stride;
+    // q8_0 pool
+    const void *k_codes, *k_scales, *v_codes, *v_scales;
+    const int32_t *block_tables, *context_lens;
+    int max_blocks_per_seq;
+    long long num_blocks;
+};
+constexpr int kMaxSpanGroup = 64;  // query heads per kv head
+size_t span_attn_workspace_bytes(int head_dim);
+cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream);
+
+// Pool rows of the sequences start_loc, packed: 16-bit copies or q8_0 values.
+struct GatherArgs {
+    const void *k, *v;                // 16-bit pools, or codes
+    const void *k_scales, *v_scales;  // q8_0 only
+    const int32_t *block_tables, *start_loc;
+    int num_seqs, total_tokens, num_kv_heads, head_dim, block_size, max_blocks_per_seq;
+    long long num_blocks;
+    void *k_out, *v_out;
+    ns_dtype dtype;
+    unsigned *status;
+};
+cudaError_t launch_kv_gather(const GatherArgs &a, bool q8, cudaStream_t stream);
+
+struct VerifyArgs {
+    const float *target, *draft;
+    const int32_t *tokens, *start;
+    const float *accept_u, *sample_u;
+    int num_seqs, total_drafts, vocab;
+    long long target_stride, draft_stride;
+    int32_t *out_tokens, *num_accepted;
+    unsigned *status;
+};
+cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t stream);
+
 }  // namespace ns
