@@ -1,0 +1,1127 @@
+// span_attn.cuh -- causal attention of query spans on the tcgen05 tensor cores:
+// whole packed prompts over contiguous K/V rows, or new tokens over a q8_0
+// paged cache.
+//
+// Row i of a span of n tokens over L keys sits at position L-n+i and sees the
+// keys p <= L-n+i: out = sum_p 2^(z_p - m) v_p / sum_p 2^(z_p - m) with z in
+// log2 units, one pass over the keys with a running reference m.
+//
+// Unit of work: (sequence, kv head, 2 QT query tokens), QT = 128 / G for groups
+// of G query heads.  A unit is two query tiles of QT tokens x G heads (row r of a
+// tile: token r / G, head r % G), so every K/V tile is loaded once for up to 256
+// rows.  The units of a call are laid end to end, each as long as the keys it
+// sees, and every CTA of a persistent grid takes an equal run of that line: long
+// and short sequences, prompts and single tokens share the SMs evenly.  A unit
+// that a cut falls into leaves its parts in fp32 records, and a second small
+// kernel joins them.
+//
+// Warps of a CTA (512 threads):
+//   0-3, 4-7  softmax of query tile 0 and 1: a thread owns a row.  It lays its row
+//             of Q into shared memory, reads its row of S from TMEM, and writes P
+//             (fp16) back to TMEM;
+//   8-11      conversion: K and V tiles into the form that the products take;
+//   12        producer: TMA copies of K and V tiles;
+//   13, 14    issue S = Q K^T and O += P V;
+//   15        walks the CTA's run of units.
+// The two tiles' softmax and products alternate by themselves: while one tile's
+// scores are exponentiated, the other's products run.
+//
+// P is rounded to fp16 (11 bits) for both types: the products of a bf16 call
+// would need P in two bf16 parts for the same accuracy, twice the value products.
+// So V is fp16 too: a bf16 tile is scaled by a power of two, 2^-Ev, that puts its
+// largest value just below 2^15, which keeps every value within 2^-29 of that
+// exact.  Ev moves into the exponent of P, 2^(z + Ev - m), with m a running
+// reference of z + Ev; the sum takes it back out.  q8_0 tiles are dequantised to
+// fp16 in the same way, with Ek for K in the score's scale.
+#pragma once
+
+#include <algorithm>
+#include <cstddef>
+
+#include "ns_internal.h"
+#include "tcgen05.cuh"
+
+namespace ns {
+namespace span {
+
+constexpr int kRows = 128;       // rows of a query tile (MMA M)
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRegs = 128;       // registers a thread at launch; the warpgroups then share them out:
+constexpr int kSoftmaxRegs = 200, kConvertRegs = 64, kOtherRegs = 48;
+static_assert(2 * kSoftmaxRegs + kConvertRegs + kOtherRegs <= 4 * kRegs, "the shares fit the launch's registers");
+constexpr int kConvertWarp = 8, kProducerWarp = 12, kScoreWarp = 13, kValueWarp = 14, kPlanWarp = 15;
+constexpr int kPanel = 128;      // bytes of a row of a panel: 64 elements, one swizzle span
+constexpr int kUnits = 4;        // units announced ahead
+constexpr int kMaxCtas = 160;    // grid, at most: the workspace has two records for each
+constexpr float kSlack = 8.0f;   // the reference moves when a score passes it by more (log2 units)
+
+template <int D, bool Q8>
+struct Geo {
+    static constexpr int KT = D == 64 ? 128 : 64;  // keys of a tile
+    static constexpr int REG = D / 64;             // panels of a row
+    static constexpr int TILE = REG * KT * kPanel; // bytes of a K or V tile
+    static constexpr int STAGES = Q8 ? 3 : 4;
+    static constexpr int RAW = Q8 ? 4 : 1;         // q8_0 tiles in flight
+    // TMEM columns: S of tile t at KT t, O at 2 KT + D t, P at 2 KT + 2 D + KT / 2 t
+    static constexpr int O = 2 * KT, P = 2 * KT + 2 * D;
+    static_assert(P + KT <= 512, "tensor memory");
+    // cost of a unit besides its keys (laying out Q, filling the pipe, the epilogue)
+    // and the least cost that a CTA is given, in keys
+    static constexpr int OVERHEAD = 2 * KT;
+    static constexpr int SHARE = 4 * KT;
+};
+
+// A CTA's part of a unit: key tiles [t0, t1).
+struct Unit {
+    int s, h, i0, n, L;  // sequence, kv head, first token, span, keys
+    int q0, k0;          // first rows of the sequence
+    int t0, t1;          // t1 < 0: no more units
+    int rec;             // record of a cut unit, or -1
+};
+
+// What a CTA tells the joining kernel.
+struct alignas(16) Header {
+    int own;               // it holds the first part of a cut unit (record 2 c + 1)
+    int row0, tokens, h;   // that unit's first query row, its tokens, its kv head
+    int head;              // it holds a later part (record 2 c)
+    int ends;              // which is the last
+    int pad[2];
+};
+
+constexpr size_t record_floats(int D) { return (size_t)2 * kRows * (D + 2); }
+constexpr size_t header_bytes() { return kMaxCtas * sizeof(Header); }
+
+struct Params {
+    SpanAttnArgs a;
+    int group, qt;
+    float scale_log2;  // of |scale|; its sign goes into Q
+    uint32_t q_flip;   // sign bits to flip in a word of Q
+    Header *headers;
+    float *records;
+};
+
+template <int D, bool Q8>
+struct alignas(1024) Smem {
+    using GG = Geo<D, Q8>;
+    uint8_t q[2][GG::REG * kRows * kPanel];
+    uint8_t k[GG::STAGES][GG::TILE];
+    uint8_t v[GG::STAGES][GG::TILE];
+    uint8_t raw[GG::RAW][Q8 ? 2 * GG::KT * 64 + 2 * GG::KT * 4 : 16];  // codes of K, of V, scales of K, of V
+    uint64_t raw_full[GG::RAW], raw_empty[GG::RAW];
+    uint64_t v_full[GG::STAGES];
+    uint64_t k_ready[GG::STAGES], v_ready[GG::STAGES], k_empty[GG::STAGES], v_empty[GG::STAGES];
+    uint64_t q_ready[2], s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t u_full[kUnits], u_empty[kUnits];
+    uint64_t topped;  // the conversion warps have their maxima in place
+    Unit unit[kUnits], no_unit;
+    float ek[GG::STAGES], ev[GG::STAGES];   // exponents of a stage's tiles
+    uint32_t loaded[GG::STAGES];            // q8_0: blocks of the tile that were read
+    uint32_t raw_loaded[GG::RAW];
+    uint32_t top[2][2][4];                  // the conversion warps' maxima
+    long long scan[kWarps];
+    long long start_x, x0, x1;
+    int start_s;
+    uint32_t tmem_base;
+};
+
+template <int D, bool Q8>
+constexpr size_t smem_bytes()
+{
+    return sizeof(Smem<D, Q8>) + 1024;
+}
+
+// ---------------------------------------------------------------------------
+// The line of work
+// ---------------------------------------------------------------------------
+struct Seq {
+    int q0, n, k0, L;  // n = 0: nothing to do
+};
+
+template <bool Q8>
+__device__ __forceinline__ Seq read_seq(const SpanAttnArgs &a, int s, unsigned *status)
+{
+    Seq r;
+    r.q0 = __ldg(a.query_start_loc + s);
+    const int q1 = __ldg(a.query_start_loc + s + 1);
+    r.n = q1 - r.q0;
+    unsigned bad = r.q0 < 0 || q1 < r.q0 || q1 > a.total_q_tokens ? NS_DEV_BAD_QUERY_SPAN : 0u;
+    if (Q8) {
+        r.k0 = 0;
+        r.L = __ldg(a.context_lens + s);
+        if (r.L < r.n)
+            bad |= NS_DEV_BAD_QUERY_SPAN;
+        else if ((long long)r.L > (long long)a.max_blocks_per_seq * 16)
+            bad |= NS_DEV_BAD_CONTEXT_LEN;
+    } else {
+        r.k0 = __ldg(a.key_start_loc + s);
+        const int k1 = __ldg(a.key_start_loc + s + 1);
+        r.L = k1 - r.k0;
+        if (r.k0 < 0 || k1 < r.k0 || k1 > a.total_k_tokens)
+            bad |= NS_DEV_BAD_QUERY_SPAN;
+    }
+    if (bad != 0) {
+        if (status != nullptr)
+            raise_status(status, bad);
+        r.n = 0;
+    }
+    return r;
+}
+
+// Cost of the first u units of one kv head of a sequence (u < its units): unit v
+// sees b + (v + 1) R keys.
+__device__ __forceinline__ long long cost_before(long long u, long long each, long long R)
+{
+    return u * each + R * (u * (u + 1) / 2);
+}
+
+// The unit that position x of a kv head's line falls into, of `units`.
+__device__ __forceinline__ int unit_at(long long x, int units, long long each, long long R)
+{
+    // u each + R u (u + 1) / 2 <= x, solved in fp32 and put right
+    const float p = (float)each + 0.5f * (float)R, r = (float)R;
+    const float g = 2.f * (float)x / (p + sqrtf(fmaf(2.f * r, (float)x, p * p)));
+    int u = min(max((int)g, 0), units - 1);
+    while (u > 0 && cost_before(u, each, R) > x)
+        --u;
+    while (u + 1 < units && cost_before(u + 1, each, R) <= x)
+        ++u;
+    return u;
+}
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Key tiles that query tile t of a unit needs (keys up to its last token's own).
+template <int KT>
+__device__ __forceinline__ int tiles_of(const Unit &u, int t, int qt)
+{
+    const int first = u.i0 + t * qt;
+    if (first >= u.n)
+        return 0;
+    const int keys = u.L - u.n + min(u.n, first + qt);
+    return keys > 0 ? ceil_div(keys, KT) : 0;
+}
+
+// ---------------------------------------------------------------------------
+// Helpers
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float pow2(int e)  // 2^e, -126 <= e <= 127
+{
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// A bounded wait of a whole warp: its lanes leave it together, and agree.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+}
+
+// The registers are read behind this point (after a wait for a TMEM load).
+__device__ __forceinline__ void hold32(float *v)
+{
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+    asm volatile("" : "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31]));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Largest magnitude pattern of the eight 16-bit values of w, both halves.
+__device__ __forceinline__ uint32_t top16(uint4 w, uint32_t t)
+{
+    constexpr uint32_t kMag = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(__vmaxu2(w.x & kMag, w.y & kMag), __vmaxu2(w.z & kMag, w.w & kMag)), t);
+}
+
+// bf16 pair -> fp16 pair of the value times f.
+__device__ __forceinline__ uint32_t bf16_to_f16(uint32_t w, float2 f)
+{
+    const float2 x = fmul2(unpack2<BF16>(w), f);
+    return pack2<F16>(x.x, x.y);
+}
+
+__device__ __forceinline__ uint4 bf16_to_f16(uint4 w, float f)
+{
+    const float2 ff = make_float2(f, f);
+    return make_uint4(bf16_to_f16(w.x, ff), bf16_to_f16(w.y, ff), bf16_to_f16(w.z, ff), bf16_to_f16(w.w, ff));
+}
+
+// Four q8_0 codes (a word) -> two fp16 pairs of code * d.  A code plus 128 is the
+// low byte of the fp16 1024 + code + 128; the product rounds once.
+__device__ __forceinline__ uint2 codes_to_f16(uint32_t w, __half2 d)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint2 r;
+    r.x = __byte_perm(u, 0x64646464u, 0x4140);
+    r.y = __byte_perm(u, 0x64646464u, 0x4342);
+    __half2 *h = reinterpret_cast<__half2 *>(&r);
+    h[0] = __hmul2(__hsub2(h[0], off), d);
+    h[1] = __hmul2(__hsub2(h[1], off), d);
+    return r;
+}
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+template <typename T, int D, bool Q8>
+__global__ void __launch_bounds__(kThreads, 1)
+    span_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ Params P)
+{
+    using GG = Geo<D, Q8>;
+    constexpr int KT = GG::KT, REG = GG::REG, ST = GG::STAGES;
+    constexpr bool BF = T::code == NS_BF16;
+    constexpr bool SCALED = Q8 || BF;  // V tiles carry an exponent
+    extern __shared__ unsigned char smem_raw[];
+    Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const SpanAttnArgs &a = P.a;
+    const int qt = P.qt, R = 2 * P.qt;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&sm.k_ready[i], Q8 ? 128 : 1);
+            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.v_ready[i], 128);
+            mbar_init(&sm.k_empty[i], 1);
+            mbar_init(&sm.v_empty[i], 1);
+        }
+        for (int i = 0; i < GG::RAW; ++i) {
+            mbar_init(&sm.raw_full[i], 1);
+            mbar_init(&sm.raw_empty[i], 128);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sm.q_ready[t], kRows);
+            mbar_init(&sm.s_full[t], 1);
+            mbar_init(&sm.s_free[t], kRows);
+            mbar_init(&sm.p_full[t], kRows);
+            mbar_init(&sm.pv_done[t], 1);
+        }
+        for (int i = 0; i < kUnits; ++i) {
+            mbar_init(&sm.u_full[i], 1);
+            mbar_init(&sm.u_empty[i], 15);  // one arrival a warp but this walk's own
+        }
+        mbar_init(&sm.topped, 128);
+        sm.no_unit.t1 = -1;
+        mbar_init_fence();
+    }
+    if (warp == kScoreWarp) {
+        tc::tmem_alloc(&sm.tmem_base, 512);
+        tc::tmem_relinquish();
+    }
+    grid_launch_dependents();  // the joining kernel may be set up; it waits for this grid's end
+
+    // ---- this CTA's run of the line: every thread costs its share of the sequences
+    {
+        const int per = ceil_div(a.num_seqs, kThreads);
+        const int s0 = min(a.num_seqs, (int)threadIdx.x * per), s1 = min(a.num_seqs, s0 + per);
+        auto cost = [&](int s, unsigned *status) -> long long {
+            const Seq q = read_seq<Q8>(a, s, status);
+            if (q.n == 0)
+                return 0;
+            const long long units = ceil_div(q.n, R), each = GG::OVERHEAD + max(q.L - q.n, 0);
+            return (cost_before(units - 1, each, R) + each + q.n) * a.num_kv_heads;
+        };
+        long long mine = 0;
+        for (int s = s0; s < s1; ++s)
+            mine += cost(s, blockIdx.x == 0 ? a.status : nullptr);
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += y;
+        }
+        if (lane == 31)
+            sm.scan[warp] = incl;
+        __syncthreads();
+        long long before = incl - mine, total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const long long x = sm.scan[w];
+            if (w < warp)
+                before += x;
+            total += x;
+        }
+        const int ctas = (int)min((long long)gridDim.x, max(1LL, total / GG::SHARE));
+        const int c = blockIdx.x;
+        const long long x0 = c < ctas ? total * c / ctas : total, x1 = c < ctas ? total * (c + 1) / ctas : total;
+        if (threadIdx.x == 0) {
+            sm.x0 = x0;
+            sm.x1 = x1;
+        }
+        if (x0 < x1 && x0 >= before && x0 < before + mine) {
+            long long x = before;
+            int s = s0;
+            for (;; ++s) {
+                const long long w = cost(s, nullptr);
+                if (x0 < x + w)
+                    break;
+                x += w;
+            }
+            sm.start_s = s;
+            sm.start_x = x;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sm.tmem_base;
+    bool ok = true;
+
+    // The next announced unit (t1 < 0 at the end), in registers, or left in shared
+    // memory until the warp hands it back.
+    int unit_no = 0;
+    auto wait_unit = [&]() -> const Unit & {
+        const int i = unit_no % kUnits;
+        if (!warp_wait(&sm.u_full[i], (uint32_t)(unit_no / kUnits) & 1u)) {
+            ok = false;
+            return sm.no_unit;
+        }
+        ++unit_no;
+        return sm.unit[i];
+    };
+    auto release_unit = [&](int no) {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sm.u_empty[no % kUnits]);
+    };
+    auto next_unit = [&]() -> Unit {
+        const Unit u = wait_unit();
+        if (ok)
+            release_unit(unit_no - 1);
+        return u;
+    };
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        regs_grow<kSoftmaxRegs>();
+        const int t = warp >> 2;                        // query tile
+        const int r = threadIdx.x & (kRows - 1);        // row == TMEM lane
+        const int G = P.group;
+        const int rt = r / G, rg = r - rt * G;          // token and head of the row
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_addr = lane_addr + t * KT, o_addr = lane_addr + GG::O + t * D,
+                       p_addr = lane_addr + GG::P + t * (KT / 2);
+        uint8_t *qs = sm.q[t] + r * kPanel;
+        int count = 0;   // key tiles of this query tile so far
+        int vtile = 0;   // key tiles of the CTA before this unit
+        float row_scale = P.scale_log2;
+
+        // Lay row r of the unit's query tile into shared memory.
+        auto lay_q = [&](const Unit &u) {
+            const int tok = u.i0 + t * qt + rt;
+            const bool on = rt < qt && tok < u.n;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
+                                                               (long long)(u.q0 + tok) * a.q_row_stride +
+                                                               (long long)(u.h * G + rg) * D);
+            uint4 w[D / 8];
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                w[c] = on ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            if (Q8 && BF) {
+                // fp16 for the product with fp16 keys: the row's largest value goes
+                // just below 2^15, its power of two into the score's scale
+                uint32_t m = 0;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    m = top16(w[c], m);
+                const int e = max((int)(max(m & 0xffffu, m >> 16) >> 7), 15);
+                const float f = pow2(141 - e);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    w[c] = bf16_to_f16(w[c], f);
+                row_scale = P.scale_log2 * pow2(max(e - 141, -126));
+            }
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                w[c].x ^= P.q_flip;
+                w[c].y ^= P.q_flip;
+                w[c].z ^= P.q_flip;
+                w[c].w ^= P.q_flip;
+                *reinterpret_cast<uint4 *>(qs + (c >> 3) * (kRows * kPanel) + (((c & 7) ^ (r & 7)) << 4)) = w[c];
+            }
+            fence_async_smem();
+            mbar_arrive(&sm.q_ready[t]);
+        };
+
+        const Unit *up = &wait_unit();
+        if (up->t1 >= 0 && min(up->t1, tiles_of<KT>(*up, t, qt)) > up->t0)
+            lay_q(*up);
+        while (up->t1 >= 0) {
+            const int t0 = up->t0, end = min(up->t1, tiles_of<KT>(*up, t, qt));
+            // last key of the row, of the tile's first row
+            const int low = up->L - up->n + up->i0 + t * qt;
+            const int pos = rt < qt && up->i0 + t * qt + rt < up->n ? low + rt : -1;
+            float m = -INFINITY, l = 0.f;
+            for (int j = t0; ok && j < end; ++j, ++count) {
+                const int stage = (vtile + j - t0) % ST;
+                if (!warp_wait(&sm.s_full[t], (uint32_t)count & 1u)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                float sv[KT];
+#pragma unroll
+                for (int c = 0; c < KT; c += 32)
+                    tc::tmem_ld32(s_addr + c, *reinterpret_cast<float(*)[32]>(&sv[c]));
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < KT; c += 32)
+                    hold32(&sv[c]);
+                tc::fence_before_sync();
+                mbar_arrive(&sm.s_free[t]);
+
+                float sc = row_scale, ev = 0.f;
+                uint32_t loaded = 0xffffffffu;
+                if (SCALED) {
+                    if (!warp_wait(&sm.v_ready[stage], (uint32_t)((vtile + j - t0) / ST) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    ev = sm.ev[stage];
+                    if (Q8) {
+                        sc *= sm.ek[stage];
+                        loaded = sm.loaded[stage];
+                    }
+                }
+                const int base = j * KT;
+                bool masked = base + KT - 1 > low;
+                if (masked) {
+                    const int lim = pos - base;
+#pragma unroll
+                    for (int c = 0; c < KT; ++c)
+                        sv[c] = c <= lim ? sv[c] : -INFINITY;
+                }
+                if (Q8 && (loaded & 0xffu) != 0xffu) {  // blocks that are not in the pool count for nothing
+                    masked = true;
+#pragma unroll
+                    for (int c = 0; c < KT; ++c)
+                        sv[c] = (loaded >> (c / 16)) & 1u ? sv[c] : -INFINITY;
+                }
+                float tm[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+                for (int c = 4; c < KT; c += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        tm[e] = c + 4 + e < KT ? max3(tm[e], sv[c + e], sv[c + 4 + e]) : fmaxf(tm[e], sv[c + e]);
+                const float top = fmaf(fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])), sc, ev);
+                float m_new = m, alpha = 1.f;
+                bool moved = false;
+                if (top > m + kSlack) {
+                    m_new = top;
+                    alpha = fast_exp2(m - top);  // 0 at the first tile
+                    moved = j > t0;
+                    l *= alpha;
+                }
+                m = m_new;
+                const float nm = m > -INFINITY ? ev - m : 0.f;
+
+                // P is free, and O at rest, once the previous tile's value products are done
+                if (count > 0 && !warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                if (__any_sync(0xffffffffu, moved)) {
+                    const float f = moved ? alpha : 1.f;
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        float ov[32];
+                        tc::tmem_ld32(o_addr + c, ov);
+                        tc::tmem_ld_wait();
+                        hold32(ov);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            ov[e] *= f;
+                        tc::tmem_st32(o_addr + c, ov);
+                    }
+                }
+                const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < KT; c += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 z = ffma2(make_float2(sv[c + e], sv[c + e + 1]), sc2, nm2);
+                        float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                        if (masked) {  // a score of -infinity times a scale of 0 is NaN
+                            p.x = sv[c + e] > -INFINITY ? p.x : 0.f;
+                            p.y = sv[c + e + 1] > -INFINITY ? p.y : 0.f;
+                        }
+                        sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], p);
+                        pk[e >> 1] = pack2<F16>(p.x, p.y);
+                    }
+                    tc::tmem_st16(p_addr + c / 2, pk);
+                }
+                const float ts = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                l += SCALED ? ts * fast_exp2(-ev) : ts;
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                mbar_arrive(&sm.p_full[t]);
+            }
+            const Unit &u = *up;
+            vtile += u.t1 - t0;
+
+            // the next unit's Q, so that its first scores are under way during the epilogue
+            const int this_no = unit_no - 1;
+            const Unit *next = &wait_unit();
+            if (next->t1 >= 0 && min(next->t1, tiles_of<KT>(*next, t, qt)) > next->t0)
+                lay_q(*next);
+
+            // ---- epilogue
+            const int tok = u.i0 + t * qt + rt;
+            const bool on = rt < qt && tok < u.n;
+            const bool any = end > t0;
+            if (ok && any && !warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u))
+                ok = false;
+            tc::fence_after_sync();
+            if (u.rec < 0) {
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                uint16_t *out = static_cast<uint16_t *>(a.out) +
+                                ((long long)(u.q0 + tok) * a.num_q_heads + (long long)u.h * G + rg) * D;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float ov[32];
+                    tc::tmem_ld32(o_addr + c, ov);
+                    tc::tmem_ld_wait();
+                    hold32(ov);
+                    if (on && ok) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 w;
+                            uint32_t *ww = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                ww[x] = any && l > 0.f ? pack2<T>(ov[e + 2 * x] * inv, ov[e + 2 * x + 1] * inv) : 0u;
+                            *reinterpret_cast<uint4 *>(out + c + e) = w;
+                        }
+                    }
+                }
+            } else {
+                // a part: unnormalised row, reference and sum, [D / 4][256 rows][4]
+                float *rec = P.records + (size_t)u.rec * record_floats(D);
+                const int row = t * kRows + r;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float ov[32];
+                    tc::tmem_ld32(o_addr + c, ov);
+                    tc::tmem_ld_wait();
+                    hold32(ov);
+                    if (on && any) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(rec + ((size_t)((c + e) >> 2) * (2 * kRows) + row) * 4) =
+                                make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+                    }
+                }
+                if (on) {
+                    rec[(size_t)D * 2 * kRows + row] = any ? m : -INFINITY;
+                    rec[(size_t)(D + 1) * 2 * kRows + row] = any ? l : 0.f;
+                }
+            }
+            tc::fence_before_sync();
+            release_unit(this_no);
+            up = next;
+        }
+        if (!ok)
+            raise_status(a.status, NS_DEV_WAIT_TIMEOUT);
+    } else if (warp < kProducerWarp) {
+        // ------------------------------------------------------------ conversion
+        regs_shrink<kConvertRegs>();
+        const int r = threadIdx.x - kConvertWarp * 32, w4 = warp - kConvertWarp;
+        const int key = r % KT;                      // row of the tile, panel r / KT
+        const int panel = (r / KT) * (KT * kPanel) + key * kPanel;
+        int tile = 0;
+        for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
+            for (int j = u.t0; ok && j < u.t1; ++j, ++tile) {
+                const int stage = tile % ST;
+                const uint32_t par = (uint32_t)(tile / ST) & 1u;
+                const bool live = j * KT + key < u.L;  // a row behind the last key is zero
+                if (!Q8) {
+                    if (!warp_wait(&sm.v_full[stage], par)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *row = sm.v[stage] + panel;
+                    if (BF) {
+                        uint4 x[8];
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            x[c] = live ? lds128(row + ((c ^ (r & 7)) << 4)) : make_uint4(0u, 0u, 0u, 0u);
+                            top = top16(x[c], top);
+                        }
+                        top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+                        if (lane == 0)
+                            sm.top[tile & 1][0][w4] = top;
+                        mbar_arrive(&sm.topped);
+                        if (!warp_wait(&sm.topped, (uint32_t)tile & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t *all = sm.top[tile & 1][0];
+                        top = max(max(all[0], all[1]), max(all[2], all[3]));
+                        const int e = max((int)(top >> 7), 45);
+                        const float f = pow2(141 - e);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<uint4 *>(row + ((c ^ (r & 7)) << 4)) = bf16_to_f16(x[c], f);
+                        if (r == 0)
+                            sm.ev[stage] = (float)(e - 141);
+                        fence_async_smem();
+                    } else if (!live) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<uint4 *>(row + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        fence_async_smem();
+                    }
+                    mbar_arrive(&sm.v_ready[stage]);
+                } else {
+                    const int rs = tile % GG::RAW;
+                    if (!warp_wait(&sm.raw_full[rs], (uint32_t)(tile / GG::RAW) & 1u) ||
+                        !warp_wait(&sm.k_empty[stage], par ^ 1u) || !warp_wait(&sm.v_empty[stage], par ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint8_t *raw = sm.raw[rs];
+                    const uint32_t loaded = sm.raw_loaded[rs];
+                    const bool have = live && ((loaded >> (key / 16)) & 1u);
+                    const uint32_t *scales = reinterpret_cast<const uint32_t *>(raw + 2 * KT * 64);
+                    const uint32_t d[2] = {have ? scales[key] : 0u, have ? scales[KT + key] : 0u};
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t mag = d[x] & 0x7fff7fffu;
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, max(mag & 0xffffu, mag >> 16));
+                        if (lane == 0)
+                            sm.top[tile & 1][x][w4] = top;
+                    }
+                    mbar_arrive(&sm.topped);
+                    if (!warp_wait(&sm.topped, (uint32_t)tile & 1u)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t *all = sm.top[tile & 1][x];
+                        const int e = (int)(max(max(all[0], all[1]), max(all[2], all[3])) >> 10);
+                        if (r == 0) {  // the largest scale goes just below 2^8, its codes below 2^15
+                            if (x == 0) {
+                                sm.ek[stage] = pow2(e - 22);
+                                sm.loaded[stage] = loaded;
+                            } else {
+                                sm.ev[stage] = (float)(e - 22);
+                            }
+                        }
+                        const float2 ds = unpack2<F16>(d[x]);
+                        const float f = pow2(22 - e);
+                        const __half2 lo = __float2half2_rn(ds.x * f), hi = __float2half2_rn(ds.y * f);
+                        const uint8_t *codes = raw + x * KT * 64 + key * 64;
+                        uint8_t *row = (x == 0 ? sm.k[stage] : sm.v[stage]) + panel;
+                        // code chunks in an order in which neither the reads (64-byte rows)
+                        // nor the writes (swizzled 128-byte rows) of eight threads share a bank
+                        const int half = (r >> 1) & 3, turn = (half << 1) ^ ((half >> 1) * 7);
+#pragma unroll
+                        for (int c0 = 0; c0 < 4; ++c0) {
+                            const int c = c0 ^ turn;
+                            const uint4 q = lds128(codes + c * 16);
+                            const __half2 dd = c < 2 ? lo : hi;
+                            const uint2 e0 = codes_to_f16(q.x, dd), e1 = codes_to_f16(q.y, dd),
+                                        e2 = codes_to_f16(q.z, dd), e3 = codes_to_f16(q.w, dd);
+                            *reinterpret_cast<uint4 *>(row + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
+                            *reinterpret_cast<uint4 *>(row + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(e2.x, e2.y, e3.x, e3.y);
+                        }
+                        fence_async_smem();
+                        if (x == 0)
+                            mbar_arrive(&sm.k_ready[stage]);
+                    }
+                    mbar_arrive(&sm.v_ready[stage]);
+                    mbar_arrive(&sm.raw_empty[rs]);
+                }
+            }
+        }
+        if (!ok)
+            raise_status(a.status, NS_DEV_WAIT_TIMEOUT);
+    } else {
+        regs_shrink<kOtherRegs>();
+        if (warp == kProducerWarp) {
+            // ------------------------------------------------------------ producer
+            if (!Q8 && lane == 0) {
+                tc::prefetch_tensormap(&tm_k);
+                tc::prefetch_tensormap(&tm_v);
+            }
+            int tile = 0;
+            for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
+                const int blocks = Q8 ? ceil_div(u.L, 16) : 0;
+                for (int j = u.t0; ok && j < u.t1; ++j, ++tile) {
+                    const int stage = tile % ST;
+                    const uint32_t par = ((uint32_t)(tile / ST) & 1u) ^ 1u;
+                    if (!Q8) {
+                        if (lane == 0) {
+                            const int row = u.k0 + j * KT;
+                            ok = mbar_wait(&sm.k_empty[stage], par);
+                            if (ok) {
+                                mbar_arrive_expect_tx(&sm.k_ready[stage], GG::TILE);
+#pragma unroll
+                                for (int g = 0; g < REG; ++g)
+                                    tc::tma_load_3d(sm.k[stage] + g * KT * kPanel, &tm_k, g * 64, u.h, row,
+                                                    &sm.k_ready[stage]);
+                                ok = mbar_wait(&sm.v_empty[stage], par);
+                            }
+                            if (ok) {
+                                mbar_arrive_expect_tx(&sm.v_full[stage], GG::TILE);
+#pragma unroll
+                                for (int g = 0; g < REG; ++g)
+                                    tc::tma_load_3d(sm.v[stage] + g * KT * kPanel, &tm_v, g * 64, u.h, row,
+                                                    &sm.v_full[stage]);
+                            }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    } else {
+                        // lane i: block i / 4 of the tile, its codes of K, of V, scales of K, of V
+                        const int rs = tile % GG::RAW;
+                        const int b = lane >> 2, what = lane & 3, blk = j * (KT / 16) + b;
+                        int phys = -1;
+                        if (blk < blocks) {
+                            phys = __ldg(a.block_tables + (long long)u.s * a.max_blocks_per_seq + blk);
+                            if (phys < 0 || (long long)phys >= a.num_blocks) {
+                                raise_status(a.status, NS_DEV_BAD_BLOCK_ID);
+                                phys = -1;
+                            }
+                        }
+                        // blocks behind the last key are neither read nor missed
+                        const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0),
+                                       fine = __ballot_sync(0xffffffffu, phys >= 0 || blk >= blocks);
+                        if (lane == 0) {
+                            ok = mbar_wait(&sm.raw_empty[rs], ((uint32_t)(tile / GG::RAW) & 1u) ^ 1u);
+                            if (ok) {
+                                uint32_t mask = 0;
+                                for (int i = 0; i < KT / 16; ++i)
+                                    mask |= ((fine >> (4 * i)) & 1u) << i;
+                                sm.raw_loaded[rs] = mask;
+                                mbar_arrive_expect_tx(&sm.raw_full[rs],
+                                                      (uint32_t)(__popc(have) / 4) * 2u * (16u * 64u + 16u * 4u));
+                            }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                        if (ok && phys >= 0) {
+                            const long long row = ((long long)phys * a.num_kv_heads + u.h) * 16;
+                            uint8_t *raw = sm.raw[rs];
+                            if (what < 2)
+                                bulk_load(raw + what * KT * 64 + b * 1024,
+                                          static_cast<const uint8_t *>(what == 0 ? a.k_codes : a.v_codes) + row * 64, 1024u,
+                                          &sm.raw_full[rs]);
+                            else
+                                bulk_load(raw + 2 * KT * 64 + (what - 2) * KT * 4 + b * 64,
+                                          static_cast<const uint8_t *>(what == 2 ? a.k_scales : a.v_scales) + row * 4, 64u,
+                                          &sm.raw_full[rs]);
+                        }
+                    }
+                }
+            }
+            // Never leave while copies may still land in this CTA's shared memory:
+            // the last tile of every stage has arrived.
+            if (lane == 0) {
+                bool drained = true;
+                const int depth = Q8 ? GG::RAW : ST;
+                for (int i = 1; drained && i <= depth && i <= tile; ++i) {
+                    const int x = tile - i;
+                    if (Q8)
+                        drained = mbar_wait(&sm.raw_full[x % GG::RAW], (uint32_t)(x / GG::RAW) & 1u);
+                    else
+                        drained = mbar_wait(&sm.k_ready[x % ST], (uint32_t)(x / ST) & 1u) &&
+                                  mbar_wait(&sm.v_full[x % ST], (uint32_t)(x / ST) & 1u);
+                }
+                if (!drained || !ok)
+                    raise_status(a.status, NS_DEV_WAIT_TIMEOUT);
+            }
+            __syncwarp();
+        } else if (warp == kScoreWarp || warp == kValueWarp) {
+            // ------------------------------------------------------------ products
+            const bool scores = warp == kScoreWarp;
+            const uint32_t idesc_s = tc::idesc_f16(kRows, KT, BF && !Q8 ? 1 : 0, false);
+            const uint32_t idesc_o = tc::idesc_f16(kRows, 64, 0, true);
+            int tile = 0, units[2] = {0, 0}, count[2] = {0, 0};
+            for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
+                const int end[2] = {min(u.t1, tiles_of<KT>(u, 0, qt)), min(u.t1, tiles_of<KT>(u, 1, qt))};
+                if (lane == 0) {
+                    for (int j = u.t0; ok && j < u.t1; ++j) {
+                        const int stage = (tile + j - u.t0) % ST;
+                        const uint32_t par = (uint32_t)((tile + j - u.t0) / ST) & 1u;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!ok || j >= end[t])
+                                continue;
+                            if (scores) {
+                                // S of tile t, once its previous scores were read
+                                ok = (j > u.t0 || mbar_wait(&sm.q_ready[t], (uint32_t)units[t] & 1u)) &&
+                                     mbar_wait(&sm.k_ready[stage], par) &&
+                                     (count[t] == 0 || mbar_wait(&sm.s_free[t], (uint32_t)(count[t] - 1) & 1u));
+                                if (!ok)
+                                    continue;
+                                tc::fence_after_sync();
+                                const uint32_t qa = smem_addr(sm.q[t]), ka = smem_addr(sm.k[stage]);
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk)
+                                    tc::mma_ss(tmem + t * KT,
+                                               tc::desc_sw128(qa + (kk >> 2) * kRows * kPanel + (kk & 3) * 32),
+                                               tc::desc_sw128(ka + (kk >> 2) * KT * kPanel + (kk & 3) * 32), idesc_s,
+                                               kk > 0 ? 1u : 0u);
+                                tc::mma_commit(&sm.s_full[t]);
+                            } else {
+                                ok = mbar_wait(&sm.p_full[t], (uint32_t)count[t] & 1u) &&
+                                     mbar_wait(&sm.v_ready[stage], par);
+                                if (!ok)
+                                    continue;
+                                tc::fence_after_sync();
+                                const uint32_t va = smem_addr(sm.v[stage]);
+#pragma unroll
+                                for (int kk = 0; kk < KT / 16; ++kk)
+#pragma unroll
+                                    for (int g = 0; g < REG; ++g)
+                                        tc::mma_ts(tmem + GG::O + t * D + g * 64, tmem + GG::P + t * (KT / 2) + kk * 8,
+                                                   tc::desc_sw128(va + g * KT * kPanel + kk * 16 * kPanel), idesc_o,
+                                                   j > u.t0 || kk > 0 ? 1u : 0u);
+                                tc::mma_commit(&sm.pv_done[t]);
+                            }
+                            ++count[t];
+                        }
+                        if (ok)
+                            tc::mma_commit(scores ? &sm.k_empty[stage] : &sm.v_empty[stage]);
+                    }
+                    for (int t = 0; t < 2; ++t)
+                        units[t] += end[t] > u.t0 ? 1 : 0;
+                }
+                tile += u.t1 - u.t0;
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            }
+            if (!ok && lane == 0)
+                raise_status(a.status, NS_DEV_WAIT_TIMEOUT);
+        } else {
+            // ------------------------------------------------------------ the walk
+            const long long x0 = sm.x0, x1 = sm.x1;
+            Header head = {};
+            int no = 0;
+            auto announce = [&](const Unit &u) {
+                const int i = no % kUnits;
+                if (!warp_wait(&sm.u_empty[i], ((uint32_t)(no / kUnits) & 1u) ^ 1u)) {
+                    ok = false;
+                    return;
+                }
+                if (lane == 0) {
+                    sm.unit[i] = u;
+                    mbar_arrive(&sm.u_full[i]);
+                }
+                ++no;
+            };
+            if (x0 < x1) {
+                int s = sm.start_s, h = 0, v = 0;
+                long long xs = sm.start_x;  // of the sequence
+                int held = -1;              // lane i holds sequence held + i
+                Seq mine = {0, 0, 0, 0};
+                bool first = true;
+                for (; ok && s < a.num_seqs; ++s) {
+                    if (held < 0 || s >= held + 32) {
+                        held = s;
+                        if (s + lane < a.num_seqs)
+                            mine = read_seq<Q8>(a, s + lane, nullptr);
+                        else
+                            mine.n = 0;
+                    }
+                    Seq q;
+                    q.q0 = __shfl_sync(0xffffffffu, mine.q0, s - held);
+                    q.n = __shfl_sync(0xffffffffu, mine.n, s - held);
+                    q.k0 = __shfl_sync(0xffffffffu, mine.k0, s - held);
+                    q.L = __shfl_sync(0xffffffffu, mine.L, s - held);
+                    if (q.n == 0)
+                        continue;
+                    if (xs >= x1)
+                        break;
+                    const int units = ceil_div(q.n, R);
+                    const long long each = GG::OVERHEAD + max(q.L - q.n, 0);
+                    const long long per_head = cost_before(units - 1, each, R) + each + q.n;
+                    h = v = 0;
+                    if (first) {
+                        h = (int)((x0 - xs) / per_head);
+                        v = unit_at(x0 - xs - h * per_head, units, each, R);
+                        first = false;
+                    }
+                    for (; ok && h < a.num_kv_heads; ++h, v = 0)
+                        for (; ok && v < units; ++v) {
+                            const long long us = xs + h * per_head + cost_before(v, each, R);
+                            if (us >= x1) {
+                                h = a.num_kv_heads;
+                                break;
+                            }
+                            const long long ue = us + each + (v + 1 < units ? (v + 1) * R : q.n);
+                            Unit u;
+                            u.s = s;
+                            u.h = h;
+                            u.i0 = v * R;
+                            u.n = q.n;
+                            u.L = q.L;
+                            u.q0 = q.q0;
+                            u.k0 = q.k0;
+                            const int keys = q.L - q.n + min(q.n, u.i0 + R);
+                            const int all = keys > 0 ? ceil_div(keys, KT) : 0;
+                            auto cut = [&](long long x) {  // the key tile that position x falls before
+                                const long long d = (x - us - GG::OVERHEAD) / KT;
+                                return (int)min(max(d, 0LL), (long long)all);
+                            };
+                            u.t0 = us >= x0 ? 0 : cut(x0);
+                            u.t1 = ue <= x1 ? all : cut(x1);
+                            if (u.t1 <= u.t0 && !(all == 0 && us >= x0))
+                                continue;
+                            u.rec = -1;
+                            if (u.t0 > 0) {
+                                u.rec = 2 * blockIdx.x;
+                                head.head = 1;
+                                head.ends = u.t1 == all;
+                            } else if (u.t1 < all) {
+                                u.rec = 2 * blockIdx.x + 1;
+                                head.own = 1;
+                                head.row0 = q.q0 + u.i0;
+                                head.tokens = min(R, q.n - u.i0);
+                                head.h = h;
+                            }
+                            announce(u);
+                        }
+                    xs += per_head * a.num_kv_heads;
+                }
+            }
+            Unit stop = {};
+            stop.t1 = -1;
+            if (ok)
+                announce(stop);
+            if (lane == 0) {
+                P.headers[blockIdx.x] = head;
+                if (!ok)
+                    raise_status(a.status, NS_DEV_WAIT_TIMEOUT);
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == kScoreWarp) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of cut units: 32 rows of one unit a block, a warp an eighth of
+// the columns.  Parts come in the order of the keys, so results do not depend on
+// which CTA ended first.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ Params P, int ctas)
+{
+    constexpr int kPer = D / 32;  // float4 columns a thread
+    grid_dependency_wait();
+    const int c = blockIdx.x / 8, row = (blockIdx.x % 8) * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+    const Header hd = P.headers[c];
+    if (!hd.own)
+        return;
+    const int t = row / kRows, r = row % kRows, rt = r / P.group;
+    const int tok = t * P.qt + rt;
+    if (rt >= P.qt || tok >= hd.tokens)
+        return;
+    auto record = [&](int i) { return P.records + (size_t)(i == c ? 2 * c + 1 : 2 * i) * record_floats(D); };
+    // the CTAs behind c up to the unit's last part
+    int last = c;
+    float top = record(c)[(size_t)D * 2 * kRows + row];
+    for (int i = c + 1; i < ctas; ++i) {
+        const Header x = P.headers[i];
+        if (x.head) {
+            last = i;
+            top = fmaxf(top, record(i)[(size_t)D * 2 * kRows + row]);
+            if (x.ends)
+                break;
+        }
+        if (x.own)
+            break;
+    }
+    float4 acc[kPer] = {};
+    float sum = 0.f;
+    for (int i = c; i <= last; ++i) {
+        if (i > c && !P.headers[i].head)
+            continue;
+        const float *rec = record(i);
+        const float l = rec[(size_t)(D + 1) * 2 * kRows + row];
+        if (l <= 0.f)
+            continue;
+        const float f = fast_exp2(rec[(size_t)D * 2 * kRows + row] - top);
+        sum = fmaf(f, l, sum);
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const float4 o = *reinterpret_cast<const float4 *>(rec + ((size_t)(warp * kPer + x) * (2 * kRows) + row) * 4);
+            acc[x].x = fmaf(f, o.x, acc[x].x);
+            acc[x].y = fmaf(f, o.y, acc[x].y);
+            acc[x].z = fmaf(f, o.z, acc[x].z);
+            acc[x].w = fmaf(f, o.w, acc[x].w);
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    uint16_t *out = static_cast<uint16_t *>(P.a.out) +
+                    ((long long)(hd.row0 + tok) * P.a.num_q_heads + (long long)hd.h * P.group + (r - rt * P.group)) * D +
+                    warp * kPer * 4;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x)
+        *reinterpret_cast<uint2 *>(out + 4 * x) =
+            make_uint2(pack2<T>(acc[x].x * inv, acc[x].y * inv), pack2<T>(acc[x].z * inv, acc[x].w * inv));
+}
+
+// ---------------------------------------------------------------------------
+// Launch
+// ---------------------------------------------------------------------------
+template <typename T, int D, bool Q8>
+cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &P, int ctas, cudaStream_t stream)
+{
+    // once for each device: the shared memory, and that the kernel has the registers
+    // that its warpgroups share out (with fewer they would wait for ever)
+    static unsigned long long ready = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !((__atomic_load_n(&ready, __ATOMIC_RELAXED) >> dev) & 1ull)) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, span_attn_kernel<T, D, Q8>);
+        if (e == cudaSuccess && fa.numRegs != kRegs)
+            e = cudaErrorInvalidValue;
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(span_attn_kernel<T, D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)smem_bytes<D, Q8>());
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELAXED);
+    }
+    span_attn_kernel<T, D, Q8><<<ctas, kThreads, smem_bytes<D, Q8>(), stream>>>(tk, tv, P);
+    e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas * 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, span_join_kernel<T, D>, P, ctas);
+}
+
+}  // namespace span
+
+cudaError_t launch_span_d64(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv, const span::Params &P, int ctas,
+                            cudaStream_t stream);
+cudaError_t launch_span_d128(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv, const span::Params &P, int ctas,
+                             cudaStream_t stream);
+cudaError_t launch_span_q8(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv, const span::Params &P, int ctas,
+                           cudaStream_t stream);
+
+}  // namespace ns

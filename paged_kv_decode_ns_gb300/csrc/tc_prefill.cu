@@ -36,7 +36,6 @@
 // product, so undefined (even NaN) pool slots never reach the accumulator.
 #include <algorithm>
 #include <cstddef>
-#include <cudaTypedefs.h>
 
 #include "ns_internal.h"
 #include "tcgen05.cuh"
@@ -672,37 +671,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Host side: tensor maps and launch.
+// Host side: launch.
 // ---------------------------------------------------------------------------
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (fn == nullptr) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
-
-static bool encode(CUtensorMap *map, ns_dtype dt, int rank, const void *base, const cuuint64_t *dims,
-                   const cuuint64_t *strides, const cuuint32_t *box)
-{
-    auto fn = encode_fn();
-    if (fn == nullptr)
-        return false;
-    cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = fn(map, dt == NS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                          (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 bool tc_prefill_supported(int block_size, int group)
 {
     return (block_size == 16 || block_size == 32) && group >= 1 && group <= kMaxGroup;
@@ -764,7 +734,7 @@ cudaError_t launch_tc_prefill(const void *q, const int32_t *query_start_loc, con
         const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_q_heads, (cuuint64_t)total_q_tokens};
         const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)num_q_heads * row_bytes};
         const cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)qt};
-        if (!encode(&tq, dtype, 3, q, dims, strides, box))
+        if (!encode_tensor_map(&tq, dtype, 3, q, dims, strides, box))
             return cudaErrorInvalidValue;
     }
     {
@@ -772,8 +742,8 @@ cudaError_t launch_tc_prefill(const void *q, const int32_t *query_start_loc, con
         const cuuint64_t dims[2] = {(cuuint64_t)head_dim, rows};
         const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
         const cuuint32_t box[2] = {64u, (cuuint32_t)block_size};
-        if (!encode(&tk, dtype, 2, k_pool, dims, strides, box) ||
-            !encode(&tv, dtype, 2, v_pool, dims, strides, box))
+        if (!encode_tensor_map(&tk, dtype, 2, k_pool, dims, strides, box) ||
+            !encode_tensor_map(&tv, dtype, 2, v_pool, dims, strides, box))
             return cudaErrorInvalidValue;
     }
     PrefillParams P;

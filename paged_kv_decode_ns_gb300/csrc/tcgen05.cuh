@@ -9,6 +9,12 @@
 #include "ns_common.cuh"
 
 namespace ns {
+
+// Tensor map of `rank` <= 3 dimensions of 16-bit elements, boxes in 128-byte
+// swizzled panels, out-of-range elements read as zero.
+bool encode_tensor_map(CUtensorMap *map, ns_dtype dt, int rank, const void *base, const cuuint64_t *dims,
+                       const cuuint64_t *strides, const cuuint32_t *box);
+
 namespace tc {
 
 // ---- TMEM allocation (one full warp executes these) ------------------------

@@ -37,8 +37,27 @@ def starts(lens, first=0):
     return np.concatenate([[first], first + np.cumsum(lens)]).astype(np.int32)
 
 
-def compare(got, ref, dtype, what=""):
-    return _gpu.compare(got, ref.numpy(), dtype, what)
+# Relative L2 against the rounded exact value, bf16 outputs over a q8_0 cache.  An
+# error d of an element moves it across a rounding border with probability |d| / ulp,
+# by one ulp, so E (difference)^2 = E|d| ulp.  Three roundings to fp16 (K, V, the
+# weights; each half a step 2^-11, uniform) make d of standard deviation sqrt(3)
+# 2^-11 / sqrt(3) = 4.9e-4 of the element; E|d| <= that; the mean ulp of a bf16 value is
+# 2^-7 / (2 ln 2) = 5.6e-3 of it: sqrt(4.9e-4 * 5.6e-3) = 1.66e-3.  (fp16's ulp is an
+# eighth: 5.9e-4, below the 1e-3 of the other attention tests.)
+REL_Q8_BF16 = 1.66e-3
+
+
+def compare(got, ref, dtype, what="", q8=False):
+    """The tolerance of the other attention tests; `q8`: over a q8_0 cache."""
+    if not (q8 and dtype == wl.BF16):
+        return _gpu.compare(got, ref.numpy(), dtype, what)
+    g, r64 = _gpu.to_f64(got), ref.numpy()
+    r = _gpu.round_to_dtype(r64, dtype)
+    assert np.all(np.isfinite(g)), f"{what}: non-finite output"
+    excess = float(np.max(np.abs(g - r64) - 0.5 * _gpu.ulp(r64, dtype), initial=0.0))
+    rel = float(np.linalg.norm(g - r) / max(np.linalg.norm(r), 1e-30))
+    assert excess <= _gpu.MAX_ABS, f"{what}: max-abs {excess:.3g} beyond the output rounding"
+    assert rel <= REL_Q8_BF16, f"{what}: rel-L2 {rel:.3g}"
 
 
 class Q8Cache:

@@ -77,7 +77,7 @@ def test_prompt_then_drafts_then_read_back(dtype):
                                       SCALE, out, ws)
         ref = torch.cat([_span.attend(q[a:b].cpu(), held[0][s], held[1][s], SCALE)
                          for s, (a, b) in enumerate(zip(qsl, qsl[1:]))])
-        _span.compare(out, ref, dtype, f"drafts {step}")
+        _span.compare(out, ref, dtype, f"drafts {step}", q8=True)
         # the model's head: one row of logits per query row
         head = torch.randn(HQ * D, 1000, generator=g).cuda() * 0.3
         p = torch.softmax(out.float().flatten(1) @ head, -1)

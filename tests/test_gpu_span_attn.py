@@ -7,7 +7,8 @@ of the computation are worth at most this much of it at N(0, 1) inputs: a weight
 p <= 1 rounded to fp16 is off by p 2^-11, so a row by sum p |v| 2^-11 / sum p <=
 4.5 * 2^-11 = 2.2e-3 if every error had one sign, and by 2^-11 / sqrt(3) of its own
 size (2.8e-4) as independent ones; a q8_0 value rounded to fp16 moves a score by
-scale sqrt(64) 2^-11 / sqrt(3) = 2.8e-4 and an output by as much again.
+scale sqrt(64) 2^-11 / sqrt(3) = 2.8e-4 and an output by as much again (_span.py has
+what that makes of bf16 outputs).
 """
 import numpy as np
 import pytest
@@ -181,7 +182,7 @@ class Chunks:
         _gpu.assert_no_device_status()
         end = int(self.qsl[-1])
         assert bool((self.out[end:] == 7.0).all())
-        _span.compare(self.out[:end], self.ref()[:end], self.dtype, what)
+        _span.compare(self.out[:end], self.ref()[:end], self.dtype, what, q8=True)
 
 
 SPANS = [(1, 1), (1, 500), (5, 5), (0, 40), (8, 300), (33, 129), (200, 456), (1, 16), (3, 17), (2, 128), (130, 130)]
