@@ -30,58 +30,88 @@ __device__ __forceinline__ int owner(const int32_t *start, int num_seqs, int t)
     return t < __ldg(start + lo + 1) ? lo : -1;
 }
 
-// One thread moves 16 bytes of K and 16 of V (8 elements); a row of one head
-// is D / 8 threads.
-template <typename T, bool Q8>
-__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a, int chunks_per_row, long long n_chunks)
+// Eight codes (x, y) and their scale (z) -> eight elements: fp16(d) * code is exact
+// in fp32 and rounds once.
+template <typename T>
+__device__ __forceinline__ uint4 dequantise(uint4 w)
 {
-    const long long stride = (long long)gridDim.x * kThreads;
-    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n_chunks; i += stride) {
-        const long long row = i / chunks_per_row;
-        const int chunk = (int)(i % chunks_per_row);
-        const int t = (int)(row / a.num_kv_heads), h = (int)(row % a.num_kv_heads);
+    const float d = __half2float(__ushort_as_half((uint16_t)w.z));
+    auto pair = [&](uint32_t x, int i) {
+        return pack2<T>(d * (float)(int8_t)(x >> (8 * i)), d * (float)(int8_t)(x >> (8 * i + 8)));
+    };
+    return make_uint4(pair(w.x, 0), pair(w.x, 2), pair(w.y, 0), pair(w.y, 2));
+}
+
+// A CTA copies `tokens` packed rows.  Its first threads look their rows up (owner,
+// table entry) once; then a thread moves 16 bytes of K and of V (8 elements) at a
+// time, kBatch of them loaded before the first is stored.  Bound by memory once
+// the rows fill the GPU (a thread that looked its own row up and divided by the
+// heads for every 16 bytes reached 4.1 TB/s from q8_0 and 5.0 TB/s at 16 bits).
+constexpr int kBatch = 4;
+constexpr int kMaxTokens = 256;
+
+template <typename T, bool Q8>
+__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a, int tokens, int row_chunks, int head_chunks)
+{
+    __shared__ long long src[kMaxTokens];  // first pool row of the token (its kv head 0), or -1
+    const int t0 = blockIdx.x * tokens, nt = min(tokens, a.total_tokens - t0);
+    if ((int)threadIdx.x < nt) {
+        const int t = t0 + threadIdx.x;
+        long long row = -1;
         const int s = owner(a.start_loc, a.num_seqs, t);
-        if (s < 0)
-            continue;
-        const int first = __ldg(a.start_loc + s), end = __ldg(a.start_loc + s + 1);
-        const bool lead = t == first && h == 0 && chunk == 0;
-        if (first < 0 || end > a.total_tokens) {
-            if (lead || (t == 0 && h == 0 && chunk == 0))
+        if (s >= 0) {
+            const int first = __ldg(a.start_loc + s), end = __ldg(a.start_loc + s + 1), p = t - first;
+            if (first < 0 || end > a.total_tokens) {
                 raise_status(a.status, NS_DEV_BAD_QUERY_SPAN);
-            continue;
-        }
-        if ((long long)(end - first) > (long long)a.max_blocks_per_seq * a.block_size) {
-            if (lead)
+            } else if ((long long)(end - first) > (long long)a.max_blocks_per_seq * a.block_size) {
                 raise_status(a.status, NS_DEV_BAD_CONTEXT_LEN);
-            continue;
+            } else {
+                const int blk = __ldg(a.block_tables + (long long)s * a.max_blocks_per_seq + p / a.block_size);
+                if (blk < 0 || blk >= a.num_blocks)
+                    raise_status(a.status, NS_DEV_BAD_BLOCK_ID);
+                else
+                    row = (long long)blk * a.num_kv_heads * a.block_size + p % a.block_size;
+            }
         }
-        const int p = t - first;
-        const int blk = __ldg(a.block_tables + (long long)s * a.max_blocks_per_seq + p / a.block_size);
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (h == 0 && chunk == 0)
-                raise_status(a.status, NS_DEV_BAD_BLOCK_ID);
-            continue;
+        src[threadIdx.x] = row;
+    }
+    __syncthreads();
+    const int n = nt * row_chunks;
+    const long long out0 = (long long)t0 * row_chunks;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kThreads * kBatch) {
+        uint4 k[kBatch], v[kBatch];
+        bool on[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kThreads;
+            const int t = i / row_chunks, c = i - t * row_chunks;
+            const int h = c / head_chunks, chunk = c - h * head_chunks;
+            const long long row = i < n ? src[t] : -1;
+            on[b] = row >= 0;
+            if (!on[b])
+                continue;
+            const long long prow = row + (long long)h * a.block_size;
+            if (!Q8) {
+                k[b] = __ldg(static_cast<const uint4 *>(a.k) + prow * head_chunks + chunk);
+                v[b] = __ldg(static_cast<const uint4 *>(a.v) + prow * head_chunks + chunk);
+            } else {
+                const uint2 kc = __ldg(static_cast<const uint2 *>(a.k) + prow * 8 + chunk),
+                            vc = __ldg(static_cast<const uint2 *>(a.v) + prow * 8 + chunk);
+                k[b] = make_uint4(kc.x, kc.y, __ldg(static_cast<const uint16_t *>(a.k_scales) + prow * 2 + (chunk >> 2)), 0u);
+                v[b] = make_uint4(vc.x, vc.y, __ldg(static_cast<const uint16_t *>(a.v_scales) + prow * 2 + (chunk >> 2)), 0u);
+            }
         }
-        const long long prow = ((long long)blk * a.num_kv_heads + h) * a.block_size + p % a.block_size;
-        uint4 *ko = static_cast<uint4 *>(a.k_out) + i, *vo = static_cast<uint4 *>(a.v_out) + i;
-        if (!Q8) {
-            *ko = __ldg(static_cast<const uint4 *>(a.k) + prow * chunks_per_row + chunk);
-            *vo = __ldg(static_cast<const uint4 *>(a.v) + prow * chunks_per_row + chunk);
-        } else {
-            auto values = [&](const void *codes, const void *scales) {
-                const uint2 c = __ldg(static_cast<const uint2 *>(codes) + prow * chunks_per_row + chunk);
-                const float d = __half2float(__ushort_as_half(
-                    __ldg(static_cast<const uint16_t *>(scales) + prow * 2 + (chunk >> 2))));
-                const int8_t *b = reinterpret_cast<const int8_t *>(&c);
-                uint4 w;
-                w.x = pack2<T>(d * (float)b[0], d * (float)b[1]);
-                w.y = pack2<T>(d * (float)b[2], d * (float)b[3]);
-                w.z = pack2<T>(d * (float)b[4], d * (float)b[5]);
-                w.w = pack2<T>(d * (float)b[6], d * (float)b[7]);
-                return w;
-            };
-            *ko = values(a.k, a.k_scales);
-            *vo = values(a.v, a.v_scales);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (!on[b])
+                continue;
+            const long long o = out0 + i0 + b * kThreads;
+            if (Q8) {
+                k[b] = dequantise<T>(k[b]);
+                v[b] = dequantise<T>(v[b]);
+            }
+            static_cast<uint4 *>(a.k_out)[o] = k[b];
+            static_cast<uint4 *>(a.v_out)[o] = v[b];
         }
     }
 }
@@ -90,12 +120,13 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a,
 
 cudaError_t launch_kv_gather(const GatherArgs &a, bool q8, cudaStream_t stream)
 {
-    const int chunks = a.head_dim / 8;
-    const long long n = (long long)a.total_tokens * a.num_kv_heads * chunks;
-    const unsigned grid = (unsigned)std::min<long long>((n + kThreads - 1) / kThreads, 65535);
+    const int head_chunks = a.head_dim / 8, row_chunks = a.num_kv_heads * head_chunks;
+    // a batch for every thread; at least eight rows, so that the look-ups are shared
+    const int tokens = std::min(kMaxTokens, std::max(8, kThreads * kBatch / row_chunks));
+    const unsigned grid = (unsigned)((a.total_tokens + tokens - 1) / tokens);
     auto kern = !q8 ? kv_gather_kernel<F16, false>
                     : a.dtype == NS_BF16 ? kv_gather_kernel<BF16, true> : kv_gather_kernel<F16, true>;
-    kern<<<grid, kThreads, 0, stream>>>(a, chunks, n);
+    kern<<<grid, kThreads, 0, stream>>>(a, tokens, row_chunks, head_chunks);
     return cudaGetLastError();
 }
 

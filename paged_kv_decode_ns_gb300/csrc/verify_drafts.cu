@@ -3,42 +3,185 @@
 // Draft i is accepted when u_i q_i(x_i) < p_i(x_i) (the product of two floats
 // is exact in fp64).  At the first rejection the next token is drawn from
 // w = max(p - q, 0), with no rejection from w = p_n: the smallest v whose
-// cumulative weight exceeds r * sum w.  Sums are fp64.
+// cumulative weight exceeds r * sum w.
+//
+// A cluster of CTAs per sequence: every CTA finds the first rejection itself (a
+// few gathers), then sums its contiguous slice of the one row that matters, a
+// contiguous run per warp.  The run sums go to every CTA of the cluster through
+// distributed shared memory; the CTA that owns the run the goal falls into reads
+// that run again and finds the token.  One pass over one row of p and one of q is
+// all the memory traffic, and bounds a large batch.
+//
+// Precision: neighbouring cumulative weights differ by single probabilities, so
+// fp32 sums would move the drawn token.  fp64 additions (about two a clock on an SM)
+// would cost more than the memory pass (one CTA a sequence with fp64 sums: 798 us
+// for 256 sequences of 151936 tokens); here w is split exactly into a float and its
+// rounding error (w > 0 implies p > q >= 0, so (p - s) - q is exact) and sums are
+// pairs of floats (48 bits).  fp64 joins the few sums that are compared.
 #include "ns_common.cuh"
 #include "ns_internal.h"
+#include "tcgen05.cuh"
 
 namespace ns {
 
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 
-struct Weights {
+// h + l, l the rounding error of h.
+struct Pair {
+    float h, l;
+    __device__ __forceinline__ double value() const { return (double)h + (double)l; }
+};
+
+// The weight of a token, exactly max(p - q, 0).  NaN counts as 0.
+__device__ __forceinline__ Pair weight(float p, float q)
+{
+    Pair w;
+    w.h = p - q;
+    w.l = (p - w.h) - q;
+    if (!(w.h > 0.f))
+        w.h = w.l = 0.f;
+    return w;
+}
+
+// The two heads are added without error; what is small stays in l.
+__device__ __forceinline__ Pair operator+(Pair a, Pair b)
+{
+    const float t = a.h + b.h, x = t - a.h;
+    return {t, ((a.h - (t - x)) + (b.h - x)) + (a.l + b.l)};
+}
+
+__device__ __forceinline__ Pair shfl_xor(Pair a, int o)
+{
+    return {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
+}
+
+struct Row {
     const float *p, *q;  // q: nullptr when only p counts
     int skip;            // token of weight 0 (certain draft), or -1
-    __device__ __forceinline__ double operator()(int v) const
+    __device__ __forceinline__ Pair at(int v) const
     {
-        const float a = __ldg(p + v);
-        double w = a;
-        if (q != nullptr)
-            w -= (double)__ldg(q + v);
-        return (w > 0.0 && v != skip) ? w : 0.0;
+        return weight(v == skip ? 0.f : __ldg(p + v), q != nullptr ? __ldg(q + v) : 0.f);
     }
 };
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a)
+// This thread's share of [lo, hi): elements 4 lane + 128 i .. + 3 when the rows are
+// 16-byte aligned at lo, lane + 32 i otherwise.
+template <bool Q>
+__device__ Pair slice_sum(const Row &r, int lo, int hi, int lane, bool aligned)
 {
-    __shared__ int sh_state;      // 0: go on, 1: skip the sequence
+    Pair sum[4] = {};
+    int v = lo;
+    if (aligned) {
+        for (; v + 256 <= hi; v += 256) {
+            float4 p[2], q[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                p[i] = __ldg(reinterpret_cast<const float4 *>(r.p + v + i * 128) + lane);
+                q[i] = Q ? __ldg(reinterpret_cast<const float4 *>(r.q + v + i * 128) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float pv[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
+                const float qv[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (!Q && v + i * 128 + 4 * lane + e == r.skip)
+                        pv[e] = 0.f;
+                    sum[e] = sum[e] + weight(pv[e], qv[e]);
+                }
+            }
+        }
+    } else {
+        for (; v + 256 <= hi; v += 256) {
+            float p[8], q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i] = __ldg(r.p + v + i * 32 + lane);
+                q[i] = Q ? __ldg(r.q + v + i * 32 + lane) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (!Q && v + i * 32 + lane == r.skip)
+                    p[i] = 0.f;
+                sum[i & 3] = sum[i & 3] + weight(p[i], q[i]);
+            }
+        }
+    }
+    for (v += lane; v < hi; v += 32)
+        sum[0] = sum[0] + r.at(v);
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+__device__ __forceinline__ void st_cluster_pair(uint32_t addr, Pair a)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a.h), "f"(a.l) : "memory");
+}
+
+// One warp: the first of `count` <= 256 weights, in order, whose cumulative sum
+// exceeds goal; -1 when none does.  before: what came before the first, then before
+// the one found.
+struct Place {
+    int at;
+    double before, total;
+};
+template <class Goal>
+__device__ Place find(const Pair *w, int count, int lane, double before, Goal goal)
+{
+    const int each = (count + 31) / 32, i0 = lane * each;
+    double x[8], mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = i < each && i0 + i < count ? w[i0 + i].value() : 0.0;
+        if (i < each)
+            mine += x[i];
+    }
+    double incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += y;
+    }
+    Place r;
+    r.total = __shfl_sync(0xffffffffu, incl, 31);
+    const double g = goal(r.total);
+    double c = before + (incl - mine);
+    int at = -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < each && at < 0) {
+            if (x[i] > 0.0 && c + x[i] > g)
+                at = i0 + i;
+            else
+                c += x[i];
+        }
+    const unsigned who = __ballot_sync(0xffffffffu, at >= 0);
+    const int src = who != 0 ? __ffs(who) - 1 : 0;
+    r.at = who != 0 ? __shfl_sync(0xffffffffu, at, src) : -1;
+    r.before = __shfl_sync(0xffffffffu, c, src);
+    return r;
+}
+
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a, int cluster)
+{
+    __shared__ int sh_state;  // 0: go on, 1: skip the sequence
     __shared__ int sh_accepted;
-    __shared__ double sh_sum[kWarps];
-    __shared__ int sh_last[kWarps];
-    const int s = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ __align__(8) Pair sh_run[2][kMaxCluster * kWarps];  // run sums of the cluster, in order (one set a pass)
+    __shared__ Pair sh_part[kWarps];
+    __shared__ Place sh_place;
+    __shared__ double sh_goal;
+    __shared__ int sh_last;
+    const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = __ldg(a.start + s), end = __ldg(a.start + s + 1);
     const int n = end - first;
     if (first < 0 || end < first || end > a.total_drafts) {
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0 && rank == 0)
             raise_status(a.status, NS_DEV_BAD_QUERY_SPAN);
-        return;
+        return;  // the whole cluster
     }
     int32_t *out = a.out_tokens + first + s;
     if (warp == 0) {
@@ -61,102 +204,148 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a)
             if (no != 0 && accepted == n)
                 accepted = i0 + __ffs(no) - 1;
         }
-        for (int i = lane; i <= n; i += 32)
-            out[i] = !bad && i < accepted ? __ldg(a.tokens + first + i) : -1;
+        if (rank == 0)  // the place of the drawn token is left to the CTA that finds it
+            for (int i = lane; i <= n; i += 32)
+                if (bad || i != accepted)
+                    out[i] = !bad && i < accepted ? __ldg(a.tokens + first + i) : -1;
         if (lane == 0) {
             sh_state = bad ? 1 : 0;
             sh_accepted = accepted;
-            a.num_accepted[s] = bad ? -1 : accepted;
-            if (bad)
-                raise_status(a.status, NS_DEV_BAD_TOKEN);
+            sh_last = -1;
+            if (rank == 0) {
+                a.num_accepted[s] = bad ? -1 : accepted;
+                if (bad)
+                    raise_status(a.status, NS_DEV_BAD_TOKEN);
+            }
         }
     }
     __syncthreads();
     if (sh_state != 0)
-        return;
+        return;  // the whole cluster
+    // every CTA of the cluster has started before another one writes to it
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int acc = sh_accepted;
     const bool refused = acc < n;
-    Weights w;
-    w.p = a.target + (long long)(first + s + acc) * a.target_stride;
-    w.q = refused && a.draft ? a.draft + (long long)(first + acc) * a.draft_stride : nullptr;
-    w.skip = refused && !a.draft ? __ldg(a.tokens + first + acc) : -1;
+    Row r;
+    r.p = a.target + (long long)(first + s + acc) * a.target_stride;
+    r.q = refused && a.draft ? a.draft + (long long)(first + acc) * a.draft_stride : nullptr;
+    r.skip = refused && !a.draft ? __ldg(a.tokens + first + acc) : -1;
+    const double u = __ldg(a.sample_u + s);
 
-    // each warp owns a contiguous run of the vocabulary
-    const int per = (a.vocab + kWarps - 1) / kWarps;
-    const int lo = min(a.vocab, warp * per), hi = min(a.vocab, lo + per);
-    double total = 0.0;
+    // contiguous runs, one for each warp of the cluster, of whole 128-byte lines
+    const int runs = cluster * kWarps;
+    const int per = ((a.vocab + runs - 1) / runs + 31) / 32 * 32;
+    const int mine = rank * kWarps + warp;
+    const int lo = (int)min((long long)a.vocab, (long long)mine * per), hi = (int)min((long long)a.vocab, (long long)lo + per);
     for (int pass = 0; pass < 2; ++pass) {
-        double sum = 0.0;
-        int last = -1;  // the last token with a positive weight
-        for (int v = lo + lane; v < hi; v += 32) {
-            const double x = w(v);
-            sum += x;
-            last = x > 0.0 ? v : last;
-        }
+        const bool aligned = ((reinterpret_cast<uintptr_t>(r.p) | reinterpret_cast<uintptr_t>(r.q)) & 15u) == 0;
+        Pair sum = r.q != nullptr ? slice_sum<true>(r, lo, hi, lane, aligned) : slice_sum<false>(r, lo, hi, lane, aligned);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
-        }
-        if (lane == 0) {
-            sh_sum[warp] = sum;
-            sh_last[warp] = last;
+        for (int o = 16; o; o >>= 1)
+            sum = sum + shfl_xor(sum, o);
+        if (pass == 0)
+            asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if (lane < cluster)
+            st_cluster_pair(tc::map_to_rank(&sh_run[pass][mine], lane), sum);
+        tc::cluster_sync();
+        if (warp == 0) {
+            const Place at = find(sh_run[pass], runs, lane, 0.0, [&](double total) { return u * total; });
+            if (lane == 0) {
+                sh_place = at;
+                sh_goal = u * at.total;
+            }
         }
         __syncthreads();
-        total = 0.0;
-        for (int i = 0; i < kWarps; ++i)
-            total += sh_sum[i];
-        if (total > 0.0 || (w.q == nullptr && w.skip < 0))
+        if (sh_place.total > 0.0 || (r.q == nullptr && r.skip < 0))
             break;
-        w.q = nullptr;  // nothing is left of p after the draft's distribution: draw from p
-        w.skip = -1;
+        r.q = nullptr;  // nothing is left of p after the draft's distribution: draw from p
+        r.skip = -1;
         __syncthreads();
     }
-    const double goal = (double)__ldg(a.sample_u + s) * total;
-    double before = 0.0;  // weight of the warps before this one
-    int mine = -1, lastv = -1;
-    for (int i = 0; i < kWarps; ++i) {
-        if (mine < 0 && before + sh_sum[i] > goal)
-            mine = i;
-        if (mine < 0)
-            before += sh_sum[i];
-        lastv = max(lastv, sh_last[i]);
-    }
-    if (mine < 0) {  // no cumulative weight exceeds the goal: no positive weight at all
-        if (threadIdx.x == 0)
-            out[acc] = lastv;
+    const int run = sh_place.at;
+    if (run < 0) {  // no positive weight at all
+        if (threadIdx.x == 0 && rank == 0)
+            out[acc] = -1;
         return;
     }
-    if (warp != mine)
+    if (run / kWarps != rank)
         return;
-    for (int v0 = lo; v0 < hi; v0 += 32) {
-        const double x = v0 + lane < hi ? w(v0 + lane) : 0.0;
-        double cum = x;
+    // ---- the run's owner: a warp a stretch of it, then the warp that the goal falls to
+    const double before = sh_place.before, goal = sh_goal;
+    const int r0 = (int)min((long long)a.vocab, (long long)run * per), r1 = (int)min((long long)a.vocab, (long long)r0 + per);
+    const int each = (per + kWarps - 1) / kWarps;
+    const int v0 = min(r1, r0 + warp * each), v1 = min(r1, v0 + each);
+    Pair sum = {0.f, 0.f};
+    int lastv = -1;
+    for (int v = v0 + lane; v < v1; v += 32) {
+        const Pair w = r.at(v);
+        sum = sum + w;
+        lastv = w.h > 0.f ? v : lastv;
+    }
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, cum, o);
-            if (lane >= o)
-                cum += y;
-        }
-        const unsigned over = __ballot_sync(0xffffffffu, x > 0.0 && before + cum > goal);
-        if (over != 0) {
-            if (lane == 0)
-                out[acc] = v0 + __ffs(over) - 1;
-            return;
-        }
-        before += __shfl_sync(0xffffffffu, cum, 31);
+    for (int o = 16; o; o >>= 1) {
+        sum = sum + shfl_xor(sum, o);
+        lastv = max(lastv, __shfl_xor_sync(0xffffffffu, lastv, o));
     }
-    // the run's sum in this order fell short of the goal by its rounding
+    if (lane == 0) {
+        sh_part[warp] = sum;
+        if (lastv >= 0)
+            atomicMax(&sh_last, lastv);
+    }
+    __syncthreads();
+    if (warp != 0)
+        return;
+    const Place part = find(sh_part, kWarps, lane, before, [&](double) { return goal; });
+    int token = sh_last;  // the run's sum in this order may fall short of the goal by its rounding
+    if (part.at >= 0) {
+        double c = part.before;
+        const int e0 = min(r1, r0 + part.at * each), e1 = min(r1, e0 + each);
+        int lastp = -1;
+        bool found = false;
+        for (int v = e0; v < e1 && !found; v += 32) {
+            const double x = v + lane < e1 ? r.at(v + lane).value() : 0.0;
+            double incl = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += y;
+            }
+            const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
+            const unsigned over = __ballot_sync(0xffffffffu, x > 0.0 && c + incl > goal);
+            if (some != 0)
+                lastp = v + 31 - __clz(some);
+            if (over != 0) {
+                token = v + __ffs(over) - 1;
+                found = true;
+            }
+            c += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (!found && lastp >= 0)
+            token = lastp;
+    }
     if (lane == 0)
-        out[acc] = sh_last[mine];
+        out[acc] = token;
 }
 
 }  // namespace
 
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t stream)
 {
-    verify_kernel<<<a.num_seqs, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    int cluster = kMaxCluster;
+    while (cluster > 1 && (long long)a.num_seqs * cluster > 1216)
+        cluster /= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.num_seqs * cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, verify_kernel, a, cluster);
 }
 
 }  // namespace ns
