@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool SCALED = Q8 || BF;  // V tiles carry an exponent
     extern __shared__ unsigned char smem_raw[];
     Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const SpanAttnArgs &a = P.a;
     const int qt = P.qt, R = 2 * P.qt;
 
@@ -520,6 +520,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = m_new;
                 const float nm = m > -INFINITY ? ev - m : 0.f;
 
+                const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t pk[KT / 2];
+#pragma unroll
+                for (int c = 0; c < KT; c += 2) {
+                    const float2 z = ffma2(make_float2(sv[c], sv[c + 1]), sc2, nm2);
+                    float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                    if (masked) {  // a score of -infinity times a scale of 0 is NaN
+                        p.x = sv[c] > -INFINITY ? p.x : 0.f;
+                        p.y = sv[c + 1] > -INFINITY ? p.y : 0.f;
+                    }
+                    sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], p);
+                    pk[c >> 1] = pack2<F16>(p.x, p.y);
+                }
+                const float ts = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                l += SCALED ? ts * fast_exp2(-ev) : ts;
+
                 // P is free, and O at rest, once the previous tile's value products are done
                 if (count > 0 && !warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u)) {
                     ok = false;
@@ -540,26 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::tmem_st32(o_addr + c, ov);
                     }
                 }
-                const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < KT; c += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 z = ffma2(make_float2(sv[c + e], sv[c + e + 1]), sc2, nm2);
-                        float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-                        if (masked) {  // a score of -infinity times a scale of 0 is NaN
-                            p.x = sv[c + e] > -INFINITY ? p.x : 0.f;
-                            p.y = sv[c + e + 1] > -INFINITY ? p.y : 0.f;
-                        }
-                        sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], p);
-                        pk[e >> 1] = pack2<F16>(p.x, p.y);
-                    }
-                    tc::tmem_st16(p_addr + c / 2, pk);
-                }
-                const float ts = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                l += SCALED ? ts * fast_exp2(-ev) : ts;
+                for (int c = 0; c < KT / 2; c += 32)
+                    tc::tmem_st32(p_addr + c, *reinterpret_cast<const uint32_t(*)[32]>(&pk[c]));
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
                 mbar_arrive(&sm.p_full[t]);
@@ -842,62 +842,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (warp == kScoreWarp || warp == kValueWarp) {
             // ------------------------------------------------------------ products
+            // the whole warp walks the tiles; operands are warp-uniform
             const bool scores = warp == kScoreWarp;
             const uint32_t idesc_s = tc::idesc_f16(kRows, KT, BF && !Q8 ? 1 : 0, false);
-            const uint32_t idesc_o = tc::idesc_f16(kRows, 64, 0, true);
-            int tile = 0, units[2] = {0, 0}, count[2] = {0, 0};
+            const uint32_t idesc_o = tc::idesc_f16(kRows, D, 0, true);
+            const uint64_t d0 = scores ? tc::desc_sw128(0) : tc::desc_sw128_panels(0, KT * kPanel);
+            const uint32_t d_lo = (uint32_t)d0, d_hi = (uint32_t)(d0 >> 32);
+            auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+            const uint32_t tm = uniform(tmem), q_lo = uniform(d_lo + (smem_addr(sm.q[0]) >> 4)),
+                           kv_lo = uniform(d_lo + (smem_addr(scores ? sm.k[0] : sm.v[0]) >> 4));
+            uint32_t stage = 0, par = 0, units[2] = {0, 0}, count[2] = {0, 0};
             for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
                 const int end[2] = {min(u.t1, tiles_of<KT>(u, 0, qt)), min(u.t1, tiles_of<KT>(u, 1, qt))};
-                if (lane == 0) {
-                    for (int j = u.t0; ok && j < u.t1; ++j) {
-                        const int stage = (tile + j - u.t0) % ST;
-                        const uint32_t par = (uint32_t)((tile + j - u.t0) / ST) & 1u;
+                for (int j = u.t0; ok && j < u.t1; ++j) {
+                    const uint32_t b_lo = uniform(kv_lo + stage * (GG::TILE >> 4));
+                    const bool more = uniform(j > u.t0 ? 1u : 0u) != 0;
+                    ok = warp_wait(scores ? &sm.k_ready[stage] : &sm.v_ready[stage], par);
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (!ok || j >= end[t])
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok || j >= end[t])
+                            continue;
+                        if (scores) {
+                            // S of tile t, once its previous scores were read
+                            ok = (j > u.t0 || warp_wait(&sm.q_ready[t], units[t] & 1u)) &&
+                                 (count[t] == 0 || warp_wait(&sm.s_free[t], (count[t] - 1) & 1u));
+                            if (!ok)
                                 continue;
-                            if (scores) {
-                                // S of tile t, once its previous scores were read
-                                ok = (j > u.t0 || mbar_wait(&sm.q_ready[t], (uint32_t)units[t] & 1u)) &&
-                                     mbar_wait(&sm.k_ready[stage], par) &&
-                                     (count[t] == 0 || mbar_wait(&sm.s_free[t], (uint32_t)(count[t] - 1) & 1u));
-                                if (!ok)
-                                    continue;
-                                tc::fence_after_sync();
-                                const uint32_t qa = smem_addr(sm.q[t]), ka = smem_addr(sm.k[stage]);
+                            tc::fence_after_sync();
 #pragma unroll
-                                for (int kk = 0; kk < D / 16; ++kk)
-                                    tc::mma_ss(tmem + t * KT,
-                                               tc::desc_sw128(qa + (kk >> 2) * kRows * kPanel + (kk & 3) * 32),
-                                               tc::desc_sw128(ka + (kk >> 2) * KT * kPanel + (kk & 3) * 32), idesc_s,
-                                               kk > 0 ? 1u : 0u);
-                                tc::mma_commit(&sm.s_full[t]);
-                            } else {
-                                ok = mbar_wait(&sm.p_full[t], (uint32_t)count[t] & 1u) &&
-                                     mbar_wait(&sm.v_ready[stage], par);
-                                if (!ok)
-                                    continue;
-                                tc::fence_after_sync();
-                                const uint32_t va = smem_addr(sm.v[stage]);
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                tc::mma_ss_warp(tm + t * KT,
+                                                q_lo + ((t * (REG * kRows * kPanel) + (kk >> 2) * (kRows * kPanel) + (kk & 3) * 32) >> 4),
+                                                b_lo + (((kk >> 2) * (KT * kPanel) + (kk & 3) * 32) >> 4), d_hi, idesc_s,
+                                                kk > 0);
+                            tc::mma_commit_warp(&sm.s_full[t]);
+                        } else {
+                            ok = warp_wait(&sm.p_full[t], count[t] & 1u);
+                            if (!ok)
+                                continue;
+                            tc::fence_after_sync();
 #pragma unroll
-                                for (int kk = 0; kk < KT / 16; ++kk)
-#pragma unroll
-                                    for (int g = 0; g < REG; ++g)
-                                        tc::mma_ts(tmem + GG::O + t * D + g * 64, tmem + GG::P + t * (KT / 2) + kk * 8,
-                                                   tc::desc_sw128(va + g * KT * kPanel + kk * 16 * kPanel), idesc_o,
-                                                   j > u.t0 || kk > 0 ? 1u : 0u);
-                                tc::mma_commit(&sm.pv_done[t]);
-                            }
-                            ++count[t];
+                            for (int kk = 0; kk < KT / 16; ++kk)
+                                tc::mma_ts_warp(tm + GG::O + t * D, tm + GG::P + t * (KT / 2) + kk * 8,
+                                                b_lo + ((kk * 16 * kPanel) >> 4), d_hi, idesc_o, kk > 0 || more);
+                            tc::mma_commit_warp(&sm.pv_done[t]);
                         }
-                        if (ok)
-                            tc::mma_commit(scores ? &sm.k_empty[stage] : &sm.v_empty[stage]);
+                        ++count[t];
                     }
-                    for (int t = 0; t < 2; ++t)
-                        units[t] += end[t] > u.t0 ? 1 : 0;
+                    if (ok)
+                        tc::mma_commit_warp(scores ? &sm.k_empty[stage] : &sm.v_empty[stage]);
+                    if (++stage == ST) {
+                        stage = 0;
+                        par ^= 1u;
+                    }
                 }
-                tile += u.t1 - u.t0;
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                for (int t = 0; t < 2; ++t)
+                    units[t] += end[t] > u.t0 ? 1 : 0;
             }
             if (!ok && lane == 0)
                 raise_status(a.status, NS_DEV_WAIT_TIMEOUT);

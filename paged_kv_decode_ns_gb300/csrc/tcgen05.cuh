@@ -70,6 +70,13 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr)
     return d;
 }
 
+// The same for an MN-major tile of several 64-wide panels: the next panel along
+// the MN dimension sits `panel` bytes further (the leading offset).
+__device__ __forceinline__ uint64_t desc_sw128_panels(uint32_t saddr, uint32_t panel)
+{
+    return (desc_sw128(saddr) & ~((uint64_t)0x3FFFu << 16)) | (uint64_t)((panel >> 4) & 0x3FFFu) << 16;
+}
+
 // Instruction descriptor, kind::f16: D fp32, A and B fp16 (fmt 0) or bf16
 // (fmt 1), A K-major, B K-major or MN-major, shape M x N (K = 16).
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int ab_fmt, bool b_mn_major)
@@ -104,6 +111,41 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The same three issued by a whole converged warp, through one elected lane (always
+// the same one).  With warp-uniform operands this keeps the tensor pipe busy: a
+// lane that branches off to issue on its own spends 70 to 95 clocks on moving each
+// product's descriptors to uniform registers, against 32 to 64 for the product.
+// Descriptors are given as (low word, high word).
+__device__ __forceinline__ void mma_ss_warp(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                            bool accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n"
+        " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+                                            uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+        " elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_warp(uint64_t *bar)
+{
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar))
         : "memory");
 }
 
