@@ -24,7 +24,7 @@ cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream
     P.a = a;
     P.group = a.num_q_heads / a.num_kv_heads;
     P.qt = span::kRows / P.group;
-    P.scale_log2 = std::fabs(a.scale) * 1.4426950408889634f;
+    P.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, span::kTinyScale);
     P.q_flip = a.scale < 0.f ? 0x80008000u : 0u;
     P.headers = static_cast<span::Header *>(a.workspace);
     P.records = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + span::header_bytes());

@@ -54,6 +54,7 @@ constexpr int kConvertWarp = 8, kProducerWarp = 12, kScoreWarp = 13, kValueWarp 
 constexpr int kPanel = 128;      // bytes of a row of a panel: 64 elements, one swizzle span
 constexpr int kUnits = 4;        // units announced ahead
 constexpr int kMaxCtas = 160;    // grid, at most: the workspace has two records for each
+constexpr float kTinyScale = 1.17549435e-38f;  // a score of -infinity times a scale of 0 would be NaN
 constexpr float kSlack = 8.0f;   // the reference moves when a score passes it by more (log2 units)
 
 template <int D, bool Q8>
@@ -484,20 +485,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ev = sm.ev[stage];
                     if (Q8) {
-                        sc *= sm.ek[stage];
+                        sc = fmaxf(sc * sm.ek[stage], kTinyScale);
                         loaded = sm.loaded[stage];
                     }
                 }
                 const int base = j * KT;
-                bool masked = base + KT - 1 > low;
-                if (masked) {
+                if (base + KT - 1 > low) {
                     const int lim = pos - base;
 #pragma unroll
                     for (int c = 0; c < KT; ++c)
                         sv[c] = c <= lim ? sv[c] : -INFINITY;
                 }
                 if (Q8 && (loaded & 0xffu) != 0xffu) {  // blocks that are not in the pool count for nothing
-                    masked = true;
 #pragma unroll
                     for (int c = 0; c < KT; ++c)
                         sv[c] = (loaded >> (c / 16)) & 1u ? sv[c] : -INFINITY;
@@ -526,11 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < KT; c += 2) {
                     const float2 z = ffma2(make_float2(sv[c], sv[c + 1]), sc2, nm2);
-                    float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-                    if (masked) {  // a score of -infinity times a scale of 0 is NaN
-                        p.x = sv[c] > -INFINITY ? p.x : 0.f;
-                        p.y = sv[c + 1] > -INFINITY ? p.y : 0.f;
-                    }
+                    const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
                     sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], p);
                     pk[c >> 1] = pack2<F16>(p.x, p.y);
                 }
