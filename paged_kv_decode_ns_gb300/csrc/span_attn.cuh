@@ -21,7 +21,7 @@
 //             (fp16) back to TMEM;
 //   8-11      conversion: K and V tiles into the form that the products take;
 //   12        producer: TMA copies of K and V tiles;
-//   13, 14    issue S = Q K^T and O += P V;
+//   13, 14    issue S = Q K^T and O += P V of query tile 0 and 1;
 //   15        walks the CTA's run of units.
 // The two tiles' softmax and products alternate by themselves: while one tile's
 // scores are exponentiated, the other's products run.
@@ -50,7 +50,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRegs = 128;       // registers a thread at launch; the warpgroups then share them out:
 constexpr int kSoftmaxRegs = 200, kConvertRegs = 64, kOtherRegs = 48;
 static_assert(2 * kSoftmaxRegs + kConvertRegs + kOtherRegs <= 4 * kRegs, "the shares fit the launch's registers");
-constexpr int kConvertWarp = 8, kProducerWarp = 12, kScoreWarp = 13, kValueWarp = 14, kPlanWarp = 15;
+constexpr int kTileWarps = 4;    // softmax warps of a query tile
+constexpr int kConvertWarp = 8, kProducerWarp = 12, kProductWarp = 13;  // 13, 14: query tiles 0, 1
 constexpr int kPanel = 128;      // bytes of a row of a panel: 64 elements, one swizzle span
 constexpr int kUnits = 4;        // units announced ahead
 constexpr int kMaxCtas = 160;    // grid, at most: the workspace has two records for each
@@ -287,29 +288,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.k_ready[i], Q8 ? 128 : 1);
             mbar_init(&sm.v_full[i], 1);
             mbar_init(&sm.v_ready[i], 128);
-            mbar_init(&sm.k_empty[i], 1);
-            mbar_init(&sm.v_empty[i], 1);
+            mbar_init(&sm.k_empty[i], 2);  // both tiles' products
+            mbar_init(&sm.v_empty[i], 2);
         }
         for (int i = 0; i < GG::RAW; ++i) {
             mbar_init(&sm.raw_full[i], 1);
             mbar_init(&sm.raw_empty[i], 128);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&sm.q_ready[t], kRows);
+            mbar_init(&sm.q_ready[t], kTileWarps);
             mbar_init(&sm.s_full[t], 1);
-            mbar_init(&sm.s_free[t], kRows);
-            mbar_init(&sm.p_full[t], kRows);
+            mbar_init(&sm.s_free[t], kTileWarps);
+            mbar_init(&sm.p_full[t], kTileWarps);
             mbar_init(&sm.pv_done[t], 1);
         }
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&sm.u_full[i], 1);
-            mbar_init(&sm.u_empty[i], 15);  // one arrival a warp but this walk's own
+            mbar_init(&sm.u_empty[i], kWarps - 1);  // one arrival a warp, but the walk's
         }
         mbar_init(&sm.topped, 128);
         sm.no_unit.t1 = -1;
         mbar_init_fence();
     }
-    if (warp == kScoreWarp) {
+    if (warp == kProductWarp) {
         tc::tmem_alloc(&sm.tmem_base, 512);
         tc::tmem_relinquish();
     }
@@ -411,6 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int count = 0;   // key tiles of this query tile so far
         int vtile = 0;   // key tiles of the CTA before this unit
         float row_scale = P.scale_log2;
+        auto arrive = [&](uint64_t *bar) {  // one arrival for the warp's work so far
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar);
+        };
 
         // Lay row r of the unit's query tile into shared memory.
         auto lay_q = [&](const Unit &u) {
@@ -446,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4 *>(qs + (c >> 3) * (kRows * kPanel) + (((c & 7) ^ (r & 7)) << 4)) = w[c];
             }
             fence_async_smem();
-            mbar_arrive(&sm.q_ready[t]);
+            arrive(&sm.q_ready[t]);
         };
 
         const Unit *up = &wait_unit();
@@ -457,12 +463,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             // last key of the row, of the tile's first row
             const int low = up->L - up->n + up->i0 + t * qt;
             const int pos = rt < qt && up->i0 + t * qt + rt < up->n ? low + rt : -1;
+            // rows are independent: 32 rows without a token need no weights
+            const bool busy = __any_sync(0xffffffffu, pos >= 0 || (rt < qt && up->i0 + t * qt + rt < up->n));
             float m = -INFINITY, l = 0.f;
             for (int j = t0; ok && j < end; ++j, ++count) {
                 const int stage = (vtile + j - t0) % ST;
                 if (!warp_wait(&sm.s_full[t], (uint32_t)count & 1u)) {
                     ok = false;
                     break;
+                }
+                if (!busy) {
+                    arrive(&sm.s_free[t]);
+                    if (count > 0 && !warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    arrive(&sm.p_full[t]);
+                    continue;
                 }
                 tc::fence_after_sync();
                 float sv[KT];
@@ -474,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < KT; c += 32)
                     hold32(&sv[c]);
                 tc::fence_before_sync();
-                mbar_arrive(&sm.s_free[t]);
+                arrive(&sm.s_free[t]);
 
                 float sc = row_scale, ev = 0.f;
                 uint32_t loaded = 0xffffffffu;
@@ -557,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::tmem_st32(p_addr + c, *reinterpret_cast<const uint32_t(*)[32]>(&pk[c]));
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
-                mbar_arrive(&sm.p_full[t]);
+                arrive(&sm.p_full[t]);
             }
             const Unit &u = *up;
             vtile += u.t1 - t0;
@@ -835,64 +852,82 @@ __global__ void __launch_bounds__(kThreads, 1)
                     raise_status(a.status, NS_DEV_WAIT_TIMEOUT);
             }
             __syncwarp();
-        } else if (warp == kScoreWarp || warp == kValueWarp) {
+        } else if (warp == kProductWarp || warp == kProductWarp + 1) {
             // ------------------------------------------------------------ products
-            // the whole warp walks the tiles; operands are warp-uniform
-            const bool scores = warp == kScoreWarp;
+            // One warp for each query tile: the scores of key tile j + 1 as soon as those
+            // of j were read, then the values of j as soon as its weights are there.  The
+            // whole warp walks the tiles; operands are warp-uniform.
+            const int t = warp - kProductWarp;
             const uint32_t idesc_s = tc::idesc_f16(kRows, KT, BF && !Q8 ? 1 : 0, false);
             const uint32_t idesc_o = tc::idesc_f16(kRows, D, 0, true);
-            const uint64_t d0 = scores ? tc::desc_sw128(0) : tc::desc_sw128_panels(0, KT * kPanel);
-            const uint32_t d_lo = (uint32_t)d0, d_hi = (uint32_t)(d0 >> 32);
+            const uint64_t dk = tc::desc_sw128(0), dv = tc::desc_sw128_panels(0, KT * kPanel);
             auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
-            const uint32_t tm = uniform(tmem), q_lo = uniform(d_lo + (smem_addr(sm.q[0]) >> 4)),
-                           kv_lo = uniform(d_lo + (smem_addr(scores ? sm.k[0] : sm.v[0]) >> 4));
-            uint32_t stage = 0, par = 0, units[2] = {0, 0}, count[2] = {0, 0};
+            const uint32_t tm = uniform(tmem), q_lo = uniform((uint32_t)dk + (smem_addr(sm.q[t]) >> 4)),
+                           k_lo = uniform((uint32_t)dk + (smem_addr(sm.k[0]) >> 4)),
+                           v_lo = uniform((uint32_t)dv + (smem_addr(sm.v[0]) >> 4));
+            uint32_t units = 0, count = 0;
+            uint32_t ks = 0, kpar = 0, vs = 0, vpar = 0;  // stages of K and V
             for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
-                const int end[2] = {min(u.t1, tiles_of<KT>(u, 0, qt)), min(u.t1, tiles_of<KT>(u, 1, qt))};
-                for (int j = u.t0; ok && j < u.t1; ++j) {
-                    const uint32_t b_lo = uniform(kv_lo + stage * (GG::TILE >> 4));
-                    const bool more = uniform(j > u.t0 ? 1u : 0u) != 0;
-                    ok = warp_wait(scores ? &sm.k_ready[stage] : &sm.v_ready[stage], par);
+                const int end = min(u.t1, tiles_of<KT>(u, t, qt));
+                // a tile without rows for this key tile still hands its stages back, once
+                // they hold it, so that both tiles count the same uses
+                auto scores = [&](int j) {
+                    ok = warp_wait(&sm.k_ready[ks], kpar);
+                    if (!ok)
+                        return;
+                    if (j < end) {
+                        ok = (j > u.t0 || warp_wait(&sm.q_ready[t], units & 1u)) &&
+                             (count == 0 || warp_wait(&sm.s_free[t], (count - 1) & 1u));
+                        if (!ok)
+                            return;
+                        tc::fence_after_sync();
+                        const uint32_t b_lo = uniform(k_lo + ks * (GG::TILE >> 4));
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (!ok || j >= end[t])
-                            continue;
-                        if (scores) {
-                            // S of tile t, once its previous scores were read
-                            ok = (j > u.t0 || warp_wait(&sm.q_ready[t], units[t] & 1u)) &&
-                                 (count[t] == 0 || warp_wait(&sm.s_free[t], (count[t] - 1) & 1u));
-                            if (!ok)
-                                continue;
-                            tc::fence_after_sync();
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                tc::mma_ss_warp(tm + t * KT,
-                                                q_lo + ((t * (REG * kRows * kPanel) + (kk >> 2) * (kRows * kPanel) + (kk & 3) * 32) >> 4),
-                                                b_lo + (((kk >> 2) * (KT * kPanel) + (kk & 3) * 32) >> 4), d_hi, idesc_s,
-                                                kk > 0);
-                            tc::mma_commit_warp(&sm.s_full[t]);
-                        } else {
-                            ok = warp_wait(&sm.p_full[t], count[t] & 1u);
-                            if (!ok)
-                                continue;
-                            tc::fence_after_sync();
-#pragma unroll
-                            for (int kk = 0; kk < KT / 16; ++kk)
-                                tc::mma_ts_warp(tm + GG::O + t * D, tm + GG::P + t * (KT / 2) + kk * 8,
-                                                b_lo + ((kk * 16 * kPanel) >> 4), d_hi, idesc_o, kk > 0 || more);
-                            tc::mma_commit_warp(&sm.pv_done[t]);
-                        }
-                        ++count[t];
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc::mma_ss_warp(tm + t * KT, q_lo + (((kk >> 2) * (kRows * kPanel) + (kk & 3) * 32) >> 4),
+                                            b_lo + (((kk >> 2) * (KT * kPanel) + (kk & 3) * 32) >> 4),
+                                            (uint32_t)(dk >> 32), idesc_s, kk > 0);
+                        tc::mma_commit_warp(&sm.s_full[t]);
+                        ++count;
                     }
-                    if (ok)
-                        tc::mma_commit_warp(scores ? &sm.k_empty[stage] : &sm.v_empty[stage]);
-                    if (++stage == ST) {
-                        stage = 0;
-                        par ^= 1u;
+                    tc::mma_commit_warp(&sm.k_empty[ks]);
+                    if (++ks == ST) {
+                        ks = 0;
+                        kpar ^= 1u;
+                    }
+                };
+                if (u.t0 < u.t1)
+                    scores(u.t0);
+                uint32_t done = count - (end > u.t0 ? 1u : 0u);  // value products so far
+                for (int j = u.t0; ok && j < u.t1; ++j) {
+                    if (j + 1 < u.t1)
+                        scores(j + 1);
+                    if (!ok)
+                        break;
+                    ok = warp_wait(&sm.v_ready[vs], vpar);
+                    if (!ok)
+                        break;
+                    if (j < end) {
+                        ok = warp_wait(&sm.p_full[t], done & 1u);
+                        if (!ok)
+                            break;
+                        ++done;
+                        tc::fence_after_sync();
+                        const uint32_t b_lo = uniform(v_lo + vs * (GG::TILE >> 4));
+                        const bool more = uniform(j > u.t0 ? 1u : 0u) != 0;
+#pragma unroll
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            tc::mma_ts_warp(tm + GG::O + t * D, tm + GG::P + t * (KT / 2) + kk * 8,
+                                            b_lo + ((kk * 16 * kPanel) >> 4), (uint32_t)(dv >> 32), idesc_o, kk > 0 || more);
+                        tc::mma_commit_warp(&sm.pv_done[t]);
+                    }
+                    tc::mma_commit_warp(&sm.v_empty[vs]);
+                    if (++vs == ST) {
+                        vs = 0;
+                        vpar ^= 1u;
                     }
                 }
-                for (int t = 0; t < 2; ++t)
-                    units[t] += end[t] > u.t0 ? 1 : 0;
+                units += end > u.t0 ? 1u : 0u;
             }
             if (!ok && lane == 0)
                 raise_status(a.status, NS_DEV_WAIT_TIMEOUT);
@@ -1001,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == kScoreWarp) {
+    if (warp == kProductWarp) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
     }
