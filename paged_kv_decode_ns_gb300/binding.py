@@ -142,10 +142,16 @@ def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
     return t.data_ptr()
 
 
+# The current stream's handle without the Python object around it (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if getattr(_capture, "on", False):
         return _STREAM_SLOT
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -394,22 +400,20 @@ def ns_kv_append_paged_attn_decode_q8_0(q, k_new, v_new, slot_mapping, k_codes, 
     _check(st, "ns_kv_append_paged_attn_decode_q8_0")
 
 
-def _rows(t: torch.Tensor, name: str, dtype) -> int:
-    """Pointer of [T, H, D] rows that are dense themselves and any stride apart."""
+def _rows(t: torch.Tensor, name: str, dtype):
+    """Pointer of [T, H, D] rows that are dense themselves, and elements from one to the next
+    (with no next row, the row's own width)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.numel() and ((t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1)):
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if n and h and d and ((s2 != 1 and d > 1) or (s1 != d and h > 1)):
         raise ValueError(f"the rows of {name} must be dense [heads, head_dim]")
-    return t.data_ptr()
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """Elements from one row to the next; with no next row, the row's own width."""
-    return t.stride(0) if t.shape[0] > 1 else t[0].numel() if t.shape[0] else t.shape[1] * t.shape[2]
+    return t.data_ptr(), s0 if n > 1 else h * d
 
 
 def ns_span_attn_workspace_bytes(head_dim: int = 64) -> int:
@@ -439,12 +443,13 @@ def ns_prompt_attn(q, k, v, query_start_loc, scale, out, workspace, key_start_lo
             raise ValueError("k and v must have q's rows when key_start_loc is not given")
     elif key_start_loc.shape != query_start_loc.shape:
         raise ValueError("key_start_loc must be [num_seqs + 1]")
+    dtype = q.dtype
     dt = _dtype_code(q)
-    st = _invoke("ns_prompt_attn", _rows(q, "q", q.dtype), _rows(k, "k", q.dtype), _rows(v, "v", q.dtype),
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", dtype), _rows(k, "k", dtype), _rows(v, "v", dtype)
+    st = _invoke("ns_prompt_attn", qp, kp, vp,
                  _dev(query_start_loc, "query_start_loc", torch.int32),
                  None if key_start_loc is None else _dev(key_start_loc, "key_start_loc", torch.int32),
-                 S, T, Tk, hq, hkv, d, _row_stride(q), _row_stride(k), _row_stride(v), float(scale),
-                 _dev(out, "out", q.dtype), _stream(stream), dt, _dev(workspace, "workspace", torch.uint8),
+                 S, T, Tk, hq, hkv, d, qs, ks, vs, float(scale), _dev(out, "out", dtype), _stream(stream), dt, _dev(workspace, "workspace", torch.uint8),
                  workspace.numel())
     _check(st, "ns_prompt_attn")
 

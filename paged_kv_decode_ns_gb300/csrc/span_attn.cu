@@ -2,6 +2,7 @@
 // dispatch (the kernels are in span_attn.cuh).
 #include "span_attn.cuh"
 
+#include <atomic>
 #include <cmath>
 
 namespace ns {
@@ -14,12 +15,19 @@ size_t span_attn_workspace_bytes(int head_dim)
 
 cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream)
 {
-    int dev = 0, sms = 0;
+    static std::atomic<int> known[64];  // SMs of each device
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
+    int sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (sms == 0) {
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            known[dev].store(sms, std::memory_order_relaxed);
+    }
     span::Params P;
     P.a = a;
     P.group = a.num_q_heads / a.num_kv_heads;

@@ -51,7 +51,7 @@ constexpr int kRegs = 128;       // registers a thread at launch; the warpgroups
 constexpr int kSoftmaxRegs = 200, kConvertRegs = 64, kOtherRegs = 48;
 static_assert(2 * kSoftmaxRegs + kConvertRegs + kOtherRegs <= 4 * kRegs, "the shares fit the launch's registers");
 constexpr int kTileWarps = 4;    // softmax warps of a query tile
-constexpr int kConvertWarp = 8, kProducerWarp = 12, kProductWarp = 13;  // 13, 14: query tiles 0, 1
+constexpr int kConvertWarp = 8, kProducerWarp = 12, kProductWarp = 13, kPlanWarp = 15;  // 13, 14: query tiles 0, 1
 constexpr int kPanel = 128;      // bytes of a row of a panel: 64 elements, one swizzle span
 constexpr int kUnits = 4;        // units announced ahead
 constexpr int kMaxCtas = 160;    // grid, at most: the workspace has two records for each
@@ -71,7 +71,8 @@ struct Geo {
     // cost of a unit besides its keys (laying out Q, filling the pipe, the epilogue)
     // and the least cost that a CTA is given, in keys
     static constexpr int OVERHEAD = 2 * KT;
-    static constexpr int SHARE = 4 * KT;
+    static constexpr int SHARE = OVERHEAD + KT / 2;
+    static constexpr int WHOLE = 4;  // units of so few key tiles are not cut
 };
 
 // A CTA's part of a unit: key tiles [t0, t1).
@@ -168,6 +169,11 @@ __device__ __forceinline__ Seq read_seq(const SpanAttnArgs &a, int s, unsigned *
         r.n = 0;
     }
     return r;
+}
+
+__device__ __forceinline__ long long quotient(long long a, long long b)  // a >= 0, b > 0
+{
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Cost of the first u units of one kv head of a sequence (u < its units): unit v
@@ -283,6 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const SpanAttnArgs &a = P.a;
     const int qt = P.qt, R = 2 * P.qt;
 
+    if (!Q8 && threadIdx.x == kProducerWarp * 32) {
+        tc::prefetch_tensormap(&tm_k);
+        tc::prefetch_tensormap(&tm_v);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&sm.k_ready[i], Q8 ? 128 : 1);
@@ -316,10 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     grid_launch_dependents();  // the joining kernel may be set up; it waits for this grid's end
 
-    // ---- this CTA's run of the line: every thread costs its share of the sequences
+    // ---- this CTA's run of the line: one warp costs up to 32 sequences, the whole
+    // CTA more of them, a share for every thread
     {
-        const int per = ceil_div(a.num_seqs, kThreads);
-        const int s0 = min(a.num_seqs, (int)threadIdx.x * per), s1 = min(a.num_seqs, s0 + per);
         auto cost = [&](int s, unsigned *status) -> long long {
             const Seq q = read_seq<Q8>(a, s, status);
             if (q.n == 0)
@@ -327,45 +336,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long units = ceil_div(q.n, R), each = GG::OVERHEAD + max(q.L - q.n, 0);
             return (cost_before(units - 1, each, R) + each + q.n) * a.num_kv_heads;
         };
-        long long mine = 0;
-        for (int s = s0; s < s1; ++s)
-            mine += cost(s, blockIdx.x == 0 ? a.status : nullptr);
-        long long incl = mine;
+        const bool few = a.num_seqs <= 32;
+        const int per = few ? 1 : ceil_div(a.num_seqs, kThreads), who = few ? lane : (int)threadIdx.x;
+        if (!few || warp == kPlanWarp) {
+            const int s0 = min(a.num_seqs, who * per), s1 = min(a.num_seqs, s0 + per);
+            long long mine = 0;
+            for (int s = s0; s < s1; ++s)
+                mine += cost(s, blockIdx.x == 0 ? a.status : nullptr);
+            long long incl = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o)
-                incl += y;
-        }
-        if (lane == 31)
-            sm.scan[warp] = incl;
-        __syncthreads();
-        long long before = incl - mine, total = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const long long x = sm.scan[w];
-            if (w < warp)
-                before += x;
-            total += x;
-        }
-        const int ctas = (int)min((long long)gridDim.x, max(1LL, total / GG::SHARE));
-        const int c = blockIdx.x;
-        const long long x0 = c < ctas ? total * c / ctas : total, x1 = c < ctas ? total * (c + 1) / ctas : total;
-        if (threadIdx.x == 0) {
-            sm.x0 = x0;
-            sm.x1 = x1;
-        }
-        if (x0 < x1 && x0 >= before && x0 < before + mine) {
-            long long x = before;
-            int s = s0;
-            for (;; ++s) {
-                const long long w = cost(s, nullptr);
-                if (x0 < x + w)
-                    break;
-                x += w;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += y;
             }
-            sm.start_s = s;
-            sm.start_x = x;
+            long long before = incl - mine, total = __shfl_sync(0xffffffffu, incl, 31);
+            if (!few) {
+                if (lane == 31)
+                    sm.scan[warp] = incl;
+                __syncthreads();
+                total = 0;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const long long x = sm.scan[w];
+                    if (w < warp)
+                        before += x;
+                    total += x;
+                }
+            }
+            const int ctas = (int)min((long long)gridDim.x, max(1LL, quotient(total, GG::SHARE)));
+            const long long share = quotient(total, ctas), rest = total - share * ctas;
+            const long long c = min((int)blockIdx.x, ctas), x0 = share * c + min(c, rest),
+                            x1 = c < ctas ? x0 + share + (c < rest ? 1 : 0) : x0;
+            if (who == 0) {
+                sm.x0 = x0;
+                sm.x1 = x1;
+            }
+            if (x0 < x1 && x0 >= before && x0 < before + mine) {
+                long long x = before;
+                int s = s0;
+                for (;; ++s) {
+                    const long long w = cost(s, nullptr);
+                    if (x0 < x + w)
+                        break;
+                    x += w;
+                }
+                sm.start_s = s;
+                sm.start_x = x;
+            }
         }
     }
     tc::fence_before_sync();
@@ -762,10 +780,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_shrink<kOtherRegs>();
         if (warp == kProducerWarp) {
             // ------------------------------------------------------------ producer
-            if (!Q8 && lane == 0) {
-                tc::prefetch_tensormap(&tm_k);
-                tc::prefetch_tensormap(&tm_v);
-            }
             int tile = 0;
             for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
                 const int blocks = Q8 ? ceil_div(u.L, 16) : 0;
@@ -976,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const long long per_head = cost_before(units - 1, each, R) + each + q.n;
                     h = v = 0;
                     if (first) {
-                        h = (int)((x0 - xs) / per_head);
+                        h = (int)quotient(x0 - xs, per_head);
                         v = unit_at(x0 - xs - h * per_head, units, each, R);
                         first = false;
                     }
@@ -999,6 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int keys = q.L - q.n + min(q.n, u.i0 + R);
                             const int all = keys > 0 ? ceil_div(keys, KT) : 0;
                             auto cut = [&](long long x) {  // the key tile that position x falls before
+                                if (all <= GG::WHOLE)
+                                    return 2 * (x - us) > ue - us ? all : 0;
                                 const long long d = (x - us - GG::OVERHEAD) / KT;
                                 return (int)min(max(d, 0LL), (long long)all);
                             };
@@ -1109,6 +1125,7 @@ __global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ 
 template <typename T, int D, bool Q8>
 cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &P, int ctas, cudaStream_t stream)
 {
+    const long long max_keys = Q8 ? (long long)P.a.max_blocks_per_seq * 16 : P.a.total_k_tokens;
     // once for each device: the shared memory, and that the kernel has the registers
     // that its warpgroups share out (with fewer they would wait for ever)
     static unsigned long long ready = 0;
@@ -1131,7 +1148,9 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &P
     }
     span_attn_kernel<T, D, Q8><<<ctas, kThreads, smem_bytes<D, Q8>(), stream>>>(tk, tv, P);
     e = cudaGetLastError();
-    if (e != cudaSuccess)
+    // no sequence has the keys of a unit that may be cut (the second launch costs
+    // 3 us of a small call)
+    if (e != cudaSuccess || max_keys <= Geo<D, Q8>::WHOLE * Geo<D, Q8>::KT)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas * 8);
