@@ -28,11 +28,12 @@
 //
 // P is rounded to fp16 (11 bits) for both types: the products of a bf16 call
 // would need P in two bf16 parts for the same accuracy, twice the value products.
-// So V is fp16 too: a bf16 tile is scaled by a power of two, 2^-Ev, that puts its
-// largest value just below 2^15, which keeps every value within 2^-29 of that
-// exact.  Ev moves into the exponent of P, 2^(z + Ev - m), with m a running
-// reference of z + Ev; the sum takes it back out.  q8_0 tiles are dequantised to
-// fp16 in the same way, with Ek for K in the score's scale.
+// So V is fp16 too: a group of bf16 keys (those of one conversion warp) is scaled by
+// a power of two, 2^-Ev, that puts its largest value just below 2^15, which keeps
+// every value within 2^-29 of that exact.  Ev moves into the exponent of P,
+// 2^(z + Ev - m), with m a running reference of z + Ev; the sum takes it back out.
+// q8_0 tiles are dequantised to fp16 in the same way, with Ek for K in the score's
+// scale.
 #pragma once
 
 #include <algorithm>
@@ -54,6 +55,7 @@ constexpr int kTileWarps = 4;    // softmax warps of a query tile
 constexpr int kConvertWarp = 8, kProducerWarp = 12, kProductWarp = 13, kPlanWarp = 15;  // 13, 14: query tiles 0, 1
 constexpr int kPanel = 128;      // bytes of a row of a panel: 64 elements, one swizzle span
 constexpr int kUnits = 4;        // units announced ahead
+constexpr int kMeta = 8;
 constexpr int kMaxCtas = 160;    // grid, at most: the workspace has two records for each
 constexpr float kTinyScale = 1.17549435e-38f;  // a score of -infinity times a scale of 0 would be NaN
 constexpr float kSlack = 8.0f;   // the reference moves when a score passes it by more (log2 units)
@@ -63,6 +65,7 @@ struct Geo {
     static constexpr int KT = D == 64 ? 128 : 64;  // keys of a tile
     static constexpr int REG = D / 64;             // panels of a row
     static constexpr int TILE = REG * KT * kPanel; // bytes of a K or V tile
+    static constexpr int GROUP = KT / 4;           // keys with an exponent of their own: a conversion warp's
     static constexpr int STAGES = Q8 ? 3 : 4;
     static constexpr int RAW = Q8 ? 4 : 1;         // q8_0 tiles in flight
     // TMEM columns: S of tile t at KT t, O at 2 KT + D t, P at 2 KT + 2 D + KT / 2 t
@@ -70,8 +73,8 @@ struct Geo {
     static_assert(P + KT <= 512, "tensor memory");
     // cost of a unit besides its keys (laying out Q, filling the pipe, the epilogue)
     // and the least cost that a CTA is given, in keys
-    static constexpr int OVERHEAD = 2 * KT;
-    static constexpr int SHARE = OVERHEAD + KT / 2;
+    static constexpr int OVERHEAD = D == 64 ? 5 * KT / 2 : 7 * KT;
+    static constexpr int SHARE = OVERHEAD;  // at most one short unit a CTA while there are CTAs
     static constexpr int WHOLE = 4;  // units of so few key tiles are not cut
 };
 
@@ -87,8 +90,8 @@ struct Unit {
 struct alignas(16) Header {
     int own;               // it holds the first part of a cut unit (record 2 c + 1)
     int row0, tokens, h;   // that unit's first query row, its tokens, its kv head
-    int head;              // it holds a later part (record 2 c)
-    int ends;              // which is the last
+    int last;              // and the last CTA with a part of it
+    int head;              // it holds a later part of a unit (record 2 c)
     int pad[2];
 };
 
@@ -116,14 +119,15 @@ struct alignas(1024) Smem {
     uint64_t k_ready[GG::STAGES], v_ready[GG::STAGES], k_empty[GG::STAGES], v_empty[GG::STAGES];
     uint64_t q_ready[2], s_full[2], s_free[2], p_full[2], pv_done[2];
     uint64_t u_full[kUnits], u_empty[kUnits];
-    uint64_t topped;  // the conversion warps have their maxima in place
     Unit unit[kUnits], no_unit;
-    float ek[GG::STAGES], ev[GG::STAGES];   // exponents of a stage's tiles
-    uint32_t loaded[GG::STAGES];            // q8_0: blocks of the tile that were read
+    alignas(16) float ev[GG::STAGES][4];    // Ev of a stage's V, by group of keys
+    // q8_0: 2^Ek of a tile's K, and its blocks that were read.  A K stage is free
+    // before the softmax has looked here; a ring of more than STAGES + 1 is not
+    alignas(16) float ek[kMeta][4];
+    uint32_t loaded[kMeta];
     uint32_t raw_loaded[GG::RAW];
-    uint32_t top[2][2][4];                  // the conversion warps' maxima
     long long scan[kWarps];
-    long long start_x, x0, x1;
+    long long start_x, x0, x1, share, rest;
     int start_s;
     uint32_t tmem_base;
 };
@@ -295,15 +299,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&sm.k_ready[i], Q8 ? 128 : 1);
+            mbar_init(&sm.k_ready[i], Q8 ? 4 : 1);
             mbar_init(&sm.v_full[i], 1);
-            mbar_init(&sm.v_ready[i], 128);
+            mbar_init(&sm.v_ready[i], 4);
             mbar_init(&sm.k_empty[i], 2);  // both tiles' products
             mbar_init(&sm.v_empty[i], 2);
         }
         for (int i = 0; i < GG::RAW; ++i) {
             mbar_init(&sm.raw_full[i], 1);
-            mbar_init(&sm.raw_empty[i], 128);
+            mbar_init(&sm.raw_empty[i], 4);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.q_ready[t], kTileWarps);
@@ -316,7 +320,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.u_full[i], 1);
             mbar_init(&sm.u_empty[i], kWarps - 1);  // one arrival a warp, but the walk's
         }
-        mbar_init(&sm.topped, 128);
         sm.no_unit.t1 = -1;
         mbar_init_fence();
     }
@@ -324,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_alloc(&sm.tmem_base, 512);
         tc::tmem_relinquish();
     }
+    grid_dependency_wait();
     grid_launch_dependents();  // the joining kernel may be set up; it waits for this grid's end
 
     // ---- this CTA's run of the line: one warp costs up to 32 sequences, the whole
@@ -371,6 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (who == 0) {
                 sm.x0 = x0;
                 sm.x1 = x1;
+                sm.share = share;
+                sm.rest = rest;
             }
             if (x0 < x1 && x0 >= before && x0 < before + mine) {
                 long long x = before;
@@ -511,18 +517,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 arrive(&sm.s_free[t]);
 
-                float sc = row_scale, ev = 0.f;
+                // scale of the scores and exponent of the values, by group of keys
+                constexpr int NG = SCALED ? 4 : 1, GK = KT / NG;
+                float sc[NG], ev[NG];
                 uint32_t loaded = 0xffffffffu;
+                sc[0] = row_scale;
+                ev[0] = 0.f;
                 if (SCALED) {
-                    if (!warp_wait(&sm.v_ready[stage], (uint32_t)((vtile + j - t0) / ST) & 1u)) {
+                    const int tile = vtile + j - t0;
+                    if (!warp_wait(&sm.v_ready[stage], (uint32_t)(tile / ST) & 1u)) {
                         ok = false;
                         break;
                     }
-                    ev = sm.ev[stage];
-                    if (Q8) {
-                        sc = fmaxf(sc * sm.ek[stage], kTinyScale);
-                        loaded = sm.loaded[stage];
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        ev[g] = sm.ev[stage][g];
+                        sc[g] = Q8 ? fmaxf(row_scale * sm.ek[tile % kMeta][g], kTinyScale) : row_scale;
                     }
+                    if (Q8)
+                        loaded = sm.loaded[tile % kMeta];
                 }
                 const int base = j * KT;
                 if (base + KT - 1 > low) {
@@ -536,13 +549,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < KT; ++c)
                         sv[c] = (loaded >> (c / 16)) & 1u ? sv[c] : -INFINITY;
                 }
-                float tm[4] = {sv[0], sv[1], sv[2], sv[3]};
+                float top = -INFINITY;
+                {
+                    float tm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 4; c < KT; c += 8)
+                    for (int c = 0; c < KT / 4; c += 2)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        tm[e] = c + 4 + e < KT ? max3(tm[e], sv[c + e], sv[c + 4 + e]) : fmaxf(tm[e], sv[c + e]);
-                const float top = fmaf(fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])), sc, ev);
+                        for (int e = 0; e < 4; ++e)  // a quarter of the columns each
+                            tm[e] = max3(tm[e], sv[e * (KT / 4) + c], sv[e * (KT / 4) + c + 1]);
+                    if (SCALED) {
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+                            top = fmaxf(top, fmaf(tm[g], sc[g], ev[g]));
+                    } else {
+                        top = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * sc[0];
+                    }
+                }
                 float m_new = m, alpha = 1.f;
                 bool moved = false;
                 if (top > m + kSlack) {
@@ -552,20 +574,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l *= alpha;
                 }
                 m = m_new;
-                const float nm = m > -INFINITY ? ev - m : 0.f;
-
-                const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float ref = m > -INFINITY ? m : 0.f;
                 uint32_t pk[KT / 2];
 #pragma unroll
-                for (int c = 0; c < KT; c += 2) {
-                    const float2 z = ffma2(make_float2(sv[c], sv[c + 1]), sc2, nm2);
-                    const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-                    sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], p);
-                    pk[c >> 1] = pack2<F16>(p.x, p.y);
+                for (int g = 0; g < NG; ++g) {
+                    const float nm = ev[g] - ref;
+                    const float2 sc2 = make_float2(sc[g], sc[g]), nm2 = make_float2(nm, nm);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = g * GK; c < (g + 1) * GK; c += 2) {
+                        const float2 z = ffma2(make_float2(sv[c], sv[c + 1]), sc2, nm2);
+                        const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                        sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], p);
+                        pk[c >> 1] = pack2<F16>(p.x, p.y);
+                    }
+                    const float ts = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    l += SCALED ? ts * fast_exp2(-ev[g]) : ts;
                 }
-                const float ts = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                l += SCALED ? ts * fast_exp2(-ev) : ts;
 
                 // P is free, and O at rest, once the previous tile's value products are done
                 if (count > 0 && !warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u)) {
@@ -663,9 +688,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kProducerWarp) {
         // ------------------------------------------------------------ conversion
         regs_shrink<kConvertRegs>();
-        const int r = threadIdx.x - kConvertWarp * 32, w4 = warp - kConvertWarp;
-        const int key = r % KT;                      // row of the tile, panel r / KT
-        const int panel = (r / KT) * (KT * kPanel) + key * kPanel;
+        // a warp a group of keys, with exponents of its own, so that the warps do not
+        // wait for each other; a lane a key (D 64) or one panel of a key
+        const int group = warp - kConvertWarp;
+        const int key = group * GG::GROUP + lane / REG, pan = lane % REG;
+        const int panel = pan * (KT * kPanel) + key * kPanel;
+        const int turn = (key & 7) ^ (pan << 2);  // order of the chunks: no two of eight lanes share a bank
         int tile = 0;
         for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
             for (int j = u.t0; ok && j < u.t1; ++j, ++tile) {
@@ -683,26 +711,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t top = 0;
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            x[c] = live ? lds128(row + ((c ^ (r & 7)) << 4)) : make_uint4(0u, 0u, 0u, 0u);
+                            x[c] = live ? lds128(row + ((c ^ turn) << 4)) : make_uint4(0u, 0u, 0u, 0u);
                             top = top16(x[c], top);
                         }
                         top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-                        if (lane == 0)
-                            sm.top[tile & 1][0][w4] = top;
-                        mbar_arrive(&sm.topped);
-                        if (!warp_wait(&sm.topped, (uint32_t)tile & 1u)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t *all = sm.top[tile & 1][0];
-                        top = max(max(all[0], all[1]), max(all[2], all[3]));
                         const int e = max((int)(top >> 7), 45);
                         const float f = pow2(141 - e);
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
-                            *reinterpret_cast<uint4 *>(row + ((c ^ (r & 7)) << 4)) = bf16_to_f16(x[c], f);
-                        if (r == 0)
-                            sm.ev[stage] = (float)(e - 141);
+                            *reinterpret_cast<uint4 *>(row + ((c ^ turn) << 4)) = bf16_to_f16(x[c], f);
+                        if (lane == 0)
+                            sm.ev[stage][group] = (float)(e - 141);
                         fence_async_smem();
                     } else if (!live) {
 #pragma unroll
@@ -710,11 +729,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4 *>(row + c * 16) = make_uint4(0u, 0u, 0u, 0u);
                         fence_async_smem();
                     }
-                    mbar_arrive(&sm.v_ready[stage]);
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sm.v_ready[stage]);
                 } else {
                     const int rs = tile % GG::RAW;
-                    if (!warp_wait(&sm.raw_full[rs], (uint32_t)(tile / GG::RAW) & 1u) ||
-                        !warp_wait(&sm.k_empty[stage], par ^ 1u) || !warp_wait(&sm.v_empty[stage], par ^ 1u)) {
+                    if (!warp_wait(&sm.raw_full[rs], (uint32_t)(tile / GG::RAW) & 1u)) {
                         ok = false;
                         break;
                     }
@@ -723,54 +743,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool have = live && ((loaded >> (key / 16)) & 1u);
                     const uint32_t *scales = reinterpret_cast<const uint32_t *>(raw + 2 * KT * 64);
                     const uint32_t d[2] = {have ? scales[key] : 0u, have ? scales[KT + key] : 0u};
+                    // code chunks in an order in which neither the reads (64-byte rows) nor the
+                    // writes (swizzled 128-byte rows) of eight lanes share a bank
+                    const int half = (key >> 1) & 3, first = (half << 1) ^ ((half >> 1) * 7);
+                    uint4 code[2][4];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            code[x][c] = lds128(raw + x * KT * 64 + key * 64 + ((c ^ first) << 4));
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t mag = d[x] & 0x7fff7fffu;
-                        const uint32_t top = __reduce_max_sync(0xffffffffu, max(mag & 0xffffu, mag >> 16));
-                        if (lane == 0)
-                            sm.top[tile & 1][x][w4] = top;
-                    }
-                    mbar_arrive(&sm.topped);
-                    if (!warp_wait(&sm.topped, (uint32_t)tile & 1u)) {
-                        ok = false;
-                        break;
-                    }
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t *all = sm.top[tile & 1][x];
-                        const int e = (int)(max(max(all[0], all[1]), max(all[2], all[3])) >> 10);
-                        if (r == 0) {  // the largest scale goes just below 2^8, its codes below 2^15
-                            if (x == 0) {
-                                sm.ek[stage] = pow2(e - 22);
-                                sm.loaded[stage] = loaded;
-                            } else {
-                                sm.ev[stage] = (float)(e - 22);
-                            }
-                        }
+                        const int e = (int)(__reduce_max_sync(0xffffffffu, max(mag & 0xffffu, mag >> 16)) >> 10);
+                        // the largest scale goes just below 2^8, its codes below 2^15
                         const float2 ds = unpack2<F16>(d[x]);
                         const float f = pow2(22 - e);
-                        const __half2 lo = __float2half2_rn(ds.x * f), hi = __float2half2_rn(ds.y * f);
-                        const uint8_t *codes = raw + x * KT * 64 + key * 64;
+                        const __half2 dd[2] = {__float2half2_rn(ds.x * f), __float2half2_rn(ds.y * f)};
+                        if (!warp_wait(x == 0 ? &sm.k_empty[stage] : &sm.v_empty[stage], par ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) {
+                            if (x == 0)
+                                sm.ek[tile % kMeta][group] = pow2(e - 22);
+                            else
+                                sm.ev[stage][group] = (float)(e - 22);
+                            if (x == 0 && group == 0)
+                                sm.loaded[tile % kMeta] = loaded;
+                        }
                         uint8_t *row = (x == 0 ? sm.k[stage] : sm.v[stage]) + panel;
-                        // code chunks in an order in which neither the reads (64-byte rows)
-                        // nor the writes (swizzled 128-byte rows) of eight threads share a bank
-                        const int half = (r >> 1) & 3, turn = (half << 1) ^ ((half >> 1) * 7);
 #pragma unroll
                         for (int c0 = 0; c0 < 4; ++c0) {
-                            const int c = c0 ^ turn;
-                            const uint4 q = lds128(codes + c * 16);
-                            const __half2 dd = c < 2 ? lo : hi;
-                            const uint2 e0 = codes_to_f16(q.x, dd), e1 = codes_to_f16(q.y, dd),
-                                        e2 = codes_to_f16(q.z, dd), e3 = codes_to_f16(q.w, dd);
-                            *reinterpret_cast<uint4 *>(row + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
-                            *reinterpret_cast<uint4 *>(row + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(e2.x, e2.y, e3.x, e3.y);
+                            const int c = c0 ^ first;
+                            const uint4 q = code[x][c0];
+                            const __half2 s2 = c < 2 ? dd[0] : dd[1];
+                            const uint2 e0 = codes_to_f16(q.x, s2), e1 = codes_to_f16(q.y, s2),
+                                        e2 = codes_to_f16(q.z, s2), e3 = codes_to_f16(q.w, s2);
+                            *reinterpret_cast<uint4 *>(row + (((2 * c) ^ (key & 7)) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
+                            *reinterpret_cast<uint4 *>(row + (((2 * c + 1) ^ (key & 7)) << 4)) = make_uint4(e2.x, e2.y, e3.x, e3.y);
                         }
                         fence_async_smem();
-                        if (x == 0)
-                            mbar_arrive(&sm.k_ready[stage]);
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(x == 0 ? &sm.k_ready[stage] : &sm.v_ready[stage]);
                     }
-                    mbar_arrive(&sm.v_ready[stage]);
-                    mbar_arrive(&sm.raw_empty[rs]);
+                    if (lane == 0)
+                        mbar_arrive(&sm.raw_empty[rs]);
                 }
             }
         }
@@ -948,6 +967,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
             // ------------------------------------------------------------ the walk
             const long long x0 = sm.x0, x1 = sm.x1;
+            auto owner = [&](long long x) {  // the CTA whose run position x falls into
+                const long long wide = (sm.share + 1) * sm.rest;
+                return (int)(x < wide ? quotient(x, sm.share + 1) : sm.rest + quotient(x - wide, sm.share));
+            };
             Header head = {};
             int no = 0;
             auto announce = [&](const Unit &u) {
@@ -1026,13 +1049,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (u.t0 > 0) {
                                 u.rec = 2 * blockIdx.x;
                                 head.head = 1;
-                                head.ends = u.t1 == all;
                             } else if (u.t1 < all) {
                                 u.rec = 2 * blockIdx.x + 1;
                                 head.own = 1;
                                 head.row0 = q.q0 + u.i0;
                                 head.tokens = min(R, q.n - u.i0);
                                 head.h = h;
+                                head.last = owner(ue - 1);
                             }
                             announce(u);
                         }
@@ -1060,53 +1083,62 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of cut units: 32 rows of one unit a block, a warp an eighth of
 // the columns.  Parts come in the order of the keys, so results do not depend on
-// which CTA ended first.
+// which CTA ended first.  The header says which CTAs hold parts, so that everything
+// else is read at once: two round trips to L2.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ Params P, int ctas)
+__global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ Params P)
 {
     constexpr int kPer = D / 32;  // float4 columns a thread
+    constexpr int kBatch = 4;     // parts read at once
     grid_dependency_wait();
+    grid_launch_dependents();
     const int c = blockIdx.x / 8, row = (blockIdx.x % 8) * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
     const Header hd = P.headers[c];
-    if (!hd.own)
-        return;
     const int t = row / kRows, r = row % kRows, rt = r / P.group;
     const int tok = t * P.qt + rt;
-    if (rt >= P.qt || tok >= hd.tokens)
+    if (!hd.own || rt >= P.qt || tok >= hd.tokens)
         return;
-    auto record = [&](int i) { return P.records + (size_t)(i == c ? 2 * c + 1 : 2 * i) * record_floats(D); };
-    // the CTAs behind c up to the unit's last part
-    int last = c;
-    float top = record(c)[(size_t)D * 2 * kRows + row];
-    for (int i = c + 1; i < ctas; ++i) {
-        const Header x = P.headers[i];
-        if (x.head) {
-            last = i;
-            top = fmaxf(top, record(i)[(size_t)D * 2 * kRows + row]);
-            if (x.ends)
-                break;
-        }
-        if (x.own)
-            break;
-    }
     float4 acc[kPer] = {};
-    float sum = 0.f;
-    for (int i = c; i <= last; ++i) {
-        if (i > c && !P.headers[i].head)
-            continue;
-        const float *rec = record(i);
-        const float l = rec[(size_t)(D + 1) * 2 * kRows + row];
-        if (l <= 0.f)
-            continue;
-        const float f = fast_exp2(rec[(size_t)D * 2 * kRows + row] - top);
-        sum = fmaf(f, l, sum);
+    float sum = 0.f, top = -INFINITY;
+    for (int i0 = c; i0 <= hd.last; i0 += kBatch) {
+        float m[kBatch], l[kBatch];
+        float4 o[kBatch][kPer];
 #pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-            const float4 o = *reinterpret_cast<const float4 *>(rec + ((size_t)(warp * kPer + x) * (2 * kRows) + row) * 4);
-            acc[x].x = fmaf(f, o.x, acc[x].x);
-            acc[x].y = fmaf(f, o.y, acc[x].y);
-            acc[x].z = fmaf(f, o.z, acc[x].z);
-            acc[x].w = fmaf(f, o.w, acc[x].w);
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = min(i0 + b, hd.last);
+            const float *rec = P.records + (size_t)(i == c ? 2 * c + 1 : 2 * i) * record_floats(D);
+            const bool part = i0 + b <= hd.last && (i == c || P.headers[i].head);
+            m[b] = rec[(size_t)D * 2 * kRows + row];
+            l[b] = rec[(size_t)(D + 1) * 2 * kRows + row];
+#pragma unroll
+            for (int x = 0; x < kPer; ++x)
+                o[b][x] = *reinterpret_cast<const float4 *>(rec + ((size_t)(warp * kPer + x) * (2 * kRows) + row) * 4);
+            if (!part)
+                l[b] = 0.f;
+        }
+        float most = top;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            most = l[b] > 0.f ? fmaxf(most, m[b]) : most;
+        const float f0 = top > -INFINITY ? fast_exp2(top - most) : 0.f;
+        top = most;
+        sum *= f0;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x)
+            acc[x] = make_float4(acc[x].x * f0, acc[x].y * f0, acc[x].z * f0, acc[x].w * f0);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (!(l[b] > 0.f))
+                continue;
+            const float f = fast_exp2(m[b] - top);
+            sum = fmaf(f, l[b], sum);
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+                acc[x].x = fmaf(f, o[b][x].x, acc[x].x);
+                acc[x].y = fmaf(f, o[b][x].y, acc[x].y);
+                acc[x].z = fmaf(f, o[b][x].z, acc[x].z);
+                acc[x].w = fmaf(f, o[b][x].w, acc[x].w);
+            }
         }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -1146,22 +1178,27 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &P
         if (dev < 64)
             __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELAXED);
     }
-    span_attn_kernel<T, D, Q8><<<ctas, kThreads, smem_bytes<D, Q8>(), stream>>>(tk, tv, P);
-    e = cudaGetLastError();
-    // no sequence has the keys of a unit that may be cut (the second launch costs
-    // 3 us of a small call)
-    if (e != cudaSuccess || max_keys <= Geo<D, Q8>::WHOLE * Geo<D, Q8>::KT)
-        return e;
+    // Programmatic dependents: the set-up of a kernel runs while the one before it on
+    // the stream ends, and each waits for that one before it reads anything.
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas * 8);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<D, Q8>();
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, span_join_kernel<T, D>, P, ctas);
+    e = cudaLaunchKernelEx(&cfg, span_attn_kernel<T, D, Q8>, tk, tv, P);
+    // no sequence has the keys of a unit that may be cut (the second launch costs
+    // 3 us of a small call)
+    if (e != cudaSuccess || max_keys <= Geo<D, Q8>::WHOLE * Geo<D, Q8>::KT)
+        return e;
+    cfg.gridDim = dim3(ctas * 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, span_join_kernel<T, D>, P);
 }
 
 }  // namespace span
