@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.q_ready[t], kTileWarps);
-            mbar_init(&sm.s_full[t], 1);
+            mbar_init(&sm.s_full[t], SCALED ? 2 : 1);
             mbar_init(&sm.s_free[t], kTileWarps);
             mbar_init(&sm.p_full[t], kTileWarps);
             mbar_init(&sm.pv_done[t], 1);
@@ -491,7 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool busy = __any_sync(0xffffffffu, pos >= 0 || (rt < qt && up->i0 + t * qt + rt < up->n));
             float m = -INFINITY, l = 0.f;
             for (int j = t0; ok && j < end; ++j, ++count) {
-                const int stage = (vtile + j - t0) % ST;
                 if (!warp_wait(&sm.s_full[t], (uint32_t)count & 1u)) {
                     ok = false;
                     break;
@@ -510,13 +509,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < KT; c += 32)
                     tc::tmem_ld32(s_addr + c, *reinterpret_cast<float(*)[32]>(&sv[c]));
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < KT; c += 32)
-                    hold32(&sv[c]);
-                tc::fence_before_sync();
-                arrive(&sm.s_free[t]);
-
                 // scale of the scores and exponent of the values, by group of keys
                 constexpr int NG = SCALED ? 4 : 1, GK = KT / NG;
                 float sc[NG], ev[NG];
@@ -524,19 +516,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sc[0] = row_scale;
                 ev[0] = 0.f;
                 if (SCALED) {
-                    const int tile = vtile + j - t0;
-                    if (!warp_wait(&sm.v_ready[stage], (uint32_t)(tile / ST) & 1u)) {
-                        ok = false;
-                        break;
-                    }
+                    const int tile = vtile + j - t0, stage = tile % ST;
+                    const float4 v4 = *reinterpret_cast<const float4 *>(sm.ev[stage]);
+                    const float4 k4 = Q8 ? *reinterpret_cast<const float4 *>(sm.ek[tile % kMeta])
+                                         : make_float4(1.f, 1.f, 1.f, 1.f);
+                    ev[0] = v4.x, ev[NG / 4] = v4.y, ev[NG / 2] = v4.z, ev[NG - 1] = v4.w;
+                    const float k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        ev[g] = sm.ev[stage][g];
-                        sc[g] = Q8 ? fmaxf(row_scale * sm.ek[tile % kMeta][g], kTinyScale) : row_scale;
-                    }
+                    for (int g = 0; g < NG; ++g)
+                        sc[g] = Q8 ? fmaxf(row_scale * k[g], kTinyScale) : row_scale;
                     if (Q8)
                         loaded = sm.loaded[tile % kMeta];
                 }
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < KT; c += 32)
+                    hold32(&sv[c]);
+                tc::fence_before_sync();
+                arrive(&sm.s_free[t]);
+
                 const int base = j * KT;
                 if (base + KT - 1 > low) {
                     const int lim = pos - base;
@@ -921,6 +919,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             b_lo + (((kk >> 2) * (KT * kPanel) + (kk & 3) * 32) >> 4),
                                             (uint32_t)(dk >> 32), idesc_s, kk > 0);
                         tc::mma_commit_warp(&sm.s_full[t]);
+                        if (SCALED) {
+                            // the softmax reads the exponents of this tile's groups, too: they are
+                            // in place when its V is
+                            ok = warp_wait(&sm.v_ready[ks], kpar);
+                            if (!ok)
+                                return;
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(&sm.s_full[t]);
+                        }
                         ++count;
                     }
                     tc::mma_commit_warp(&sm.k_empty[ks]);
