@@ -131,6 +131,11 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
+    try:
+        if t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -144,14 +149,15 @@ def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
 
 # The current stream's handle without the Python object around it (3 us a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
-    if getattr(_capture, "on", False):
+    if _capture.on:
         return _STREAM_SLOT
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -161,12 +167,17 @@ def _stream(stream) -> int:
 # While a call is prepared, the entry points record their marshalled arguments
 # instead of calling the library, and the stream argument is a slot filled in
 # at each run.
-_capture = threading.local()
+class _Capture(threading.local):
+    on = False
+    record = None
+
+
+_capture = _Capture()
 _STREAM_SLOT = object()
 
 
 def _invoke(name: str, *args) -> int:
-    if getattr(_capture, "on", False):
+    if _capture.on:
         _capture.record = (name, args)
         return NS_OK
     return getattr(lib(), name)(*args)
@@ -403,11 +414,9 @@ def ns_kv_append_paged_attn_decode_q8_0(q, k_new, v_new, slot_mapping, k_codes, 
 def _rows(t: torch.Tensor, name: str, dtype):
     """Pointer of [T, H, D] rows that are dense themselves, and elements from one to the next
     (with no next row, the row's own width)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     n, h, d = t.shape
     s0, s1, s2 = t.stride()

@@ -53,6 +53,8 @@ constexpr int kMaxTokens = 256;
 template <typename T, bool Q8>
 __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a, int tokens, int row_chunks, int head_chunks)
 {
+    grid_dependency_wait();
+    grid_launch_dependents();
     __shared__ long long src[kMaxTokens];  // first pool row of the token (its kv head 0), or -1
     const int t0 = blockIdx.x * tokens, nt = min(tokens, a.total_tokens - t0);
     if ((int)threadIdx.x < nt) {
@@ -126,8 +128,17 @@ cudaError_t launch_kv_gather(const GatherArgs &a, bool q8, cudaStream_t stream)
     const unsigned grid = (unsigned)((a.total_tokens + tokens - 1) / tokens);
     auto kern = !q8 ? kv_gather_kernel<F16, false>
                     : a.dtype == NS_BF16 ? kv_gather_kernel<BF16, true> : kv_gather_kernel<F16, true>;
-    kern<<<grid, kThreads, 0, stream>>>(a, tokens, row_chunks, head_chunks);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    // its set-up overlaps the end of the kernel before, which it waits for
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, tokens, row_chunks, head_chunks);
 }
 
 }  // namespace ns
