@@ -222,10 +222,25 @@ __device__ __forceinline__ float pow2(int e)  // 2^e, -126 <= e <= 127
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// A bounded wait of a whole warp: its lanes leave it together, and agree.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+// Waits and arrivals of a whole warp, with as few branches as possible: a taken branch
+// costs a lone warp some 25 clocks, and these are in everyone's inner loop.
+
+// Bounded wait; the warp's lanes go on together, `ok` falls when the time is up.
+__device__ __forceinline__ void warp_wait(uint64_t *bar, uint32_t parity, bool &ok)
 {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+    const bool done = mbar_try_wait(bar, parity);
+    if (__builtin_expect(__any_sync(0xffffffffu, !done), 0))
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0 && ok;
+}
+
+// One arrival for the warp, through an elected lane.  What the lanes wrote to shared
+// memory needs a __syncwarp before.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar)
+{
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(smem_addr(bar))
+        : "memory");
 }
 
 // The registers are read behind this point (after a wait for a TMEM load).
@@ -403,17 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     int unit_no = 0;
     auto wait_unit = [&]() -> const Unit & {
         const int i = unit_no % kUnits;
-        if (!warp_wait(&sm.u_full[i], (uint32_t)(unit_no / kUnits) & 1u)) {
-            ok = false;
+        warp_wait(&sm.u_full[i], (uint32_t)(unit_no / kUnits) & 1u, ok);
+        if (!ok)
             return sm.no_unit;
-        }
         ++unit_no;
         return sm.unit[i];
     };
     auto release_unit = [&](int no) {
         __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&sm.u_empty[no % kUnits]);
+        warp_arrive(&sm.u_empty[no % kUnits]);
     };
     auto next_unit = [&]() -> Unit {
         const Unit u = wait_unit();
@@ -436,12 +449,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         int count = 0;   // key tiles of this query tile so far
         int vtile = 0;   // key tiles of the CTA before this unit
         float row_scale = P.scale_log2;
-        auto arrive = [&](uint64_t *bar) {  // one arrival for the warp's work so far
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar);
-        };
-
         // Lay row r of the unit's query tile into shared memory.
         auto lay_q = [&](const Unit &u) {
             const int tok = u.i0 + t * qt + rt;
@@ -476,34 +483,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4 *>(qs + (c >> 3) * (kRows * kPanel) + (((c & 7) ^ (r & 7)) << 4)) = w[c];
             }
             fence_async_smem();
-            arrive(&sm.q_ready[t]);
+            __syncwarp();
+            warp_arrive(&sm.q_ready[t]);
         };
 
-        const Unit *up = &wait_unit();
-        if (up->t1 >= 0 && min(up->t1, tiles_of<KT>(*up, t, qt)) > up->t0)
-            lay_q(*up);
-        while (up->t1 >= 0) {
-            const int t0 = up->t0, end = min(up->t1, tiles_of<KT>(*up, t, qt));
+        const Unit *now = &wait_unit();
+        if (now->t1 >= 0 && min(now->t1, tiles_of<KT>(*now, t, qt)) > now->t0)
+            lay_q(*now);
+        while (now->t1 >= 0) {
+            const int t0 = now->t0, end = min(now->t1, tiles_of<KT>(*now, t, qt));
             // last key of the row, of the tile's first row
-            const int low = up->L - up->n + up->i0 + t * qt;
-            const int pos = rt < qt && up->i0 + t * qt + rt < up->n ? low + rt : -1;
+            const int low = now->L - now->n + now->i0 + t * qt;
+            const int pos = rt < qt && now->i0 + t * qt + rt < now->n ? low + rt : -1;
             // rows are independent: 32 rows without a token need no weights
-            const bool busy = __any_sync(0xffffffffu, pos >= 0 || (rt < qt && up->i0 + t * qt + rt < up->n));
+            const bool busy = __any_sync(0xffffffffu, pos >= 0 || (rt < qt && now->i0 + t * qt + rt < now->n));
             float m = -INFINITY, l = 0.f;
-            for (int j = t0; ok && j < end; ++j, ++count) {
-                if (!warp_wait(&sm.s_full[t], (uint32_t)count & 1u)) {
-                    ok = false;
-                    break;
-                }
-                if (!busy) {
-                    arrive(&sm.s_free[t]);
-                    if (count > 0 && !warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    arrive(&sm.p_full[t]);
-                    continue;
-                }
+            for (int j = t0; ok && !busy && j < end; ++j, ++count) {
+                warp_wait(&sm.s_full[t], (uint32_t)count & 1u, ok);
+                warp_arrive(&sm.s_free[t]);
+                warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u, ok);
+                warp_arrive(&sm.p_full[t]);
+            }
+            for (int j = t0; ok && busy && j < end; ++j, ++count) {
+                warp_wait(&sm.s_full[t], (uint32_t)count & 1u, ok);
                 tc::fence_after_sync();
                 float sv[KT];
 #pragma unroll
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < KT; c += 32)
                     hold32(&sv[c]);
                 tc::fence_before_sync();
-                arrive(&sm.s_free[t]);
+                warp_arrive(&sm.s_free[t]);
 
                 const int base = j * KT;
                 if (base + KT - 1 > low) {
@@ -563,15 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * sc[0];
                     }
                 }
-                float m_new = m, alpha = 1.f;
-                bool moved = false;
-                if (top > m + kSlack) {
-                    m_new = top;
-                    alpha = fast_exp2(m - top);  // 0 at the first tile
-                    moved = j > t0;
-                    l *= alpha;
-                }
-                m = m_new;
+                // the reference moves to a score that passes it by more than the slack
+                const bool up = top > m + kSlack;
+                const float alpha = fast_exp2(up ? m - top : 0.f);  // 0 at the first tile
+                const bool moved = up && j > t0;
+                l *= alpha;
+                m = up ? top : m;
                 const float ref = m > -INFINITY ? m : 0.f;
                 uint32_t pk[KT / 2];
 #pragma unroll
@@ -591,10 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 
                 // P is free, and O at rest, once the previous tile's value products are done
-                if (count > 0 && !warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u)) {
-                    ok = false;
-                    break;
-                }
+                warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u, ok);
                 tc::fence_after_sync();
                 if (__any_sync(0xffffffffu, moved)) {
                     const float f = moved ? alpha : 1.f;
@@ -615,9 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::tmem_st32(p_addr + c, *reinterpret_cast<const uint32_t(*)[32]>(&pk[c]));
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
-                arrive(&sm.p_full[t]);
+                warp_arrive(&sm.p_full[t]);
             }
-            const Unit &u = *up;
+            const Unit &u = *now;
             vtile += u.t1 - t0;
 
             // the next unit's Q, so that its first scores are under way during the epilogue
@@ -630,8 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tok = u.i0 + t * qt + rt;
             const bool on = rt < qt && tok < u.n;
             const bool any = end > t0;
-            if (ok && any && !warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u))
-                ok = false;
+            if (any)
+                warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u, ok);
             tc::fence_after_sync();
             if (u.rec < 0) {
                 const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -679,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::fence_before_sync();
             release_unit(this_no);
-            up = next;
+            now = next;
         }
         if (!ok)
             raise_status(a.status, NS_DEV_WAIT_TIMEOUT);
@@ -699,10 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t par = (uint32_t)(tile / ST) & 1u;
                 const bool live = j * KT + key < u.L;  // a row behind the last key is zero
                 if (!Q8) {
-                    if (!warp_wait(&sm.v_full[stage], par)) {
-                        ok = false;
-                        break;
-                    }
+                    warp_wait(&sm.v_full[stage], par, ok);
                     uint8_t *row = sm.v[stage] + panel;
                     if (BF) {
                         uint4 x[8];
@@ -728,14 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fence_async_smem();
                     }
                     __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&sm.v_ready[stage]);
+                    warp_arrive(&sm.v_ready[stage]);
                 } else {
                     const int rs = tile % GG::RAW;
-                    if (!warp_wait(&sm.raw_full[rs], (uint32_t)(tile / GG::RAW) & 1u)) {
-                        ok = false;
-                        break;
-                    }
+                    warp_wait(&sm.raw_full[rs], (uint32_t)(tile / GG::RAW) & 1u, ok);
                     const uint8_t *raw = sm.raw[rs];
                     const uint32_t loaded = sm.raw_loaded[rs];
                     const bool have = live && ((loaded >> (key / 16)) & 1u);
@@ -758,10 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float2 ds = unpack2<F16>(d[x]);
                         const float f = pow2(22 - e);
                         const __half2 dd[2] = {__float2half2_rn(ds.x * f), __float2half2_rn(ds.y * f)};
-                        if (!warp_wait(x == 0 ? &sm.k_empty[stage] : &sm.v_empty[stage], par ^ 1u)) {
-                            ok = false;
-                            break;
-                        }
+                        warp_wait(x == 0 ? &sm.k_empty[stage] : &sm.v_empty[stage], par ^ 1u, ok);
                         if (lane == 0) {
                             if (x == 0)
                                 sm.ek[tile % kMeta][group] = pow2(e - 22);
@@ -783,11 +769,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         fence_async_smem();
                         __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(x == 0 ? &sm.k_ready[stage] : &sm.v_ready[stage]);
+                        warp_arrive(x == 0 ? &sm.k_ready[stage] : &sm.v_ready[stage]);
                     }
-                    if (lane == 0)
-                        mbar_arrive(&sm.raw_empty[rs]);
+                    warp_arrive(&sm.raw_empty[rs]);
                 }
             }
         }
@@ -896,79 +880,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tm = uniform(tmem), q_lo = uniform((uint32_t)dk + (smem_addr(sm.q[t]) >> 4)),
                            k_lo = uniform((uint32_t)dk + (smem_addr(sm.k[0]) >> 4)),
                            v_lo = uniform((uint32_t)dv + (smem_addr(sm.v[0]) >> 4));
-            uint32_t units = 0, count = 0;
+            uint32_t units = 0, count = 0, done = 0;
             uint32_t ks = 0, kpar = 0, vs = 0, vpar = 0;  // stages of K and V
             for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
-                const int end = min(u.t1, tiles_of<KT>(u, t, qt));
-                // a tile without rows for this key tile still hands its stages back, once
-                // they hold it, so that both tiles count the same uses
-                auto scores = [&](int j) {
-                    ok = warp_wait(&sm.k_ready[ks], kpar);
-                    if (!ok)
-                        return;
-                    if (j < end) {
-                        ok = (j > u.t0 || warp_wait(&sm.q_ready[t], units & 1u)) &&
-                             (count == 0 || warp_wait(&sm.s_free[t], (count - 1) & 1u));
-                        if (!ok)
-                            return;
-                        tc::fence_after_sync();
-                        const uint32_t b_lo = uniform(k_lo + ks * (GG::TILE >> 4));
+                const int n = u.t1 - u.t0, mine = min(u.t1, tiles_of<KT>(u, t, qt)) - u.t0;
+                if (mine > 0)
+                    warp_wait(&sm.q_ready[t], units++ & 1u, ok);
+                // a tile without rows for a key tile still hands its stages back, once they
+                // hold it, so that both tiles count the same uses
+                for (int i = 0; ok && i <= n; ++i) {
+                    if (i < n) {
+                        warp_wait(&sm.k_ready[ks], kpar, ok);
+                        if (i < mine) {
+                            warp_wait(&sm.s_free[t], (count - 1) & 1u, ok);
+                            tc::fence_after_sync();
+                            const uint32_t b_lo = uniform(k_lo + ks * (GG::TILE >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            tc::mma_ss_warp(tm + t * KT, q_lo + (((kk >> 2) * (kRows * kPanel) + (kk & 3) * 32) >> 4),
-                                            b_lo + (((kk >> 2) * (KT * kPanel) + (kk & 3) * 32) >> 4),
-                                            (uint32_t)(dk >> 32), idesc_s, kk > 0);
-                        tc::mma_commit_warp(&sm.s_full[t]);
-                        if (SCALED) {
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                tc::mma_ss_warp(tm + t * KT, q_lo + (((kk >> 2) * (kRows * kPanel) + (kk & 3) * 32) >> 4),
+                                                b_lo + (((kk >> 2) * (KT * kPanel) + (kk & 3) * 32) >> 4),
+                                                (uint32_t)(dk >> 32), idesc_s, kk > 0);
+                            tc::mma_commit_warp(&sm.s_full[t]);
+                            ++count;
+                        }
+                        tc::mma_commit_warp(&sm.k_empty[ks]);
+                        if (SCALED && i < mine) {
                             // the softmax reads the exponents of this tile's groups, too: they are
                             // in place when its V is
-                            ok = warp_wait(&sm.v_ready[ks], kpar);
-                            if (!ok)
-                                return;
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(&sm.s_full[t]);
+                            warp_wait(&sm.v_ready[ks], kpar, ok);
+                            warp_arrive(&sm.s_full[t]);
                         }
-                        ++count;
+                        const bool wrap = ks == ST - 1;
+                        ks = wrap ? 0 : ks + 1;
+                        kpar ^= wrap ? 1u : 0u;
                     }
-                    tc::mma_commit_warp(&sm.k_empty[ks]);
-                    if (++ks == ST) {
-                        ks = 0;
-                        kpar ^= 1u;
-                    }
-                };
-                if (u.t0 < u.t1)
-                    scores(u.t0);
-                uint32_t done = count - (end > u.t0 ? 1u : 0u);  // value products so far
-                for (int j = u.t0; ok && j < u.t1; ++j) {
-                    if (j + 1 < u.t1)
-                        scores(j + 1);
-                    if (!ok)
-                        break;
-                    ok = warp_wait(&sm.v_ready[vs], vpar);
-                    if (!ok)
-                        break;
-                    if (j < end) {
-                        ok = warp_wait(&sm.p_full[t], done & 1u);
-                        if (!ok)
-                            break;
-                        ++done;
-                        tc::fence_after_sync();
-                        const uint32_t b_lo = uniform(v_lo + vs * (GG::TILE >> 4));
-                        const bool more = uniform(j > u.t0 ? 1u : 0u) != 0;
+                    if (i > 0) {
+                        warp_wait(&sm.v_ready[vs], vpar, ok);
+                        if (i <= mine) {
+                            warp_wait(&sm.p_full[t], done & 1u, ok);
+                            ++done;
+                            tc::fence_after_sync();
+                            const uint32_t b_lo = uniform(v_lo + vs * (GG::TILE >> 4));
+                            const bool more = uniform(i > 1 ? 1u : 0u) != 0;
 #pragma unroll
-                        for (int kk = 0; kk < KT / 16; ++kk)
-                            tc::mma_ts_warp(tm + GG::O + t * D, tm + GG::P + t * (KT / 2) + kk * 8,
-                                            b_lo + ((kk * 16 * kPanel) >> 4), (uint32_t)(dv >> 32), idesc_o, kk > 0 || more);
-                        tc::mma_commit_warp(&sm.pv_done[t]);
-                    }
-                    tc::mma_commit_warp(&sm.v_empty[vs]);
-                    if (++vs == ST) {
-                        vs = 0;
-                        vpar ^= 1u;
+                            for (int kk = 0; kk < KT / 16; ++kk)
+                                tc::mma_ts_warp(tm + GG::O + t * D, tm + GG::P + t * (KT / 2) + kk * 8,
+                                                b_lo + ((kk * 16 * kPanel) >> 4), (uint32_t)(dv >> 32), idesc_o,
+                                                kk > 0 || more);
+                            tc::mma_commit_warp(&sm.pv_done[t]);
+                        }
+                        tc::mma_commit_warp(&sm.v_empty[vs]);
+                        const bool wrap = vs == ST - 1;
+                        vs = wrap ? 0 : vs + 1;
+                        vpar ^= wrap ? 1u : 0u;
                     }
                 }
-                units += end > u.t0 ? 1u : 0u;
             }
             if (!ok && lane == 0)
                 raise_status(a.status, NS_DEV_WAIT_TIMEOUT);
@@ -983,11 +949,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int no = 0;
             auto announce = [&](const Unit &u) {
                 const int i = no % kUnits;
-                if (!warp_wait(&sm.u_empty[i], ((uint32_t)(no / kUnits) & 1u) ^ 1u)) {
-                    ok = false;
-                    return;
-                }
-                if (lane == 0) {
+                warp_wait(&sm.u_empty[i], ((uint32_t)(no / kUnits) & 1u) ^ 1u, ok);
+                if (lane == 0 && ok) {
                     sm.unit[i] = u;
                     mbar_arrive(&sm.u_full[i]);
                 }
