@@ -233,6 +233,14 @@ __device__ __forceinline__ void warp_wait(uint64_t *bar, uint32_t parity, bool &
         ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0 && ok;
 }
 
+// Two or three waits at the price of one while all of them are over.
+__device__ __forceinline__ void warp_wait(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb, bool &ok)
+{
+    const bool da = mbar_try_wait(a, pa), db = mbar_try_wait(b, pb);
+    if (__builtin_expect(__any_sync(0xffffffffu, !(da && db)), 0))
+        ok = __all_sync(0xffffffffu, mbar_wait(a, pa) && mbar_wait(b, pb)) != 0 && ok;
+}
+
 // One arrival for the warp, through an elected lane.  What the lanes wrote to shared
 // memory needs a __syncwarp before.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar)
@@ -880,60 +888,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tm = uniform(tmem), q_lo = uniform((uint32_t)dk + (smem_addr(sm.q[t]) >> 4)),
                            k_lo = uniform((uint32_t)dk + (smem_addr(sm.k[0]) >> 4)),
                            v_lo = uniform((uint32_t)dv + (smem_addr(sm.v[0]) >> 4));
-            uint32_t units = 0, count = 0, done = 0;
+            uint32_t units = 0, count = 0;                // units and scores so far
             uint32_t ks = 0, kpar = 0, vs = 0, vpar = 0;  // stages of K and V
+            auto next_stage = [](uint32_t &stage, uint32_t &parity) {
+                const bool wrap = stage == ST - 1;
+                stage = wrap ? 0 : stage + 1;
+                parity ^= wrap ? 1u : 0u;
+            };
             for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
-                const int n = u.t1 - u.t0, mine = min(u.t1, tiles_of<KT>(u, t, qt)) - u.t0;
+                const int n = uniform(u.t1 - u.t0),
+                          mine = uniform(max(0, min(u.t1, tiles_of<KT>(u, t, qt)) - u.t0));
                 if (mine > 0)
                     warp_wait(&sm.q_ready[t], units++ & 1u, ok);
-                // a tile without rows for a key tile still hands its stages back, once they
-                // hold it, so that both tiles count the same uses
-                for (int i = 0; ok && i <= n; ++i) {
-                    if (i < n) {
-                        warp_wait(&sm.k_ready[ks], kpar, ok);
-                        if (i < mine) {
-                            warp_wait(&sm.s_free[t], (count - 1) & 1u, ok);
-                            tc::fence_after_sync();
-                            const uint32_t b_lo = uniform(k_lo + ks * (GG::TILE >> 4));
+                for (int i = 0; ok && i <= mine && mine > 0; ++i) {
+                    if (i < mine) {
+                        // S of tile i, once the scores before were read
+                        warp_wait(&sm.k_ready[ks], kpar, &sm.s_free[t], (count - 1) & 1u, ok);
+                        tc::fence_after_sync();
+                        const uint32_t b_lo = uniform(k_lo + ks * (GG::TILE >> 4));
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                tc::mma_ss_warp(tm + t * KT, q_lo + (((kk >> 2) * (kRows * kPanel) + (kk & 3) * 32) >> 4),
-                                                b_lo + (((kk >> 2) * (KT * kPanel) + (kk & 3) * 32) >> 4),
-                                                (uint32_t)(dk >> 32), idesc_s, kk > 0);
-                            tc::mma_commit_warp(&sm.s_full[t]);
-                            ++count;
-                        }
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc::mma_ss_warp(tm + t * KT, q_lo + (((kk >> 2) * (kRows * kPanel) + (kk & 3) * 32) >> 4),
+                                            b_lo + (((kk >> 2) * (KT * kPanel) + (kk & 3) * 32) >> 4),
+                                            (uint32_t)(dk >> 32), idesc_s, kk > 0);
+                        tc::mma_commit_warp(&sm.s_full[t]);
                         tc::mma_commit_warp(&sm.k_empty[ks]);
-                        if (SCALED && i < mine) {
+                        ++count;
+                        if (SCALED) {
                             // the softmax reads the exponents of this tile's groups, too: they are
                             // in place when its V is
                             warp_wait(&sm.v_ready[ks], kpar, ok);
                             warp_arrive(&sm.s_full[t]);
                         }
-                        const bool wrap = ks == ST - 1;
-                        ks = wrap ? 0 : ks + 1;
-                        kpar ^= wrap ? 1u : 0u;
+                        next_stage(ks, kpar);
                     }
                     if (i > 0) {
-                        warp_wait(&sm.v_ready[vs], vpar, ok);
-                        if (i <= mine) {
-                            warp_wait(&sm.p_full[t], done & 1u, ok);
-                            ++done;
-                            tc::fence_after_sync();
-                            const uint32_t b_lo = uniform(v_lo + vs * (GG::TILE >> 4));
-                            const bool more = uniform(i > 1 ? 1u : 0u) != 0;
+                        // the values of tile i - 1, once its weights are there
+                        const uint32_t done = (i < mine ? count - 2 : count - 1) & 1u;
+                        warp_wait(&sm.v_ready[vs], vpar, &sm.p_full[t], done, ok);
+                        tc::fence_after_sync();
+                        const uint32_t b_lo = uniform(v_lo + vs * (GG::TILE >> 4));
+                        const bool more = uniform(i > 1 ? 1u : 0u) != 0;
 #pragma unroll
-                            for (int kk = 0; kk < KT / 16; ++kk)
-                                tc::mma_ts_warp(tm + GG::O + t * D, tm + GG::P + t * (KT / 2) + kk * 8,
-                                                b_lo + ((kk * 16 * kPanel) >> 4), (uint32_t)(dv >> 32), idesc_o,
-                                                kk > 0 || more);
-                            tc::mma_commit_warp(&sm.pv_done[t]);
-                        }
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            tc::mma_ts_warp(tm + GG::O + t * D, tm + GG::P + t * (KT / 2) + kk * 8,
+                                            b_lo + ((kk * 16 * kPanel) >> 4), (uint32_t)(dv >> 32), idesc_o,
+                                            kk > 0 || more);
+                        tc::mma_commit_warp(&sm.pv_done[t]);
                         tc::mma_commit_warp(&sm.v_empty[vs]);
-                        const bool wrap = vs == ST - 1;
-                        vs = wrap ? 0 : vs + 1;
-                        vpar ^= wrap ? 1u : 0u;
+                        next_stage(vs, vpar);
                     }
+                }
+                // key tiles that this query tile has no rows for: their stages go back once
+                // they are held, so that both query tiles count the same uses
+                for (int i = mine; ok && i < n; ++i) {
+                    warp_wait(&sm.k_ready[ks], kpar, &sm.v_ready[vs], vpar, ok);
+                    warp_arrive(&sm.k_empty[ks]);
+                    warp_arrive(&sm.v_empty[vs]);
+                    next_stage(ks, kpar);
+                    next_stage(vs, vpar);
                 }
             }
             if (!ok && lane == 0)
