@@ -49,7 +49,7 @@ constexpr int kRows = 128;       // rows of a query tile (MMA M)
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRegs = 128;       // registers a thread at launch; the warpgroups then share them out:
-constexpr int kSoftmaxRegs = 200, kConvertRegs = 64, kOtherRegs = 48;
+constexpr int kSoftmaxRegs = 184, kConvertRegs = 72, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kConvertRegs + kOtherRegs <= 4 * kRegs, "the shares fit the launch's registers");
 constexpr int kTileWarps = 4;    // softmax warps of a query tile
 constexpr int kConvertWarp = 8, kProducerWarp = 12, kProductWarp = 13, kPlanWarp = 15;  // 13, 14: query tiles 0, 1
