@@ -56,6 +56,12 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a,
     grid_dependency_wait();
     grid_launch_dependents();
     __shared__ long long src[kMaxTokens];  // first pool row of the token (its kv head 0), or -1
+    if (blockIdx.x == 0)  // entries out of order, also those that no row falls between
+        for (int s = threadIdx.x; s < a.num_seqs; s += kThreads) {
+            const int first = __ldg(a.start_loc + s), end = __ldg(a.start_loc + s + 1);
+            if (first < 0 || end < first || end > a.total_tokens)
+                raise_status(a.status, NS_DEV_BAD_QUERY_SPAN);
+        }
     const int t0 = blockIdx.x * tokens, nt = min(tokens, a.total_tokens - t0);
     if ((int)threadIdx.x < nt) {
         const int t = t0 + threadIdx.x;
@@ -64,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a,
         if (s >= 0) {
             const int first = __ldg(a.start_loc + s), end = __ldg(a.start_loc + s + 1), p = t - first;
             if (first < 0 || end > a.total_tokens) {
-                raise_status(a.status, NS_DEV_BAD_QUERY_SPAN);
+                // reported above
             } else if ((long long)(end - first) > (long long)a.max_blocks_per_seq * a.block_size) {
                 raise_status(a.status, NS_DEV_BAD_CONTEXT_LEN);
             } else {

@@ -73,7 +73,7 @@ struct Geo {
     static_assert(P + KT <= 512, "tensor memory");
     // cost of a unit besides its keys (laying out Q, filling the pipe, the epilogue)
     // and the least cost that a CTA is given, in keys
-    static constexpr int OVERHEAD = D == 64 ? 5 * KT / 2 : 7 * KT;
+    static constexpr int OVERHEAD = D == 128 ? 7 * KT : Q8 ? 5 * KT / 2 : 3 * KT;
     static constexpr int SHARE = OVERHEAD;  // at most one short unit a CTA while there are CTAs
     static constexpr int WHOLE = 4;  // units of so few key tiles are not cut
 };
@@ -251,6 +251,13 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar)
         : "memory");
 }
 
+// x 2^d, d <= 0: also where 2^d alone leaves fp32 (references of values 2^-60 and 2^60
+// in size differ by that much).
+__device__ __forceinline__ float times_pow2(float x, float d)
+{
+    return x * fast_exp2(fmaxf(d, -100.f)) * fast_exp2(fminf(d + 100.f, 0.f));
+}
+
 // The registers are read behind this point (after a wait for a TMEM load).
 __device__ __forceinline__ void hold32(float *v)
 {
@@ -310,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int KT = GG::KT, REG = GG::REG, ST = GG::STAGES;
     constexpr bool BF = T::code == NS_BF16;
     constexpr bool SCALED = Q8 || BF;  // V tiles carry an exponent
+    constexpr bool WIDE = BF && !Q8;   // of any size that bf16 has
     extern __shared__ unsigned char smem_raw[];
     Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -557,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < KT; ++c)
                         sv[c] = (loaded >> (c / 16)) & 1u ? sv[c] : -INFINITY;
                 }
+                float zmax[NG];  // largest score of each group of keys
                 float top = -INFINITY;
                 {
                     float tm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -567,19 +576,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tm[e] = max3(tm[e], sv[e * (KT / 4) + c], sv[e * (KT / 4) + c + 1]);
                     if (SCALED) {
 #pragma unroll
-                        for (int g = 0; g < NG; ++g)
-                            top = fmaxf(top, fmaf(tm[g], sc[g], ev[g]));
+                        for (int g = 0; g < NG; ++g) {
+                            zmax[g] = tm[g] * sc[g];
+                            top = fmaxf(top, zmax[g] + ev[g]);
+                        }
                     } else {
-                        top = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * sc[0];
+                        top = zmax[0] = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * sc[0];
                     }
                 }
                 // the reference moves to a score that passes it by more than the slack
                 const bool up = top > m + kSlack;
-                const float alpha = fast_exp2(up ? m - top : 0.f);  // 0 at the first tile
+                const float drop = up ? m - top : 0.f;
+                const float alpha = fast_exp2(drop);  // 0 at the first tile
                 const bool moved = up && j > t0;
-                l *= alpha;
+                l = WIDE ? times_pow2(l, drop) : l * alpha;
                 m = up ? top : m;
                 const float ref = m > -INFINITY ? m : 0.f;
+                if (WIDE) {
+                    // Values so small beside others that their weights would vanish in fp32
+                    // (zeros, above all) still count in the sum: their exponent is raised
+                    // until they do, which no output notices (2^-100 of it)
+                    float least = zmax[0] + ev[0];
+#pragma unroll
+                    for (int g = 1; g < NG; ++g)
+                        least = fminf(least, zmax[g] + ev[g]);
+                    if (__any_sync(0xffffffffu, least - ref < -100.f)) {
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+                            ev[g] = fmaxf(ev[g], ref - 100.f - fmaxf(zmax[g], -1e30f));
+                    }
+                }
                 uint32_t pk[KT / 2];
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
@@ -1104,9 +1130,9 @@ __global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ 
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
             most = l[b] > 0.f ? fmaxf(most, m[b]) : most;
-        const float f0 = top > -INFINITY ? fast_exp2(top - most) : 0.f;
+        const float drop = top > -INFINITY ? top - most : 0.f, f0 = fast_exp2(drop);
         top = most;
-        sum *= f0;
+        sum = times_pow2(sum, drop);
 #pragma unroll
         for (int x = 0; x < kPer; ++x)
             acc[x] = make_float4(acc[x].x * f0, acc[x].y * f0, acc[x].z * f0, acc[x].w * f0);
@@ -1115,7 +1141,7 @@ __global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ 
             if (!(l[b] > 0.f))
                 continue;
             const float f = fast_exp2(m[b] - top);
-            sum = fmaf(f, l[b], sum);
+            sum += times_pow2(l[b], m[b] - top);
 #pragma unroll
             for (int x = 0; x < kPer; ++x) {
                 acc[x].x = fmaf(f, o[b][x].x, acc[x].x);

@@ -121,6 +121,16 @@ def test_bad_device_data():
     assert np.array_equal(_gpu.to_bits(k)[:20], c.rows(c.k, 0, 20))
 
 
+@pytest.mark.parametrize("sl", [[0, 20, 10, 30], [0, 20, 60, 70], [-1, 5, 10, 20], [0, 60, 60, 61]])
+def test_entries_out_of_order_are_reported(sl):
+    c = Pool16([64, 64, 64], 2, 16, 64)
+    k = _gpu.to_dev(np.full((60, 2, 64), 0x1234, np.uint16), wl.F16)
+    nb.ns_kv_gather(_gpu.to_dev(c.k, wl.F16), _gpu.to_dev(c.v, wl.F16), _gpu.dev_ints(c.tables, np.int32),
+                    _gpu.dev_ints(sl, np.int32), k, k.clone())
+    torch.cuda.synchronize()
+    assert nb.ns_get_device_status() == 0x20
+
+
 def test_refusals():
     c = _span.Q8Cache(np.random.default_rng(0), [20])
     kc, ks, vc, vs, tables = c.dev()

@@ -141,6 +141,20 @@ def test_bf16_values_of_mixed_size():
     _gpu.assert_no_device_status()
 
 
+def test_values_that_vanish_beside_others_still_count_in_the_sum():
+    """Stretches of 2^-60, of zeros and of 2^60 in one prompt: the small ones add nothing
+    to a row that sees the large ones, but their weights divide it."""
+    p = Prompts([900], wl.BF16, 2, 1, 64, seed=19)
+    factor = torch.ones(900, device="cuda")
+    factor[:256], factor[256:420], factor[420:700] = 2.0 ** -60, 0.0, 2.0 ** 60
+    p.v.mul_(factor[:, None, None])
+    got = p.call().double().cpu()
+    want = _span.attend(p.q.cpu(), p.k.cpu(), p.v.cpu(), p.scale)
+    err = (got - want).norm(dim=-1) / want.norm(dim=-1)
+    assert float(err.max()) < 2.0 ** -8 + 4e-3  # as above
+    _gpu.assert_no_device_status()
+
+
 def test_large_scores():
     """Scores far apart: the running maximum moves by hundreds within a row."""
     p = Prompts([700, 128], wl.F16, 4, 2, 64, seed=10)
