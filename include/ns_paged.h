@@ -481,9 +481,12 @@ size_t ns_span_attn_workspace_bytes(int head_dim);
  *           entries break that is skipped and sets NS_DEV_BAD_QUERY_SPAN.
  *   out     [total_q_tokens][num_q_heads][head_dim], dense (written)
  * Strides are multiples of 8 and at least the heads' width.  head_dim is 64
- * or 128; num_q_heads / num_kv_heads is any whole number up to 64.  A value
- * that is infinite or NaN in k or v may reach every row of its own sequence,
- * and no other sequence.
+ * or 128; num_q_heads / num_kv_heads is any whole number up to 64.  NaN in a
+ * query, or in a key that a row sees, makes that row NaN; a value of v that is
+ * infinite or NaN may reach every row of its own sequence.  No sequence
+ * reaches another.  Softmax weights and v are rounded to fp16 (11 bits) for the
+ * value product, scaled by powers of two so that bf16 values of any size keep
+ * them; scores, sums and outputs are fp32 until the last rounding.
  */
 ns_status ns_prompt_attn(const void *q, const void *k, const void *v, const int32_t *query_start_loc,
                          const int32_t *key_start_loc, int num_seqs, int total_q_tokens,
@@ -502,8 +505,10 @@ ns_status ns_prompt_attn(const void *q, const void *k, const void *v, const int3
  * to 64.  A span longer than its context, negative or outside the query rows
  * is skipped (NS_DEV_BAD_QUERY_SPAN), as is a sequence whose context exceeds
  * its table row (NS_DEV_BAD_CONTEXT_LEN); a block id outside the pool sets
- * NS_DEV_BAD_BLOCK_ID and its tokens are left out.  workspace:
- * ns_span_attn_workspace_bytes(64).
+ * NS_DEV_BAD_BLOCK_ID and its tokens are left out.  The dequantised keys and
+ * values and the softmax weights are rounded to fp16 for the products, and so
+ * are bf16 queries, each scaled by a power of two first.  An infinite or NaN
+ * scale may reach every row of its own span.  workspace: ns_span_attn_workspace_bytes(64).
  */
 ns_status ns_paged_attn_prefill_q8_0(const void *q, const int32_t *query_start_loc, const void *k_codes,
                                      const void *k_scales, const void *v_codes, const void *v_scales,
@@ -565,7 +570,7 @@ ns_status ns_kv_gather_q8_0(const void *k_codes, const void *k_scales, const voi
  * distribution whatever the drafts were.  Products, sums and comparisons are
  * exact or carry at least 45 bits, so that a value next to a border decides
  * as it does in fp64.  A NaN probability counts as 0; without any positive
- * weight y = -1.
+ * weight y = -1.  vocab_size is at most 2^30.
  *
  *   target_probs  float [total_drafts+num_seqs][vocab_size], rows
  *                 target_row_stride elements apart (read)

@@ -203,6 +203,8 @@ ns_status ns_verify_drafts(const float *target_probs, const float *draft_probs, 
 {
     if (num_seqs < 0 || total_drafts < 0 || vocab_size < 1 || (long long)num_seqs + total_drafts > 0x7fffffffLL)
         return NS_ERR_INVALID_ARG;
+    if (vocab_size > (1 << 30))  // sums of positions are 32-bit
+        return NS_ERR_UNSUPPORTED;
     if (target_row_stride < vocab_size || (draft_probs && draft_row_stride < vocab_size))
         return NS_ERR_INVALID_ARG;
     if (num_seqs == 0)

@@ -93,3 +93,8 @@ def test_workspace_sizes(lib):
     assert lib.ns_span_attn_workspace_bytes(64) > 0 and lib.ns_span_attn_workspace_bytes(128) > 0
     assert lib.ns_span_attn_workspace_bytes(96) == 0
     assert ctypes.sizeof(ctypes.c_size_t) == 8
+
+
+def test_verify_refuses_a_vocabulary_beyond_its_positions(lib):
+    assert verify(lib, V=(1 << 30) + 1, ps=1 << 31, qs=1 << 31) == UNSUPPORTED
+    assert verify(lib, V=1 << 30, ps=1 << 31, qs=1 << 31, out=None) == INVALID
