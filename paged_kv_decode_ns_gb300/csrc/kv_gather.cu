@@ -45,13 +45,15 @@ __device__ __forceinline__ uint4 dequantise(uint4 w)
 // A CTA copies `tokens` packed rows.  Its first threads look their rows up (owner,
 // table entry) once; then a thread moves 16 bytes of K and of V (8 elements) at a
 // time, kBatch of them loaded before the first is stored.  Bound by memory once
-// the rows fill the GPU (a thread that looked its own row up and divided by the
-// heads for every 16 bytes reached 4.1 TB/s from q8_0 and 5.0 TB/s at 16 bits).
+// the rows fill the GPU: 256 sequences of q8_0 (381 MB) 62.7 us, 6.1 TB/s; 32 of
+// 16 bits at head_dim 128 (165 MB) 27.9 us, 5.9 TB/s.  (A thread that looked its own
+// row up and divided by the heads for every 16 bytes: 4.1 and 5.0 TB/s.)  Five CTAs an
+// SM cap the registers at 48: 66.0 us at four, 90.8 at six, which spills.
 constexpr int kBatch = 4;
 constexpr int kMaxTokens = 256;
 
 template <typename T, bool Q8>
-__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a, int tokens, int row_chunks, int head_chunks)
+__global__ void __launch_bounds__(kThreads, 5) kv_gather_kernel(const GatherArgs a, int tokens, int row_chunks, int head_chunks)
 {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -129,8 +131,9 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a,
 cudaError_t launch_kv_gather(const GatherArgs &a, bool q8, cudaStream_t stream)
 {
     const int head_chunks = a.head_dim / 8, row_chunks = a.num_kv_heads * head_chunks;
-    // a batch for every thread; at least eight rows, so that the look-ups are shared
-    const int tokens = std::min(kMaxTokens, std::max(8, kThreads * kBatch / row_chunks));
+    // a batch for every thread, two of the smaller reads from q8_0 (71 us with one);
+    // at least eight rows, so that the look-ups are shared
+    const int tokens = std::min(kMaxTokens, std::max(8, (q8 ? 2 : 1) * kThreads * kBatch / row_chunks));
     const unsigned grid = (unsigned)((a.total_tokens + tokens - 1) / tokens);
     auto kern = !q8 ? kv_gather_kernel<F16, false>
                     : a.dtype == NS_BF16 ? kv_gather_kernel<BF16, true> : kv_gather_kernel<F16, true>;

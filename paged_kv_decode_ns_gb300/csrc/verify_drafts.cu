@@ -5,12 +5,14 @@
 // w = max(p - q, 0), with no rejection from w = p_n: the smallest v whose
 // cumulative weight exceeds r * sum w.
 //
-// A cluster of CTAs per sequence: every CTA finds the first rejection itself (a
-// few gathers), then sums its contiguous slice of the one row that matters, a
-// contiguous run per warp.  The run sums go to every CTA of the cluster through
-// distributed shared memory; the CTA that owns the run the goal falls into reads
-// that run again and finds the token.  One pass over one row of p and one of q is
-// all the memory traffic, and bounds a large batch.
+// A CTA per sequence, a cluster of up to eight while sequences are few: every CTA
+// finds the first rejection itself (a few gathers), then sums its contiguous slice of
+// the one row that matters, a contiguous run per warp.  The run sums go to every CTA
+// of the cluster through distributed shared memory; the CTA that owns the run the
+// goal falls into reads that run again, a stretch a warp, and one warp narrows the
+// stretch down to the token.  One pass over one row of p and one of q is all the
+// memory traffic and bounds a large batch: 256 sequences of 151936 tokens (311 MB)
+// 54.8 us, 5.7 TB/s.  Four sequences take 11 us, a chain of dependent reads.
 //
 // Precision: neighbouring cumulative weights differ by single probabilities, so
 // fp32 sums would move the drawn token.  fp64 additions (about two a clock on an SM)
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     const int v0 = min(r1, r0 + warp * each), v1 = min(r1, v0 + each);
     Pair sum = {0.f, 0.f};
     int lastv = -1;
+#pragma unroll 8
     for (int v = v0 + lane; v < v1; v += 32) {
         const Pair w = r.at(v);
         sum = sum + w;
@@ -329,12 +332,18 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     const Place part = find(sh_part, kWarps, lane, before, [&](double) { return goal; });
     int token = sh_last;  // the run's sum in this order may fall short of the goal by its rounding
     if (part.at >= 0) {
+        // narrow the stretch down, a lane a segment: a row read once in parallel for each
+        // level (a warp that walked it in steps of 32 took 8 us at 600 tokens)
         double c = part.before;
-        const int e0 = min(r1, r0 + part.at * each), e1 = min(r1, e0 + each);
-        int lastp = -1;
-        bool found = false;
-        for (int v = e0; v < e1 && !found; v += 32) {
-            const double x = v + lane < e1 ? r.at(v + lane).value() : 0.0;
+        int a0 = min(r1, r0 + part.at * each), a1 = min(r1, a0 + each);
+        bool last = false;  // short of the goal: the last token with a weight
+        while (true) {
+            const int seg = (a1 - a0 + 31) / 32, s0 = min(a1, a0 + lane * seg), s1 = min(a1, s0 + seg);
+            Pair w = {0.f, 0.f};
+#pragma unroll 8
+            for (int v = s0; v < s1; ++v)
+                w = w + r.at(v);
+            const double x = w.value();
             double incl = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -344,16 +353,18 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
             }
             const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
             const unsigned over = __ballot_sync(0xffffffffu, x > 0.0 && c + incl > goal);
-            if (some != 0)
-                lastp = v + 31 - __clz(some);
-            if (over != 0) {
-                token = v + __ffs(over) - 1;
-                found = true;
+            if (some == 0)
+                break;
+            last |= over == 0;
+            const int at = last ? 31 - __clz(some) : __ffs(over) - 1;
+            c += __shfl_sync(0xffffffffu, incl - x, at);
+            a0 = __shfl_sync(0xffffffffu, s0, at);
+            a1 = __shfl_sync(0xffffffffu, s1, at);
+            if (seg <= 1) {
+                token = a0;
+                break;
             }
-            c += __shfl_sync(0xffffffffu, incl, 31);
         }
-        if (!found && lastp >= 0)
-            token = lastp;
     }
     if (lane == 0)
         out[acc] = token;
@@ -364,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t stream)
 {
     // CTAs for a sequence: as many as run at once (two on an SM), up to a cluster of
-    // eight.  256 sequences of 151936 tokens: one each 65.8 us, two 68.3, four 70.8;
-    // 33 of 50257: eight 12.6 us, clusters of sixteen 18.6.
+    // eight.  256 sequences of 151936 tokens: one each 54.8 us, two 60.2, four 67.1;
+    // 33 of 50257: eight 10.4 us, sixteen 6 us more.
     int cluster = kMaxCluster;
     while (cluster > 1 && (long long)a.num_seqs * cluster > 304)
         cluster /= 2;
