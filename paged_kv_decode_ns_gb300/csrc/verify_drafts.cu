@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     __shared__ int sh_state;  // 0: go on, 1: skip the sequence
     __shared__ int sh_accepted;
     __shared__ __align__(8) Pair sh_run[2][kMaxCluster * kWarps];  // run sums of the cluster, in order (one set a pass)
-    __shared__ Pair sh_part[kWarps];
+    __shared__ Pair sh_part[kWarps], sh_lane[kThreads];
     __shared__ Place sh_place;
     __shared__ double sh_goal;
     __shared__ int sh_last;
@@ -308,14 +308,16 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     const int r0 = (int)min((long long)a.vocab, (long long)run * per), r1 = (int)min((long long)a.vocab, (long long)r0 + per);
     const int each = (per + kWarps - 1) / kWarps;
     const int v0 = min(r1, r0 + warp * each), v1 = min(r1, v0 + each);
+    int seg = (each + 31) / 32, s0 = min(v1, v0 + lane * seg), s1 = min(v1, s0 + seg);  // a lane's part of it
     Pair sum = {0.f, 0.f};
     int lastv = -1;
 #pragma unroll 8
-    for (int v = v0 + lane; v < v1; v += 32) {
+    for (int v = s0; v < s1; ++v) {
         const Pair w = r.at(v);
         sum = sum + w;
         lastv = w.h > 0.f ? v : lastv;
     }
+    sh_lane[threadIdx.x] = sum;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         sum = sum + shfl_xor(sum, o);
@@ -332,17 +334,16 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     const Place part = find(sh_part, kWarps, lane, before, [&](double) { return goal; });
     int token = sh_last;  // the run's sum in this order may fall short of the goal by its rounding
     if (part.at >= 0) {
-        // narrow the stretch down, a lane a segment: a row read once in parallel for each
-        // level (a warp that walked it in steps of 32 took 8 us at 600 tokens)
+        // narrow the stretch down: the lanes' parts of it are summed already, then a lane
+        // a token of that part (a warp that walked the stretch in steps of 32 took 8 us
+        // at 600 tokens)
         double c = part.before;
         int a0 = min(r1, r0 + part.at * each), a1 = min(r1, a0 + each);
         bool last = false;  // short of the goal: the last token with a weight
+        Pair w = sh_lane[part.at * 32 + lane];
         while (true) {
-            const int seg = (a1 - a0 + 31) / 32, s0 = min(a1, a0 + lane * seg), s1 = min(a1, s0 + seg);
-            Pair w = {0.f, 0.f};
-#pragma unroll 8
-            for (int v = s0; v < s1; ++v)
-                w = w + r.at(v);
+            s0 = min(a1, a0 + lane * seg);
+            s1 = min(a1, s0 + seg);
             const double x = w.value();
             double incl = x;
 #pragma unroll
@@ -364,6 +365,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
                 token = a0;
                 break;
             }
+            seg = (a1 - a0 + 31) / 32;
+            w = {0.f, 0.f};
+            for (int v = a0 + lane * seg; v < min(a1, a0 + (lane + 1) * seg); ++v)
+                w = w + r.at(v);
         }
     }
     if (lane == 0)
