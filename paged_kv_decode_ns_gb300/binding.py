@@ -180,7 +180,7 @@ def _invoke(name: str, *args) -> int:
     if _capture.on:
         _capture.record = (name, args)
         return NS_OK
-    return getattr(lib(), name)(*args)
+    return getattr(_LIB or lib(), name)(*args)
 
 
 class PreparedCall:
@@ -213,10 +213,10 @@ class PreparedCall:
 def prepare(fn, *args, **kwargs) -> PreparedCall:
     """``fn`` (a launching entry point of this module: ns_kv_append,
     ns_paged_attn_decode, ns_kv_append_paged_attn_decode, ns_paged_attn_prefill,
-    a q8_0 one, ns_prompt_attn, ns_kv_gather or ns_verify_drafts) with these arguments, checked now and run by calling the
-    returned object.  It is what a serving loop that calls the same step on the
-    same buffers every iteration uses, so that a call costs the host one
-    foreign call."""
+    a q8_0 one, ns_prompt_attn, ns_kv_gather or ns_verify_drafts) with these
+    arguments, checked now and run by calling the returned object.  It is what a
+    serving loop that calls the same step on the same buffers every iteration
+    uses, so that a call costs the host one foreign call."""
     if kwargs.get("stream") is not None:
         raise ValueError("the stream is given to each run of a prepared call")
     _capture.on, _capture.record = True, None
@@ -411,14 +411,14 @@ def ns_kv_append_paged_attn_decode_q8_0(q, k_new, v_new, slot_mapping, k_codes, 
     _check(st, "ns_kv_append_paged_attn_decode_q8_0")
 
 
-def _rows(t: torch.Tensor, name: str, dtype):
+def _rows(t: torch.Tensor, name: str, dtype, shape):
     """Pointer of [T, H, D] rows that are dense themselves, and elements from one to the next
     (with no next row, the row's own width)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    n, h, d = t.shape
+    n, h, d = shape
     s0, s1, s2 = t.stride()
     if n and h and d and ((s2 != 1 and d > 1) or (s1 != d and h > 1)):
         raise ValueError(f"the rows of {name} must be dense [heads, head_dim]")
@@ -438,28 +438,28 @@ def ns_prompt_attn(q, k, v, query_start_loc, scale, out, workspace, key_start_lo
     """Causal attention of packed prompts: q [T, Hq, D] over k and v [T', Hkv, D] (rows any stride
     apart); sequence s owns the rows query_start_loc[s]..[s+1] (int32 [S+1]) of q, and of k and v
     unless key_start_loc says otherwise."""
-    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[2] != q.shape[2]:
+    rows, keys, starts = q.shape, k.shape, query_start_loc.shape
+    if len(rows) != 3 or len(keys) != 3 or v.shape != keys or keys[2] != rows[2]:
         raise ValueError("q must be [T, Hq, D], k and v [T', Hkv, D]")
-    T, hq, d = q.shape
-    Tk, hkv, _ = k.shape
-    if out.shape != q.shape:
+    T, hq, d = rows
+    Tk, hkv, _ = keys
+    if out.shape != rows:
         raise ValueError("out must have q's shape")
-    S = query_start_loc.shape[0] - 1
-    if query_start_loc.dim() != 1 or S < 0:
+    if len(starts) != 1 or starts[0] < 1:
         raise ValueError("query_start_loc must be [num_seqs + 1]")
+    S = starts[0] - 1
     if key_start_loc is None:
         if Tk != T:
             raise ValueError("k and v must have q's rows when key_start_loc is not given")
-    elif key_start_loc.shape != query_start_loc.shape:
+    elif key_start_loc.shape != starts:
         raise ValueError("key_start_loc must be [num_seqs + 1]")
     dtype = q.dtype
     dt = _dtype_code(q)
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", dtype), _rows(k, "k", dtype), _rows(v, "v", dtype)
-    st = _invoke("ns_prompt_attn", qp, kp, vp,
-                 _dev(query_start_loc, "query_start_loc", torch.int32),
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", dtype, rows), _rows(k, "k", dtype, keys), _rows(v, "v", dtype, keys)
+    st = _invoke("ns_prompt_attn", qp, kp, vp, _dev(query_start_loc, "query_start_loc", torch.int32),
                  None if key_start_loc is None else _dev(key_start_loc, "key_start_loc", torch.int32),
-                 S, T, Tk, hq, hkv, d, qs, ks, vs, float(scale), _dev(out, "out", dtype), _stream(stream), dt, _dev(workspace, "workspace", torch.uint8),
-                 workspace.numel())
+                 S, T, Tk, hq, hkv, d, qs, ks, vs, float(scale), _dev(out, "out", dtype), _stream(stream), dt,
+                 _dev(workspace, "workspace", torch.uint8), workspace.numel())
     _check(st, "ns_prompt_attn")
 
 
@@ -482,46 +482,51 @@ def ns_paged_attn_prefill_q8_0(q, query_start_loc, k_codes, k_scales, v_codes, v
     _check(st, "ns_paged_attn_prefill_q8_0")
 
 
-def _gather_shapes(nb, hkv, d, block_tables, start_loc, k_out, v_out):
-    if k_out.dim() != 3 or k_out.shape[1:] != (hkv, d) or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+def _gather_shapes(hkv, d, block_tables, start_loc, k_out, v_out):
+    """(num_seqs, max_blocks_per_seq, total_tokens, type) of a read-back."""
+    out, tables, dtype = k_out.shape, block_tables.shape, k_out.dtype
+    if len(out) != 3 or out[1] != hkv or out[2] != d or v_out.shape != out or v_out.dtype is not dtype:
         raise ValueError("k_out and v_out must be [total_tokens, Hkv, D]")
-    if block_tables.dim() != 2 or start_loc.shape != (block_tables.shape[0] + 1,):
+    if len(tables) != 2 or start_loc.shape != (tables[0] + 1,):
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq], start_loc [num_seqs + 1]")
+    return tables[0], tables[1], out[0], dtype
 
 
 def ns_kv_gather(k_pool, v_pool, block_tables, start_loc, k_out, v_out, stream=None):
     """Read the first start_loc[s+1]-start_loc[s] tokens of each sequence from the pools into the
     packed rows k_out/v_out [T, Hkv, D]."""
-    nb, hkv, bs, d = k_pool.shape
-    if v_pool.shape != k_pool.shape:
+    pool = k_pool.shape
+    nb, hkv, bs, d = pool
+    if v_pool.shape != pool:
         raise ValueError("shape mismatch")
-    _gather_shapes(nb, hkv, d, block_tables, start_loc, k_out, v_out)
-    st = _invoke("ns_kv_gather", _dev(k_pool, "k_pool", k_out.dtype), _dev(v_pool, "v_pool", k_out.dtype),
+    S, width, T, dtype = _gather_shapes(hkv, d, block_tables, start_loc, k_out, v_out)
+    st = _invoke("ns_kv_gather", _dev(k_pool, "k_pool", dtype), _dev(v_pool, "v_pool", dtype),
                  _dev(block_tables, "block_tables", torch.int32), _dev(start_loc, "start_loc", torch.int32),
-                 block_tables.shape[0], k_out.shape[0], hkv, d, bs, _dev(k_out, "k_out"),
-                 _dev(v_out, "v_out"), _stream(stream), block_tables.shape[1], nb, _dtype_code(k_out))
+                 S, T, hkv, d, bs, _dev(k_out, "k_out"), _dev(v_out, "v_out"), _stream(stream), width, nb,
+                 _dtype_code(k_out))
     _check(st, "ns_kv_gather")
 
 
 def ns_kv_gather_q8_0(k_codes, k_scales, v_codes, v_scales, block_tables, start_loc, k_out, v_out, stream=None):
     """ns_kv_gather from a q8_0 pool: the dequantised rows, rounded to k_out's type."""
     nb, hkv, bs, d, kc, ks, vc, vs = _q8_pools(k_codes, k_scales, v_codes, v_scales)
-    _gather_shapes(nb, hkv, d, block_tables, start_loc, k_out, v_out)
+    S, width, T, _ = _gather_shapes(hkv, d, block_tables, start_loc, k_out, v_out)
     st = _invoke("ns_kv_gather_q8_0", kc, ks, vc, vs, _dev(block_tables, "block_tables", torch.int32),
-                 _dev(start_loc, "start_loc", torch.int32), block_tables.shape[0], k_out.shape[0], hkv, d, bs,
-                 _dev(k_out, "k_out"), _dev(v_out, "v_out"), _stream(stream), block_tables.shape[1], nb,
-                 _dtype_code(k_out))
+                 _dev(start_loc, "start_loc", torch.int32), S, T, hkv, d, bs, _dev(k_out, "k_out"),
+                 _dev(v_out, "v_out"), _stream(stream), width, nb, _dtype_code(k_out))
     _check(st, "ns_kv_gather_q8_0")
 
 
-def _prob_rows(t, name):
-    if t.dtype != torch.float32:
+def _prob_rows(t, name, shape):
+    if t.dtype is not torch.float32:
         raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+    n, width = shape
+    s0, s1 = t.stride()
+    if n and width > 1 and s1 != 1:
         raise ValueError(f"the rows of {name} must be dense")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    return t.data_ptr(), (s0 if n > 1 else width)
 
 
 def ns_verify_drafts(target_probs, draft_probs, draft_tokens, draft_start_loc, accept_uniforms, sample_uniforms,
@@ -532,16 +537,19 @@ def ns_verify_drafts(target_probs, draft_probs, draft_tokens, draft_start_loc, a
     None (certain drafts), draft_tokens int32 [T], draft_start_loc int32 [S + 1], uniforms in [0, 1).
     Writes out_tokens int32 [T + S] (accepted drafts, the drawn token, then -1) and num_accepted [S].
     """
-    T, S = draft_tokens.shape[0], num_accepted.shape[0]
-    if target_probs.dim() != 2 or target_probs.shape[0] != T + S or out_tokens.shape != (T + S,):
+    target, drafts, accepted = target_probs.shape, draft_tokens.shape, num_accepted.shape
+    if len(drafts) != 1 or len(accepted) != 1:
+        raise ValueError("draft_tokens must be [num_drafts], num_accepted [num_seqs]")
+    T, S = drafts[0], accepted[0]
+    if len(target) != 2 or target[0] != T + S or out_tokens.shape != (T + S,):
         raise ValueError("target_probs must be [num_drafts + num_seqs, V], out_tokens [num_drafts + num_seqs]")
-    V = target_probs.shape[1]
+    V = target[1]
     if draft_probs is not None and draft_probs.shape != (T, V):
         raise ValueError("draft_probs must be [num_drafts, V]")
     if draft_start_loc.shape != (S + 1,) or accept_uniforms.shape != (T,) or sample_uniforms.shape != (S,):
         raise ValueError("draft_start_loc must be [S + 1], accept_uniforms [num_drafts], sample_uniforms [S]")
-    p, ps = _prob_rows(target_probs, "target_probs")
-    q, qs = (None, 0) if draft_probs is None else _prob_rows(draft_probs, "draft_probs")
+    p, ps = _prob_rows(target_probs, "target_probs", target)
+    q, qs = (None, 0) if draft_probs is None else _prob_rows(draft_probs, "draft_probs", (T, V))
     st = _invoke("ns_verify_drafts", p, q, _dev(draft_tokens, "draft_tokens", torch.int32),
                  _dev(draft_start_loc, "draft_start_loc", torch.int32),
                  _dev(accept_uniforms, "accept_uniforms", torch.float32),
