@@ -33,7 +33,24 @@
 // every value within 2^-29 of that exact.  Ev moves into the exponent of P,
 // 2^(z + Ev - m), with m a running reference of z + Ev; the sum takes it back out.
 // q8_0 tiles are dequantised to fp16 in the same way, with Ek for K in the score's
-// scale.
+// scale: code times scale has up to 18 bits, so K, V and P each lose up to
+// 2^-11 of themselves there.  An fp16 call over a q8_0 cache is then off by 4.2e-4 of its output,
+// half of it the output's own rounding; two products for each would undo that at
+// twice the tensor work.  Everything else (scores, sums, O) is fp32.
+//
+// What bounds it.  At head_dim 128 the tensor cores: 8192 tokens, 32 / 8 heads, 420 us,
+// 1.31 PFLOP/s, 71% of the measured peak.  At head_dim 64 the softmax: a pair of 128 x
+// 128 tiles takes ~2370 clocks, against 1050 of products and 1024 of exponentials; two
+// softmax warps a scheduler issue half of the time and wait on TMEM, barriers and
+// each other's use of the exponential unit for the rest (134 us for 8192 fp16 tokens of
+// 14 / 2 heads, 0.90 PFLOP/s; bf16 152 us, its exponents by group on top).  Short
+// calls: launch, the plan, one unit's chain of copy, product, softmax, product and
+// the join (four prompts of up to 200 tokens 10 us; 32 spans of drafts 19 us).
+//
+// Two softmax warpgroups a query tile (96 registers a thread) take 155 us where one
+// takes 136: the row no longer fits the registers.  Tiles read from TMEM 32 columns at a
+// time, the exponentials of the two tiles in turns, and a sleep between polls were
+// slower too or made no difference.
 #pragma once
 
 #include <algorithm>
