@@ -468,8 +468,8 @@ size_t ns_span_attn_workspace_bytes(int head_dim);
  * key_start_loc NULL means query_start_loc (every token sees itself and the
  * tokens before it).  More keys than queries put a prefix in front (rows read
  * back with ns_kv_gather); with fewer, the first n-L rows see no key and get
- * 0.  Rows of q behind the last sequence are not read, their rows of out not
- * written.
+ * 0.  Rows of q behind the last sequence do not count, their rows of out are
+ * not written.
  *
  *   q       [total_q_tokens][num_q_heads][head_dim], rows q_row_stride
  *           elements apart (read)

@@ -33,12 +33,20 @@ cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream
     P.group = a.num_q_heads / a.num_kv_heads;
     P.qt = span::kRows / P.group;
     P.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, span::kTinyScale);
-    P.q_flip = a.scale < 0.f ? 0x80008000u : 0u;
+    P.negate = a.scale < 0.f;
     P.headers = static_cast<span::Header *>(a.workspace);
     P.records = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + span::header_bytes());
-    CUtensorMap tk = {}, tv = {};
+    span::Maps tm = {};
+    {
+        // Q: [token][head][element], boxes of a group's heads of a query tile's tokens
+        const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.total_q_tokens};
+        const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)a.q_row_stride * 2};
+        const cuuint32_t box[3] = {64u, (cuuint32_t)P.group, (cuuint32_t)P.qt};
+        if (!encode_tensor_map(&tm.q, a.dtype, 3, a.q, dims, strides, box))
+            return cudaErrorInvalidValue;
+    }
     if (!q8) {
-        // [token][kv head][element], boxes of one head's 64 elements of a tile of
+        // K, V: [token][kv head][element], boxes of one head's 64 elements of a tile of
         // tokens; without a single key nothing is ever copied
         const int kt = a.head_dim == 64 ? span::Geo<64, false>::KT : span::Geo<128, false>::KT;
         const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.num_kv_heads,
@@ -48,16 +56,16 @@ cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream
         const long long stride[2] = {a.k_row_stride, a.v_row_stride};
         for (int i = 0; i < 2; ++i) {
             const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)stride[i] * 2};
-            if (!encode_tensor_map(i == 0 ? &tk : &tv, a.dtype, 3, src[i], dims, strides, box))
+            if (!encode_tensor_map(i == 0 ? &tm.k : &tm.v, a.dtype, 3, src[i], dims, strides, box))
                 return cudaErrorInvalidValue;
         }
     }
     const int ctas = std::min(sms, span::kMaxCtas);
     const bool bf16 = a.dtype == NS_BF16;
     if (q8)
-        return launch_span_q8(bf16, tk, tv, P, ctas, stream);
-    return a.head_dim == 64 ? launch_span_d64(bf16, tk, tv, P, ctas, stream)
-                            : launch_span_d128(bf16, tk, tv, P, ctas, stream);
+        return launch_span_q8(bf16, tm, P, ctas, stream);
+    return a.head_dim == 64 ? launch_span_d64(bf16, tm, P, ctas, stream)
+                            : launch_span_d128(bf16, tm, P, ctas, stream);
 }
 
 }  // namespace ns

@@ -16,13 +16,12 @@
 // kernel joins them.
 //
 // Warps of a CTA (512 threads):
-//   0-3, 4-7  softmax of query tile 0 and 1: a thread owns a row.  It lays its row
-//             of Q into shared memory, reads its row of S from TMEM, and writes P
-//             (fp16) back to TMEM;
+//   0-3, 4-7  softmax of query tile 0 and 1: a thread owns a row.  It reads its row
+//             of S from TMEM, and writes P (fp16) back to TMEM;
 //   8-11      conversion: K and V tiles into the form that the products take;
 //   12        producer: TMA copies of K and V tiles;
 //   13, 14    issue S = Q K^T and O += P V of query tile 0 and 1;
-//   15        walks the CTA's run of units.
+//   15        walks the CTA's run of units, and copies their Q (fp16, or head_dim 128).
 // The two tiles' softmax and products alternate by themselves: while one tile's
 // scores are exponentiated, the other's products run.
 //
@@ -90,7 +89,7 @@ struct Geo {
     static_assert(P + KT <= 512, "tensor memory");
     // cost of a unit besides its keys (laying out Q, filling the pipe, the epilogue)
     // and the least cost that a CTA is given, in keys
-    static constexpr int OVERHEAD = D == 128 ? 7 * KT : Q8 ? 5 * KT / 2 : 3 * KT;
+    static constexpr int OVERHEAD = D == 128 ? 11 * KT / 2 : Q8 ? 5 * KT / 2 : 3 * KT;
     static constexpr int SHARE = OVERHEAD;  // at most one short unit a CTA while there are CTAs
     static constexpr int WHOLE = 4;  // units of so few key tiles are not cut
 };
@@ -118,10 +117,14 @@ constexpr size_t header_bytes() { return kMaxCtas * sizeof(Header); }
 struct Params {
     SpanAttnArgs a;
     int group, qt;
-    float scale_log2;  // of |scale|; its sign goes into Q
-    uint32_t q_flip;   // sign bits to flip in a word of Q
+    float scale_log2;  // of |scale|
+    int negate;        // scale < 0: the products take -Q
     Header *headers;
     float *records;
+};
+
+struct Maps {
+    CUtensorMap q, k, v;  // k, v: contiguous rows only
 };
 
 template <int D, bool Q8>
@@ -134,7 +137,7 @@ struct alignas(1024) Smem {
     uint64_t raw_full[GG::RAW], raw_empty[GG::RAW];
     uint64_t v_full[GG::STAGES];
     uint64_t k_ready[GG::STAGES], v_ready[GG::STAGES], k_empty[GG::STAGES], v_empty[GG::STAGES];
-    uint64_t q_ready[2], s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t q_ready[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2];
     uint64_t u_full[kUnits], u_empty[kUnits];
     Unit unit[kUnits], no_unit;
     alignas(16) float ev[GG::STAGES][4];    // Ev of a stage's V, by group of keys
@@ -327,14 +330,21 @@ __device__ __forceinline__ uint2 codes_to_f16(uint32_t w, __half2 d)
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool Q8>
 __global__ void __launch_bounds__(kThreads, 1)
-    span_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const __grid_constant__ Params P)
+    span_attn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params P)
 {
     using GG = Geo<D, Q8>;
     constexpr int KT = GG::KT, REG = GG::REG, ST = GG::STAGES;
     constexpr bool BF = T::code == NS_BF16;
     constexpr bool SCALED = Q8 || BF;  // V tiles carry an exponent
     constexpr bool WIDE = BF && !Q8;   // of any size that bf16 has
+    // Q comes by TMA as soon as the scores of the unit before are out, or by the softmax
+    // threads, a row each, between two units (1100 to 3500 clocks, of 2400 a tile).  The
+    // first is faster at head_dim 128 (8192 bf16 tokens 451 against 480 us, fp16 381 against
+    // 394) and for fp16 (mixed chunks over q8_0 32.8 against 33.4, four short prompts 10.2
+    // against 10.6; 8192 tokens 137 against 134), the second for bf16 at 64 (packed prompts 86
+    // against 92, long chunks over q8_0 156 against 160): there the two query tiles' softmax
+    // bounds the call, and the later Q of one keeps them out of step.
+    constexpr bool Q_TMA = D == 128 || !BF;
     extern __shared__ unsigned char smem_raw[];
     Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -342,9 +352,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qt = P.qt, R = 2 * P.qt;
 
     if (!Q8 && threadIdx.x == kProducerWarp * 32) {
-        tc::prefetch_tensormap(&tm_k);
-        tc::prefetch_tensormap(&tm_v);
+        tc::prefetch_tensormap(&maps.k);
+        tc::prefetch_tensormap(&maps.v);
     }
+    if (Q_TMA && threadIdx.x == kPlanWarp * 32)
+        tc::prefetch_tensormap(&maps.q);
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&sm.k_ready[i], Q8 ? 4 : 1);
@@ -358,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.raw_empty[i], 4);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&sm.q_ready[t], kTileWarps);
+            mbar_init(&sm.q_ready[t], Q_TMA ? 1 : kTileWarps);
+            mbar_init(&sm.q_empty[t], 1);
             mbar_init(&sm.s_full[t], SCALED ? 2 : 1);
             mbar_init(&sm.s_free[t], kTileWarps);
             mbar_init(&sm.p_full[t], kTileWarps);
@@ -484,6 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float row_scale = P.scale_log2;
         // Lay row r of the unit's query tile into shared memory.
         auto lay_q = [&](const Unit &u) {
+            if (Q_TMA || min(u.t1, tiles_of<KT>(u, t, qt)) <= u.t0)
+                return;
             const int tok = u.i0 + t * qt + rt;
             const bool on = rt < qt && tok < u.n;
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
@@ -508,21 +523,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 row_scale = P.scale_log2 * pow2(max(e - 141, -126));
             }
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                w[c].x ^= P.q_flip;
-                w[c].y ^= P.q_flip;
-                w[c].z ^= P.q_flip;
-                w[c].w ^= P.q_flip;
+            for (int c = 0; c < D / 8; ++c)
                 *reinterpret_cast<uint4 *>(qs + (c >> 3) * (kRows * kPanel) + (((c & 7) ^ (r & 7)) << 4)) = w[c];
-            }
             fence_async_smem();
             __syncwarp();
             warp_arrive(&sm.q_ready[t]);
         };
 
         const Unit *now = &wait_unit();
-        if (now->t1 >= 0 && min(now->t1, tiles_of<KT>(*now, t, qt)) > now->t0)
-            lay_q(*now);
+        lay_q(*now);
         while (now->t1 >= 0) {
             const int t0 = now->t0, end = min(now->t1, tiles_of<KT>(*now, t, qt));
             // last key of the row, of the tile's first row
@@ -667,11 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Unit &u = *now;
             vtile += u.t1 - t0;
 
-            // the next unit's Q, so that its first scores are under way during the epilogue
+            // the next unit's Q first, so that its scores are under way during the epilogue
             const int this_no = unit_no - 1;
             const Unit *next = &wait_unit();
-            if (next->t1 >= 0 && min(next->t1, tiles_of<KT>(*next, t, qt)) > next->t0)
-                lay_q(*next);
+            lay_q(*next);
 
             // ---- epilogue
             const int tok = u.i0 + t * qt + rt;
@@ -846,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mbar_arrive_expect_tx(&sm.k_ready[stage], GG::TILE);
 #pragma unroll
                                 for (int g = 0; g < REG; ++g)
-                                    tc::tma_load_3d(sm.k[stage] + g * KT * kPanel, &tm_k, g * 64, u.h, row,
+                                    tc::tma_load_3d(sm.k[stage] + g * KT * kPanel, &maps.k, g * 64, u.h, row,
                                                     &sm.k_ready[stage]);
                                 ok = mbar_wait(&sm.v_empty[stage], par);
                             }
@@ -854,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mbar_arrive_expect_tx(&sm.v_full[stage], GG::TILE);
 #pragma unroll
                                 for (int g = 0; g < REG; ++g)
-                                    tc::tma_load_3d(sm.v[stage] + g * KT * kPanel, &tm_v, g * 64, u.h, row,
+                                    tc::tma_load_3d(sm.v[stage] + g * KT * kPanel, &maps.v, g * 64, u.h, row,
                                                     &sm.v_full[stage]);
                             }
                         }
@@ -924,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // of j were read, then the values of j as soon as its weights are there.  The
             // whole warp walks the tiles; operands are warp-uniform.
             const int t = warp - kProductWarp;
-            const uint32_t idesc_s = tc::idesc_f16(kRows, KT, BF && !Q8 ? 1 : 0, false);
+            const uint32_t idesc_s = tc::idesc_f16(kRows, KT, BF && !Q8 ? 1 : 0, false) | (P.negate ? tc::kNegateA : 0u);
             const uint32_t idesc_o = tc::idesc_f16(kRows, D, 0, true);
             const uint64_t dk = tc::desc_sw128(0), dv = tc::desc_sw128_panels(0, KT * kPanel);
             auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
@@ -956,6 +964,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             (uint32_t)(dk >> 32), idesc_s, kk > 0);
                         tc::mma_commit_warp(&sm.s_full[t]);
                         tc::mma_commit_warp(&sm.k_empty[ks]);
+                        if (Q_TMA && i == mine - 1)
+                            tc::mma_commit_warp(&sm.q_empty[t]);
                         ++count;
                         if (SCALED) {
                             // the softmax reads the exponents of this tile's groups, too: they are
@@ -1012,6 +1022,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++no;
             };
+            // Q of both query tiles, each once the scores of the unit before are out.  The next
+            // unit is announced first, so that its keys are not held up.
+            int loads[2] = {0, 0};
+            auto load_q = [&](const Unit &u) {
+                if (lane == 0 && ok) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (min(u.t1, tiles_of<KT>(u, t, qt)) <= u.t0)
+                            continue;
+                        ok = ok && mbar_wait(&sm.q_empty[t], (uint32_t)(loads[t] - 1) & 1u);
+                        if (!ok)
+                            break;
+                        ++loads[t];
+                        mbar_arrive_expect_tx(&sm.q_ready[t], (uint32_t)(REG * P.group * qt * kPanel));
+#pragma unroll
+                        for (int g = 0; g < REG; ++g)
+                            tc::tma_load_3d(sm.q[t] + g * kRows * kPanel, &maps.q, g * 64, u.h * P.group,
+                                            u.q0 + u.i0 + t * qt, &sm.q_ready[t]);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            };
+            Unit behind = {};  // announced, its Q not yet asked for
+            bool pending = false;
             if (x0 < x1) {
                 int s = sm.start_s, h = 0, v = 0;
                 long long xs = sm.start_x;  // of the sequence
@@ -1085,6 +1119,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 head.last = owner(ue - 1);
                             }
                             announce(u);
+                            if (Q_TMA && (no == 1 || pending))
+                                load_q(pending ? behind : u);
+                            pending = no > 1;
+                            behind = u;
                         }
                     xs += per_head * a.num_kv_heads;
                 }
@@ -1093,7 +1131,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             stop.t1 = -1;
             if (ok)
                 announce(stop);
+            if (Q_TMA && pending)
+                load_q(behind);
             if (lane == 0) {
+                // the copies have landed before the CTA leaves
+                for (int t = 0; t < 2; ++t)
+                    if (loads[t] > 0)
+                        ok = mbar_wait(&sm.q_ready[t], (uint32_t)(loads[t] - 1) & 1u) && ok;
                 P.headers[blockIdx.x] = head;
                 if (!ok)
                     raise_status(a.status, NS_DEV_WAIT_TIMEOUT);
@@ -1182,7 +1226,7 @@ __global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ 
 // Launch
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool Q8>
-cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &P, int ctas, cudaStream_t stream)
+cudaError_t launch(const Maps &tm, const Params &P, int ctas, cudaStream_t stream)
 {
     const long long max_keys = Q8 ? (long long)P.a.max_blocks_per_seq * 16 : P.a.total_k_tokens;
     // once for each device: the shared memory, and that the kernel has the registers
@@ -1217,7 +1261,7 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &P
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, span_attn_kernel<T, D, Q8>, tk, tv, P);
+    e = cudaLaunchKernelEx(&cfg, span_attn_kernel<T, D, Q8>, tm, P);
     // no sequence has the keys of a unit that may be cut (the second launch costs
     // 3 us of a small call)
     if (e != cudaSuccess || max_keys <= Geo<D, Q8>::WHOLE * Geo<D, Q8>::KT)
@@ -1230,11 +1274,8 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &P
 
 }  // namespace span
 
-cudaError_t launch_span_d64(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv, const span::Params &P, int ctas,
-                            cudaStream_t stream);
-cudaError_t launch_span_d128(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv, const span::Params &P, int ctas,
-                             cudaStream_t stream);
-cudaError_t launch_span_q8(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv, const span::Params &P, int ctas,
-                           cudaStream_t stream);
+cudaError_t launch_span_d64(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
+cudaError_t launch_span_d128(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
+cudaError_t launch_span_q8(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
 
 }  // namespace ns

@@ -89,6 +89,8 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int ab_fmt, bool 
            | ((uint32_t)(M >> 4) << 24);      // M / 16
 }
 
+constexpr uint32_t kNegateA = 1u << 13;  // instruction descriptor: -A instead of A
+
 // D[tmem] = A[smem] * B[smem] (+ D when accumulate), issued by one thread.
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                        uint32_t idesc, uint32_t accumulate)
