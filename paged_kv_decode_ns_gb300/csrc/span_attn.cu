@@ -37,7 +37,7 @@ cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream
     P.headers = static_cast<span::Header *>(a.workspace);
     P.records = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + span::header_bytes());
     span::Maps tm = {};
-    {
+    if (span::q_by_tma(a.head_dim, a.dtype == NS_BF16)) {
         // Q: [token][head][element], boxes of a group's heads of a query tile's tokens
         const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.total_q_tokens};
         const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)a.q_row_stride * 2};

@@ -37,19 +37,20 @@
 // half of it the output's own rounding; two products for each would undo that at
 // twice the tensor work.  Everything else (scores, sums, O) is fp32.
 //
-// What bounds it.  At head_dim 128 the tensor cores: 8192 tokens, 32 / 8 heads, 420 us,
-// 1.31 PFLOP/s, 71% of the measured peak.  At head_dim 64 the softmax: a pair of 128 x
+// What bounds it.  At head_dim 128 the tensor cores: 8192 tokens, 32 / 8 heads, 398 us,
+// 1.38 PFLOP/s, 75% of the measured peak.  At head_dim 64 the softmax: a pair of 128 x
 // 128 tiles takes ~2370 clocks, against 1050 of products and 1024 of exponentials; two
 // softmax warps a scheduler issue half of the time and wait on TMEM, barriers and
-// each other's use of the exponential unit for the rest (134 us for 8192 fp16 tokens of
-// 14 / 2 heads, 0.90 PFLOP/s; bf16 152 us, its exponents by group on top).  Short
+// each other's use of the exponential unit for the rest (137 us for 8192 fp16 tokens of
+// 14 / 2 heads, 0.88 PFLOP/s; bf16 152 us, its exponents by group on top).  Short
 // calls: launch, the plan, one unit's chain of copy, product, softmax, product and
 // the join (four prompts of up to 200 tokens 10 us; 32 spans of drafts 19 us).
 //
 // Two softmax warpgroups a query tile (96 registers a thread) take 155 us where one
 // takes 136: the row no longer fits the registers.  Tiles read from TMEM 32 columns at a
-// time, the exponentials of the two tiles in turns, and a sleep between polls were
-// slower too or made no difference.
+// time, the exponentials of the two tiles in turns (whole or half of them), a sleep
+// between polls, a head start for one tile, and the first weights before the maximum
+// were slower too or made no difference.
 #pragma once
 
 #include <algorithm>
@@ -93,6 +94,15 @@ struct Geo {
     static constexpr int SHARE = OVERHEAD;  // at most one short unit a CTA while there are CTAs
     static constexpr int WHOLE = 4;  // units of so few key tiles are not cut
 };
+
+// Q comes by TMA as soon as the scores of the unit before are out, or by the softmax
+// threads, a row each, between two units (1100 to 3500 clocks, of 2400 a tile).  The
+// first is faster at head_dim 128 (8192 bf16 tokens 451 against 480 us, fp16 381 against
+// 394) and for fp16 (mixed chunks over q8_0 32.8 against 33.4, four short prompts 10.2
+// against 10.6; 8192 tokens 137 against 134), the second for bf16 at 64 (packed prompts 86
+// against 92, long chunks over q8_0 156 against 160): there the two query tiles' softmax
+// bounds the call, and the later Q of one keeps them out of step.
+constexpr bool q_by_tma(int D, bool bf16) { return D == 128 || !bf16; }
 
 // A CTA's part of a unit: key tiles [t0, t1).
 struct Unit {
@@ -337,14 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool BF = T::code == NS_BF16;
     constexpr bool SCALED = Q8 || BF;  // V tiles carry an exponent
     constexpr bool WIDE = BF && !Q8;   // of any size that bf16 has
-    // Q comes by TMA as soon as the scores of the unit before are out, or by the softmax
-    // threads, a row each, between two units (1100 to 3500 clocks, of 2400 a tile).  The
-    // first is faster at head_dim 128 (8192 bf16 tokens 451 against 480 us, fp16 381 against
-    // 394) and for fp16 (mixed chunks over q8_0 32.8 against 33.4, four short prompts 10.2
-    // against 10.6; 8192 tokens 137 against 134), the second for bf16 at 64 (packed prompts 86
-    // against 92, long chunks over q8_0 156 against 160): there the two query tiles' softmax
-    // bounds the call, and the later Q of one keeps them out of step.
-    constexpr bool Q_TMA = D == 128 || !BF;
+    constexpr bool Q_TMA = q_by_tma(D, BF);
     extern __shared__ unsigned char smem_raw[];
     Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
