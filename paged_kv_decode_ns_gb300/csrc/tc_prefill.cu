@@ -278,8 +278,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init_fence();
     }
     __syncthreads();
-    if (sm.u_ok != 1)
+    if (sm.u_ok != 1) {
+        // Launched as a programmatic dependent of the span walk, this grid reads nothing
+        // that the walk writes, and runs beside it.  But it must not end before the walk:
+        // a grid behind this one waits for this one alone, and may touch what the walk
+        // still reads and writes.  One CTA that stays is enough: the last one, which never
+        // has a unit (the launch's bound), so no unit waits for its SM.
+        if (blockIdx.x == gridDim.x - 1)
+            grid_dependency_wait();
         return;  // both CTAs of the cluster see the same unit and leave together
+    }
     tc::cluster_sync();  // rank 0's barriers are initialised before rank 1 can arrive on them
     const uint32_t rank = tc::cluster_rank();
     // Rows of the Q tile the TMA box does not cover are zeroed once.
@@ -701,7 +709,7 @@ static cudaError_t launch_tc(const CUtensorMap &tq, const CUtensorMap &tk, const
     }
     // programmatic dependent of the kernel before it (the span walk of the same
     // call, whose results this kernel does not read): it may start as soon as
-    // SMs free up, with no wait
+    // SMs free up, and only its last CTA waits for the walk, before it leaves
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
@@ -763,7 +771,8 @@ cudaError_t launch_tc_prefill(const void *q, const int32_t *query_start_loc, con
     P.status = status;
     // an upper bound on the units (2 CTAs each): a span of n >= min_span
     // tokens has ceil(n / qt) query tiles, and there are at most
-    // min(num_seqs, T / min_span) such spans; CTA pairs without a unit exit at once
+    // min(num_seqs, T / min_span) such spans; CTA pairs without a unit exit at once.
+    // The sum of ceil(n / qt) is below T / qt + spans, so at least the last pair has none.
     const long long spans = std::min<long long>(num_seqs, total_q_tokens / min_span);
     const long long units = (long long)num_kv_heads * ((total_q_tokens + qt - 1) / qt + spans);
     const int grid = (int)(2 * units > 0x7ffffffe ? 0x7ffffffe : 2 * units);
