@@ -18,16 +18,16 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ int owner(const int32_t *start, int num_seqs, int t)
 {
     int lo = 0, hi = num_seqs;  // start[lo] <= t < start[hi], once start[0] <= t
-    if (__ldg(start) > t)
+    if (*start > t)
         return -1;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(start + mid) <= t)
+        if (start[mid] <= t)
             lo = mid;
         else
             hi = mid;
     }
-    return t < __ldg(start + lo + 1) ? lo : -1;
+    return t < start[lo + 1] ? lo : -1;
 }
 
 // Eight codes (x, y) and their scale (z) -> eight elements: fp16(d) * code is exact
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, 5) kv_gather_kernel(const GatherArgs
     __shared__ long long src[kMaxTokens];  // first pool row of the token (its kv head 0), or -1
     if (blockIdx.x == 0)  // entries out of order, also those that no row falls between
         for (int s = threadIdx.x; s < a.num_seqs; s += kThreads) {
-            const int first = __ldg(a.start_loc + s), end = __ldg(a.start_loc + s + 1);
+            const int first = a.start_loc[s], end = a.start_loc[s + 1];
             if (first < 0 || end < first || end > a.total_tokens)
                 raise_status(a.status, NS_DEV_BAD_QUERY_SPAN);
         }
@@ -70,13 +70,13 @@ __global__ void __launch_bounds__(kThreads, 5) kv_gather_kernel(const GatherArgs
         long long row = -1;
         const int s = owner(a.start_loc, a.num_seqs, t);
         if (s >= 0) {
-            const int first = __ldg(a.start_loc + s), end = __ldg(a.start_loc + s + 1), p = t - first;
+            const int first = a.start_loc[s], end = a.start_loc[s + 1], p = t - first;
             if (first < 0 || end > a.total_tokens) {
                 // reported above
             } else if ((long long)(end - first) > (long long)a.max_blocks_per_seq * a.block_size) {
                 raise_status(a.status, NS_DEV_BAD_CONTEXT_LEN);
             } else {
-                const int blk = __ldg(a.block_tables + (long long)s * a.max_blocks_per_seq + p / a.block_size);
+                const int blk = a.block_tables[(long long)s * a.max_blocks_per_seq + p / a.block_size];
                 if (blk < 0 || blk >= a.num_blocks)
                     raise_status(a.status, NS_DEV_BAD_BLOCK_ID);
                 else
@@ -102,13 +102,13 @@ __global__ void __launch_bounds__(kThreads, 5) kv_gather_kernel(const GatherArgs
                 continue;
             const long long prow = row + (long long)h * a.block_size;
             if (!Q8) {
-                k[b] = __ldg(static_cast<const uint4 *>(a.k) + prow * head_chunks + chunk);
-                v[b] = __ldg(static_cast<const uint4 *>(a.v) + prow * head_chunks + chunk);
+                k[b] = static_cast<const uint4 *>(a.k)[prow * head_chunks + chunk];
+                v[b] = static_cast<const uint4 *>(a.v)[prow * head_chunks + chunk];
             } else {
-                const uint2 kc = __ldg(static_cast<const uint2 *>(a.k) + prow * 8 + chunk),
-                            vc = __ldg(static_cast<const uint2 *>(a.v) + prow * 8 + chunk);
-                k[b] = make_uint4(kc.x, kc.y, __ldg(static_cast<const uint16_t *>(a.k_scales) + prow * 2 + (chunk >> 2)), 0u);
-                v[b] = make_uint4(vc.x, vc.y, __ldg(static_cast<const uint16_t *>(a.v_scales) + prow * 2 + (chunk >> 2)), 0u);
+                const uint2 kc = static_cast<const uint2 *>(a.k)[prow * 8 + chunk],
+                            vc = static_cast<const uint2 *>(a.v)[prow * 8 + chunk];
+                k[b] = make_uint4(kc.x, kc.y, static_cast<const uint16_t *>(a.k_scales)[prow * 2 + (chunk >> 2)], 0u);
+                v[b] = make_uint4(vc.x, vc.y, static_cast<const uint16_t *>(a.v_scales)[prow * 2 + (chunk >> 2)], 0u);
             }
         }
 #pragma unroll

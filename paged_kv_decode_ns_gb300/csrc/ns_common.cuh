@@ -105,7 +105,10 @@ __device__ __forceinline__ void regs_shrink()
 
 // Programmatic dependent launch: wait for the previous grid on the stream
 // (complete, memory visible) / let the next one be scheduled.  Both are
-// no-ops for a grid launched without the programmatic attribute.
+// no-ops for a grid launched without the programmatic attribute.  Behind the wait a
+// kernel reads with plain loads: what the previous grid writes changes during this
+// kernel's lifetime, which rules out the non-coherent loads of __ldg, and those may
+// also be moved above the wait.
 __device__ __forceinline__ void grid_dependency_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -179,20 +179,20 @@ template <bool Q8>
 __device__ __forceinline__ Seq read_seq(const SpanAttnArgs &a, int s, unsigned *status)
 {
     Seq r;
-    r.q0 = __ldg(a.query_start_loc + s);
-    const int q1 = __ldg(a.query_start_loc + s + 1);
+    r.q0 = a.query_start_loc[s];
+    const int q1 = a.query_start_loc[s + 1];
     r.n = q1 - r.q0;
     unsigned bad = r.q0 < 0 || q1 < r.q0 || q1 > a.total_q_tokens ? NS_DEV_BAD_QUERY_SPAN : 0u;
     if (Q8) {
         r.k0 = 0;
-        r.L = __ldg(a.context_lens + s);
+        r.L = a.context_lens[s];
         if (r.L < r.n)
             bad |= NS_DEV_BAD_QUERY_SPAN;
         else if ((long long)r.L > (long long)a.max_blocks_per_seq * 16)
             bad |= NS_DEV_BAD_CONTEXT_LEN;
     } else {
-        r.k0 = __ldg(a.key_start_loc + s);
-        const int k1 = __ldg(a.key_start_loc + s + 1);
+        r.k0 = a.key_start_loc[s];
+        const int k1 = a.key_start_loc[s + 1];
         r.L = k1 - r.k0;
         if (r.k0 < 0 || k1 < r.k0 || k1 > a.total_k_tokens)
             bad |= NS_DEV_BAD_QUERY_SPAN;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 w[D / 8];
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
-                w[c] = on ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                w[c] = on ? src[c] : make_uint4(0u, 0u, 0u, 0u);
             if (Q8 && BF) {
                 // fp16 for the product with fp16 keys: the row's largest value goes
                 // just below 2^15, its power of two into the score's scale
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int b = lane >> 2, what = lane & 3, blk = j * (KT / 16) + b;
                         int phys = -1;
                         if (blk < blocks) {
-                            phys = __ldg(a.block_tables + (long long)u.s * a.max_blocks_per_seq + blk);
+                            phys = a.block_tables[(long long)u.s * a.max_blocks_per_seq + blk];
                             if (phys < 0 || (long long)phys >= a.num_blocks) {
                                 raise_status(a.status, NS_DEV_BAD_BLOCK_ID);
                                 phys = -1;

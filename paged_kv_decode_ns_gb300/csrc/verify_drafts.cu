@@ -95,7 +95,7 @@ struct Row {
     int skip;            // token of weight 0 (certain draft), or -1
     __device__ __forceinline__ Pair at(int v) const
     {
-        return weight(v == skip ? 0.f : __ldg(p + v), q != nullptr ? __ldg(q + v) : 0.f);
+        return weight(v == skip ? 0.f : p[v], q != nullptr ? q[v] : 0.f);
     }
 };
 
@@ -112,8 +112,8 @@ __device__ Pair slice_sum(const Row &r, int lo, int hi, int lane, bool aligned)
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const bool on = v + i * 128 + 4 * lane < hi;
-                p[i] = on ? __ldg(reinterpret_cast<const float4 *>(r.p + v + i * 128) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-                q[i] = Q && on ? __ldg(reinterpret_cast<const float4 *>(r.q + v + i * 128) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+                p[i] = on ? reinterpret_cast<const float4 *>(r.p + v + i * 128)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+                q[i] = Q && on ? reinterpret_cast<const float4 *>(r.q + v + i * 128)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
@@ -134,8 +134,8 @@ __device__ Pair slice_sum(const Row &r, int lo, int hi, int lane, bool aligned)
 #pragma unroll
             for (int i = 0; i < 4 * kBatch; ++i) {
                 const int at = v + i * 32 + lane;
-                p[i] = at < hi && at != r.skip ? __ldg(r.p + at) : 0.f;
-                q[i] = Q && at < hi ? __ldg(r.q + at) : 0.f;
+                p[i] = at < hi && at != r.skip ? r.p[at] : 0.f;
+                q[i] = Q && at < hi ? r.q[at] : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 4 * kBatch; i += 2)
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     grid_launch_dependents();
     const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = __ldg(a.start + s), end = __ldg(a.start + s + 1);
+    const int first = a.start[s], end = a.start[s + 1];
     const int n = end - first;
     if (first < 0 || end < first || end > a.total_drafts) {
         if (threadIdx.x == 0 && rank == 0)
@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
         return;  // the whole cluster
     }
     int32_t *out = a.out_tokens + first + s;
+    const double u = a.sample_u[s];
     if (warp == 0) {
         int accepted = n;
         bool bad = false;
@@ -224,12 +225,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
             const int i = i0 + lane;
             bool ok = true, off = false;
             if (i < n) {
-                const int x = __ldg(a.tokens + first + i);
+                const int x = a.tokens[first + i];
                 off = x < 0 || x >= a.vocab;
                 if (!off) {
-                    const double p = __ldg(a.target + (long long)(first + s + i) * a.target_stride + x);
-                    const double q = a.draft ? (double)__ldg(a.draft + (long long)(first + i) * a.draft_stride + x) : 1.0;
-                    ok = (double)__ldg(a.accept_u + first + i) * q < p;
+                    const double p = a.target[(long long)(first + s + i) * a.target_stride + x];
+                    const double q = a.draft ? (double)a.draft[(long long)(first + i) * a.draft_stride + x] : 1.0;
+                    ok = (double)a.accept_u[first + i] * q < p;
                 }
             }
             bad |= __any_sync(0xffffffffu, off);
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
         if (rank == 0)  // the place of the drawn token is left to the CTA that finds it
             for (int i = lane; i <= n; i += 32)
                 if (bad || i != accepted)
-                    out[i] = !bad && i < accepted ? __ldg(a.tokens + first + i) : -1;
+                    out[i] = !bad && i < accepted ? a.tokens[first + i] : -1;
         if (lane == 0) {
             sh_state = bad ? 1 : 0;
             sh_accepted = accepted;
@@ -262,8 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     Row r;
     r.p = a.target + (long long)(first + s + acc) * a.target_stride;
     r.q = refused && a.draft ? a.draft + (long long)(first + acc) * a.draft_stride : nullptr;
-    r.skip = refused && !a.draft ? __ldg(a.tokens + first + acc) : -1;
-    const double u = __ldg(a.sample_u + s);
+    r.skip = refused && !a.draft ? a.tokens[first + acc] : -1;
 
     // contiguous runs, one for each warp of the cluster, of whole 128-byte lines
     const int runs = cluster * kWarps;

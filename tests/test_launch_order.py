@@ -42,3 +42,11 @@ def test_kernels_launched_early_wait_for_the_grid_in_front(launch):
     name, kernels = LAUNCHED_EARLY[launch]
     for kernel in kernels:
         assert "grid_dependency_wait()" in kernel_body(name, kernel), kernel
+
+
+@pytest.mark.parametrize("name", ["span_attn.cuh", "kv_gather.cu", "verify_drafts.cu"])
+def test_loads_behind_the_wait_are_coherent(name):
+    """What the grid in front writes changes while such a kernel is resident, so its reads may not go
+    through the read-only path (the decode reads its planning arrays before the wait, by contract)."""
+    text = source(name)
+    assert "__ldg" not in text and "__restrict__" not in text and "ld.global.nc" not in text
