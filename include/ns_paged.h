@@ -486,7 +486,9 @@ size_t ns_span_attn_workspace_bytes(int head_dim);
  * infinite or NaN may reach every row of its own sequence.  No sequence
  * reaches another.  Softmax weights and v are rounded to fp16 (11 bits) for the
  * value product, scaled by powers of two so that bf16 values of any size keep
- * them; scores, sums and outputs are fp32 until the last rounding.
+ * them; scores, sums and outputs are fp32 until the last rounding.  A weight below
+ * 2^-21 of the row's largest keeps fewer bits: it is off by up to 2^-32 of that
+ * (2^-12 of the output from a million keys).
  */
 ns_status ns_prompt_attn(const void *q, const void *k, const void *v, const int32_t *query_start_loc,
                          const int32_t *key_start_loc, int num_seqs, int total_q_tokens,

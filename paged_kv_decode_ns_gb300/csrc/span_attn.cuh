@@ -75,7 +75,11 @@ constexpr int kUnits = 4;        // units announced ahead
 constexpr int kMeta = 8;
 constexpr int kMaxCtas = 160;    // grid, at most: the workspace has two records for each
 constexpr float kTinyScale = 1.17549435e-38f;  // a score of -infinity times a scale of 0 would be NaN
-constexpr float kSlack = 8.0f;   // the reference moves when a score passes it by more (log2 units)
+// The reference m of a row is set kLift below a score (log2 units), and moves when a
+// score passes that by more than kSlack: weights 2^(z - m) of up to 2^15 use fp16's range
+// down to 2^-32 of the largest weight (half of its least step 2^-24, beside a weight of
+// 2^7 or more).
+constexpr float kLift = 7.0f, kSlack = 8.0f;
 
 template <int D, bool Q8>
 struct Geo {
@@ -614,12 +618,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // the reference moves to a score that passes it by more than the slack
-                const bool up = top > m + kSlack;
-                const float drop = up ? m - top : 0.f;
+                const bool up = top > m + (kLift + kSlack);
+                const float drop = up ? m - (top - kLift) : 0.f;
                 const float alpha = fast_exp2(drop);  // 0 at the first tile
                 const bool moved = up && j > t0;
                 l = WIDE ? times_pow2(l, drop) : l * alpha;
-                m = up ? top : m;
+                m = up ? top - kLift : m;
                 const float ref = m > -INFINITY ? m : 0.f;
                 if (WIDE) {
                     // Values so small beside others that their weights would vanish in fp32
