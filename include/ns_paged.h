@@ -485,10 +485,12 @@ size_t ns_span_attn_workspace_bytes(int head_dim);
  * query, or in a key that a row sees, makes that row NaN; a value of v that is
  * infinite or NaN may reach every row of its own sequence.  No sequence
  * reaches another.  Softmax weights and v are rounded to fp16 (11 bits) for the
- * value product, scaled by powers of two so that bf16 values of any size keep
- * them; scores, sums and outputs are fp32 until the last rounding.  A weight below
- * 2^-21 of the row's largest keeps fewer bits: it is off by up to 2^-32 of that
- * (2^-12 of the output from a million keys).
+ * value product; scores, sums and outputs are fp32 until the last rounding.  A
+ * weight below 2^-21 of the row's largest keeps fewer bits: it is off by up to
+ * 2^-32 of that (2^-12 of the output from a million keys).  bf16 values are scaled
+ * by powers of two on the way, so that they may have any size: each is off by at
+ * most 2^-36 of the largest value of its sequence and kv head (and exact above
+ * 2^-28 of it), or by 2^-109.
  */
 ns_status ns_prompt_attn(const void *q, const void *k, const void *v, const int32_t *query_start_loc,
                          const int32_t *key_start_loc, int num_seqs, int total_q_tokens,
@@ -509,8 +511,10 @@ ns_status ns_prompt_attn(const void *q, const void *k, const void *v, const int3
  * its table row (NS_DEV_BAD_CONTEXT_LEN); a block id outside the pool sets
  * NS_DEV_BAD_BLOCK_ID and its tokens are left out.  The dequantised keys and
  * values and the softmax weights are rounded to fp16 for the products, and so
- * are bf16 queries, each scaled by a power of two first.  An infinite or NaN
- * scale may reach every row of its own span.  workspace: ns_span_attn_workspace_bytes(64).
+ * are bf16 queries, each scaled by a power of two first.  Weights are kept as in
+ * ns_prompt_attn; scales far below the largest of the sequence and kv head lose
+ * bits (their values are off by up to 2^-29 of the largest value).  An infinite or
+ * NaN scale may reach every row of its own span.  workspace: ns_span_attn_workspace_bytes(64).
  */
 ns_status ns_paged_attn_prefill_q8_0(const void *q, const int32_t *query_start_loc, const void *k_codes,
                                      const void *k_scales, const void *v_codes, const void *v_scales,

@@ -27,12 +27,14 @@
 //
 // P is rounded to fp16 (11 bits) for both types: the products of a bf16 call
 // would need P in two bf16 parts for the same accuracy, twice the value products.
-// So V is fp16 too: a group of bf16 keys (those of one conversion warp) is scaled by
-// a power of two, 2^-Ev, that puts its largest value just below 2^15, which keeps
-// every value within 2^-29 of that exact.  Ev moves into the exponent of P,
-// 2^(z + Ev - m), with m a running reference of z + Ev; the sum takes it back out.
-// q8_0 tiles are dequantised to fp16 in the same way, with Ek for K in the score's
-// scale: code times scale has up to 18 bits, so K, V and P each lose up to
+// So V is fp16 too: a tile of bf16 values is scaled by a power of two, 2^-Ev.  Ev only
+// rises along a unit, to 2^3 above what puts the largest value so far just below 2^15,
+// and O is rescaled when it does (seldom, thanks to the 2^3): every value is off by at
+// most 2^-36 of the largest so far, and P, 2^(z - m), does not depend on the size of the
+// values.  (With exponents of 32 keys each in the exponent of P, one value 2^12 above the
+// others took 12 bits of the weights of all keys but those 32.)
+// q8_0 tiles are dequantised to fp16 in the same way, with Ek for K, by group of keys, in
+// the score's scale: code times scale has up to 18 bits, so K, V and P each lose up to
 // 2^-11 of themselves there.  An fp16 call over a q8_0 cache is then off by 4.2e-4 of its output,
 // half of it the output's own rounding; two products for each would undo that at
 // twice the tensor work.  Everything else (scores, sums, O) is fp32.
@@ -80,13 +82,15 @@ constexpr float kTinyScale = 1.17549435e-38f;  // a score of -infinity times a s
 // down to 2^-32 of the largest weight (half of its least step 2^-24, beside a weight of
 // 2^7 or more).
 constexpr float kLift = 7.0f, kSlack = 8.0f;
+constexpr int kRoom = 3;   // the exponent of bf16 and q8_0 values is set for values 2^3 larger
+constexpr int kLeast = 54; // and not below this field: a sum times 2^84 stays in fp32
 
 template <int D, bool Q8>
 struct Geo {
     static constexpr int KT = D == 64 ? 128 : 64;  // keys of a tile
     static constexpr int REG = D / 64;             // panels of a row
     static constexpr int TILE = REG * KT * kPanel; // bytes of a K or V tile
-    static constexpr int GROUP = KT / 4;           // keys with an exponent of their own: a conversion warp's
+    static constexpr int GROUP = KT / 4;           // keys of a conversion warp
     static constexpr int STAGES = Q8 ? 3 : 4;
     static constexpr int RAW = Q8 ? 3 : 1;         // q8_0 tiles in flight (4 measured 2 to 4 % slower)
     // TMEM columns: S of tile t at KT t, O at 2 KT + D t, P at 2 KT + 2 D + KT / 2 t
@@ -153,10 +157,12 @@ struct alignas(1024) Smem {
     uint64_t k_ready[GG::STAGES], v_ready[GG::STAGES], k_empty[GG::STAGES], v_empty[GG::STAGES];
     uint64_t q_ready[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2];
     uint64_t u_full[kUnits], u_empty[kUnits];
+    uint64_t top_full[2];
     Unit unit[kUnits], no_unit;
-    alignas(16) float ev[GG::STAGES][4];    // Ev of a stage's V, by group of keys
-    // q8_0: 2^Ek of a tile's K, and its blocks that were read.  A K stage is free
-    // before the softmax has looked here; a ring of more than STAGES + 1 is not
+    float ev[GG::STAGES];                  // Ev of a stage's V
+    alignas(16) uint32_t top[2][4];        // largest bf16 value of a tile, by conversion warp
+    // q8_0: 2^Ek of a tile's K, by group of keys, and its blocks that were read.  A K
+    // stage is free before the softmax has looked here; a ring of more than STAGES + 1 is not
     alignas(16) float ek[kMeta][4];
     uint32_t loaded[kMeta];
     uint32_t raw_loaded[GG::RAW];
@@ -350,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int KT = GG::KT, REG = GG::REG, ST = GG::STAGES;
     constexpr bool BF = T::code == NS_BF16;
     constexpr bool SCALED = Q8 || BF;  // V tiles carry an exponent
-    constexpr bool WIDE = BF && !Q8;   // of any size that bf16 has
     constexpr bool Q_TMA = q_by_tma(D, BF);
     extern __shared__ unsigned char smem_raw[];
     Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -384,6 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.p_full[t], kTileWarps);
             mbar_init(&sm.pv_done[t], 1);
         }
+        for (int i = 0; i < 2; ++i)
+            mbar_init(&sm.top_full[i], 4);
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&sm.u_full[i], 1);
             mbar_init(&sm.u_empty[i], kWarps - 1);  // one arrival a warp, but the walk's
@@ -546,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = rt < qt && now->i0 + t * qt + rt < now->n ? low + rt : -1;
             // rows are independent: 32 rows without a token need no weights
             const bool busy = __any_sync(0xffffffffu, pos >= 0 || (rt < qt && now->i0 + t * qt + rt < now->n));
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, o_ev = 0.f;  // O is in units of 2^(m + o_ev)
             for (int j = t0; ok && !busy && j < end; ++j, ++count) {
                 warp_wait(&sm.s_full[t], (uint32_t)count & 1u, ok);
                 warp_arrive(&sm.s_free[t]);
@@ -560,24 +567,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < KT; c += 32)
                     tc::tmem_ld32(s_addr + c, *reinterpret_cast<float(*)[32]>(&sv[c]));
-                // scale of the scores and exponent of the values, by group of keys
-                constexpr int NG = SCALED ? 4 : 1, GK = KT / NG;
-                float sc[NG], ev[NG];
+                // scale of the scores, by group of keys, and exponent of the values; the
+                // weights are summed by groups of four for all but fp16 values (bf16 packed
+                // prompts 78.9 us, 80.2 in one)
+                constexpr int NG = Q8 ? 4 : 1, NS = SCALED ? 4 : 1, GK = KT / NS;
+                const int tile = vtile + j - t0;
+                float sc[NG];
+                const float ev = SCALED ? sm.ev[tile % ST] : 0.f;
                 uint32_t loaded = 0xffffffffu;
                 sc[0] = row_scale;
-                ev[0] = 0.f;
-                if (SCALED) {
-                    const int tile = vtile + j - t0, stage = tile % ST;
-                    const float4 v4 = *reinterpret_cast<const float4 *>(sm.ev[stage]);
-                    const float4 k4 = Q8 ? *reinterpret_cast<const float4 *>(sm.ek[tile % kMeta])
-                                         : make_float4(1.f, 1.f, 1.f, 1.f);
-                    ev[0] = v4.x, ev[NG / 4] = v4.y, ev[NG / 2] = v4.z, ev[NG - 1] = v4.w;
+                if (Q8) {
+                    const float4 k4 = *reinterpret_cast<const float4 *>(sm.ek[tile % kMeta]);
                     const float k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
-                        sc[g] = Q8 ? fmaxf(row_scale * k[g], kTinyScale) : row_scale;
-                    if (Q8)
-                        loaded = sm.loaded[tile % kMeta];
+                        sc[g] = fmaxf(row_scale * k[g], kTinyScale);
+                    loaded = sm.loaded[tile % kMeta];
                 }
                 tc::tmem_ld_wait();
 #pragma unroll
@@ -598,7 +603,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < KT; ++c)
                         sv[c] = (loaded >> (c / 16)) & 1u ? sv[c] : -INFINITY;
                 }
-                float zmax[NG];  // largest score of each group of keys
                 float top = -INFINITY;
                 {
                     float tm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -607,43 +611,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)  // a quarter of the columns each
                             tm[e] = max3(tm[e], sv[e * (KT / 4) + c], sv[e * (KT / 4) + c + 1]);
-                    if (SCALED) {
+                    if (Q8) {
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            zmax[g] = tm[g] * sc[g];
-                            top = fmaxf(top, zmax[g] + ev[g]);
-                        }
+                        for (int g = 0; g < NG; ++g)
+                            top = fmaxf(top, tm[g] * sc[g]);
                     } else {
-                        top = zmax[0] = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * sc[0];
+                        top = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * sc[0];
                     }
                 }
                 // the reference moves to a score that passes it by more than the slack
                 const bool up = top > m + (kLift + kSlack);
                 const float drop = up ? m - (top - kLift) : 0.f;
-                const float alpha = fast_exp2(drop);  // 0 at the first tile
-                const bool moved = up && j > t0;
-                l = WIDE ? times_pow2(l, drop) : l * alpha;
+                l *= fast_exp2(drop);  // 0 at the first tile
                 m = up ? top - kLift : m;
                 const float ref = m > -INFINITY ? m : 0.f;
-                if (WIDE) {
-                    // Values so small beside others that their weights would vanish in fp32
-                    // (zeros, above all) still count in the sum: their exponent is raised
-                    // until they do, which no output notices (2^-100 of it)
-                    float least = zmax[0] + ev[0];
-#pragma unroll
-                    for (int g = 1; g < NG; ++g)
-                        least = fminf(least, zmax[g] + ev[g]);
-                    if (__any_sync(0xffffffffu, least - ref < -100.f)) {
-#pragma unroll
-                        for (int g = 0; g < NG; ++g)
-                            ev[g] = fmaxf(ev[g], ref - 100.f - fmaxf(zmax[g], -1e30f));
-                    }
-                }
                 uint32_t pk[KT / 2];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float nm = ev[g] - ref;
-                    const float2 sc2 = make_float2(sc[g], sc[g]), nm2 = make_float2(nm, nm);
+                for (int g = 0; g < NS; ++g) {
+                    const float2 sc2 = make_float2(sc[g * NG / NS], sc[g * NG / NS]), nm2 = make_float2(-ref, -ref);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int c = g * GK; c < (g + 1) * GK; c += 2) {
@@ -652,15 +637,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], p);
                         pk[c >> 1] = pack2<F16>(p.x, p.y);
                     }
-                    const float ts = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    l += SCALED ? ts * fast_exp2(-ev[g]) : ts;
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 }
 
                 // P is free, and O at rest, once the previous tile's value products are done
                 warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u, ok);
                 tc::fence_after_sync();
+                const bool moved = j > t0 && (up || (SCALED && ev != o_ev));
+                const float fall = SCALED ? drop + (o_ev - ev) : drop;
+                o_ev = ev;
                 if (__any_sync(0xffffffffu, moved)) {
-                    const float f = moved ? alpha : 1.f;
+                    const float f = moved ? fast_exp2(fall) : 1.f;
 #pragma unroll
                     for (int c = 0; c < D; c += 32) {
                         float ov[32];
@@ -696,7 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u, ok);
             tc::fence_after_sync();
             if (u.rec < 0) {
-                const float inv = 1.f / l;  // no weight: the row sees nothing; a NaN is passed on
+                // no weight: the row sees nothing; a NaN is passed on
+                const float inv = SCALED ? pow2((int)o_ev) / l : 1.f / l;
                 uint16_t *out = static_cast<uint16_t *>(a.out) +
                                 ((long long)(u.q0 + tok) * a.num_q_heads + (long long)u.h * G + rg) * D;
 #pragma unroll
@@ -718,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             } else {
-                // a part: unnormalised row, reference and sum, [D / 4][256 rows][4]
+                // a part: unnormalised row, [D / 4][256 rows][4], and its reference and sum, which
+                // take the exponent of the values in
                 float *rec = P.records + (size_t)u.rec * record_floats(D);
                 const int row = t * kRows + r;
 #pragma unroll
@@ -735,8 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (on) {
-                    rec[(size_t)D * 2 * kRows + row] = any ? m : -INFINITY;
-                    rec[(size_t)(D + 1) * 2 * kRows + row] = any ? l : 0.f;
+                    rec[(size_t)D * 2 * kRows + row] = any ? m + o_ev : -INFINITY;
+                    rec[(size_t)(D + 1) * 2 * kRows + row] = any ? (SCALED ? l * pow2(-(int)o_ev) : l) : 0.f;
                 }
             }
             tc::fence_before_sync();
@@ -748,14 +737,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kProducerWarp) {
         // ------------------------------------------------------------ conversion
         regs_shrink<kConvertRegs>();
-        // a warp a group of keys, with exponents of its own, so that the warps do not
-        // wait for each other; a lane a key (D 64) or one panel of a key
+        // a warp a group of keys; a lane a key (D 64) or one panel of a key
         const int group = warp - kConvertWarp;
         const int key = group * GG::GROUP + lane / REG, pan = lane % REG;
         const int panel = pan * (KT * kPanel) + key * kPanel;
         const int turn = (key & 7) ^ (pan << 2);  // order of the chunks: no two of eight lanes share a bank
         int tile = 0;
         for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
+            int most = 0;  // exponent field that the unit's values are laid out for
+            auto raise = [&](int e) { most = e > most ? e + kRoom : most; };
             for (int j = u.t0; ok && j < u.t1; ++j, ++tile) {
                 const int stage = tile % ST;
                 const uint32_t par = (uint32_t)(tile / ST) & 1u;
@@ -772,13 +762,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             top = top16(x[c], top);
                         }
                         top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-                        const int e = max((int)(top >> 7), 45);
-                        const float f = pow2(141 - e);
+                        // the tile's largest value: the warps' own, exchanged
+                        if (lane == 0)
+                            sm.top[tile & 1][group] = top;
+                        __syncwarp();
+                        warp_arrive(&sm.top_full[tile & 1]);
+                        warp_wait(&sm.top_full[tile & 1], (uint32_t)(tile >> 1) & 1u, ok);
+                        const uint4 tops = lds128(sm.top[tile & 1]);
+                        raise(max((int)(max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 7), kLeast));
+                        const float f = pow2(141 - most);
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
                             *reinterpret_cast<uint4 *>(row + ((c ^ turn) << 4)) = bf16_to_f16(x[c], f);
-                        if (lane == 0)
-                            sm.ev[stage][group] = (float)(e - 141);
+                        if (lane == 0 && group == 0)
+                            sm.ev[stage] = (float)(most - 141);
                         fence_async_smem();
                     } else if (!live) {
 #pragma unroll
@@ -796,6 +793,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool have = live && ((loaded >> (key / 16)) & 1u);
                     const uint32_t *scales = reinterpret_cast<const uint32_t *>(raw + 2 * KT * 64);
                     const uint32_t d[2] = {have ? scales[key] : 0u, have ? scales[KT + key] : 0u};
+                    // the tile's largest scale of V, four keys a lane
+                    const int key4 = 4 * lane;
+                    const bool have4 = (loaded >> (key4 / 16)) & 1u;
+                    const uint4 v4 = lds128(scales + KT + key4);
+                    uint32_t vmag = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = (i == 0 ? v4.x : i == 1 ? v4.y : i == 2 ? v4.z : v4.w) & 0x7fff7fffu;
+                        if (have4 && j * KT + key4 + i < u.L)
+                            vmag = __vmaxu2(vmag, w);
+                    }
                     // code chunks in an order in which neither the reads (64-byte rows) nor the
                     // writes (swizzled 128-byte rows) of eight lanes share a bank
                     const int half = (key >> 1) & 3, first = (half << 1) ^ ((half >> 1) * 7);
@@ -807,9 +815,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             code[x][c] = lds128(raw + x * KT * 64 + key * 64 + ((c ^ first) << 4));
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
+                        // the largest scale of these keys' K goes just below 2^8, its codes below
+                        // 2^15; the unit's largest of V so far there or up to 2^kRoom lower
+                        if (x == 1)
+                            raise((int)(__reduce_max_sync(0xffffffffu, max(vmag & 0xffffu, vmag >> 16)) >> 10));
                         const uint32_t mag = d[x] & 0x7fff7fffu;
-                        const int e = (int)(__reduce_max_sync(0xffffffffu, max(mag & 0xffffu, mag >> 16)) >> 10);
-                        // the largest scale goes just below 2^8, its codes below 2^15
+                        const int e = x == 0 ? (int)(__reduce_max_sync(0xffffffffu, max(mag & 0xffffu, mag >> 16)) >> 10) : most;
                         const float2 ds = unpack2<F16>(d[x]);
                         const float f = pow2(22 - e);
                         const __half2 dd[2] = {__float2half2_rn(ds.x * f), __float2half2_rn(ds.y * f)};
@@ -817,8 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 0) {
                             if (x == 0)
                                 sm.ek[tile % kMeta][group] = pow2(e - 22);
-                            else
-                                sm.ev[stage][group] = (float)(e - 22);
+                            else if (group == 0)
+                                sm.ev[stage] = (float)(e - 22);
                             if (x == 0 && group == 0)
                                 sm.loaded[tile % kMeta] = loaded;
                         }
@@ -975,8 +986,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::mma_commit_warp(&sm.q_empty[t]);
                         ++count;
                         if (SCALED) {
-                            // the softmax reads the exponents of this tile's groups, too: they are
-                            // in place when its V is
+                            // the softmax reads the exponents of this tile, too: they are in
+                            // place when its V is
                             warp_wait(&sm.v_ready[ks], kpar, ok);
                             warp_arrive(&sm.s_full[t]);
                         }
