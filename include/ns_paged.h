@@ -575,8 +575,8 @@ ns_status ns_kv_gather_q8_0(const void *k_codes, const void *k_scales, const voi
  * y, then -1; num_accepted[s] = a.  The tokens then follow the target's
  * distribution whatever the drafts were.  Products, sums and comparisons are
  * exact or carry at least 45 bits, so that a value next to a border decides
- * as it does in fp64.  A NaN probability counts as 0; without any positive
- * weight y = -1.  vocab_size is at most 2^30.
+ * as it does in fp64.  A NaN or negative probability, the target's or the
+ * draft's, counts as 0; without any positive weight y = -1.  vocab_size is at most 2^30.
  *
  *   target_probs  float [total_drafts+num_seqs][vocab_size], rows
  *                 target_row_stride elements apart (read)

@@ -38,14 +38,15 @@ struct Pair {
     __device__ __forceinline__ double value() const { return (double)h + (double)l; }
 };
 
-// The weight of a token, exactly max(p - q, 0).  NaN counts as 0.
+// The weight of a token, exactly max(p - q, 0).  NaN counts as 0 in either (fmaxf and
+// fminf return the other operand); with q within [0, p] the difference needs no test.
 __device__ __forceinline__ Pair weight(float p, float q)
 {
+    p = fmaxf(p, 0.f);
+    q = fminf(fmaxf(q, 0.f), p);
     Pair w;
     w.h = p - q;
     w.l = (p - w.h) - q;
-    if (!(w.h > 0.f))
-        w.h = w.l = 0.f;
     return w;
 }
 
@@ -72,15 +73,16 @@ __device__ __forceinline__ float2 sub2(float2 a, float2 b)  // rounds once
     return ffma2(b, make_float2(-1.f, -1.f), a);
 }
 
+template <bool Q>
 __device__ __forceinline__ Pair2 weight(float2 p, float2 q)
 {
+    p = make_float2(fmaxf(p.x, 0.f), fmaxf(p.y, 0.f));
+    if (!Q)
+        return {p, make_float2(0.f, 0.f)};
+    q = make_float2(fminf(fmaxf(q.x, 0.f), p.x), fminf(fmaxf(q.y, 0.f), p.y));
     Pair2 w;
     w.h = sub2(p, q);
     w.l = sub2(sub2(p, w.h), q);
-    if (!(w.h.x > 0.f))
-        w.h.x = w.l.x = 0.f;
-    if (!(w.h.y > 0.f))
-        w.h.y = w.l.y = 0.f;
     return w;
 }
 
@@ -124,8 +126,8 @@ __device__ Pair slice_sum(const Row &r, int lo, int hi, int lane, bool aligned)
                     p[i].z = e == 2 ? 0.f : p[i].z;
                     p[i].w = e == 3 ? 0.f : p[i].w;
                 }
-                sum[0] = sum[0] + weight(make_float2(p[i].x, p[i].y), make_float2(q[i].x, q[i].y));
-                sum[1] = sum[1] + weight(make_float2(p[i].z, p[i].w), make_float2(q[i].z, q[i].w));
+                sum[0] = sum[0] + weight<Q>(make_float2(p[i].x, p[i].y), make_float2(q[i].x, q[i].y));
+                sum[1] = sum[1] + weight<Q>(make_float2(p[i].z, p[i].w), make_float2(q[i].z, q[i].w));
             }
         }
     } else {
@@ -139,7 +141,7 @@ __device__ Pair slice_sum(const Row &r, int lo, int hi, int lane, bool aligned)
             }
 #pragma unroll
             for (int i = 0; i < 4 * kBatch; i += 2)
-                sum[(i >> 1) & 1] = sum[(i >> 1) & 1] + weight(make_float2(p[i], p[i + 1]), make_float2(q[i], q[i + 1]));
+                sum[(i >> 1) & 1] = sum[(i >> 1) & 1] + weight<Q>(make_float2(p[i], p[i + 1]), make_float2(q[i], q[i + 1]));
         }
     }
     const Pair2 both = sum[0] + sum[1];
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
                 off = x < 0 || x >= a.vocab;
                 if (!off) {
                     const double p = a.target[(long long)(first + s + i) * a.target_stride + x];
-                    const double q = a.draft ? (double)a.draft[(long long)(first + i) * a.draft_stride + x] : 1.0;
+                    const double q = a.draft ? (double)fmaxf(a.draft[(long long)(first + i) * a.draft_stride + x], 0.f) : 1.0;
                     ok = (double)a.accept_u[first + i] * q < p;
                 }
             }
