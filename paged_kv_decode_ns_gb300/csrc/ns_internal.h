@@ -70,6 +70,8 @@ struct SpanAttnArgs {
     int max_blocks_per_seq;
     long long num_blocks;
 };
+// SMs of the current device (asked for once a device).
+cudaError_t current_sms(int *sms);
 constexpr int kMaxSpanGroup = 64;  // query heads per kv head
 size_t span_attn_workspace_bytes(int head_dim);
 cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream);

@@ -13,21 +13,28 @@ size_t span_attn_workspace_bytes(int head_dim)
     return span::header_bytes() + 2 * span::kMaxCtas * span::record_floats(head_dim) * sizeof(float);
 }
 
-cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream)
+cudaError_t current_sms(int *sms)
 {
-    static std::atomic<int> known[64];  // SMs of each device
+    static std::atomic<int> known[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    int sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-    if (sms == 0) {
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess)
-            return e;
-        if (dev < 64)
-            known[dev].store(sms, std::memory_order_relaxed);
-    }
+    *sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*sms != 0)
+        return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < 64)
+        known[dev].store(*sms, std::memory_order_relaxed);
+    return e;
+}
+
+cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream)
+{
+    int sms = 0;
+    const cudaError_t e = current_sms(&sms);
+    if (e != cudaSuccess)
+        return e;
     span::Params P;
     P.a = a;
     P.group = a.num_q_heads / a.num_kv_heads;

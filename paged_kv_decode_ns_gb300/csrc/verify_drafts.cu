@@ -29,7 +29,7 @@ namespace ns {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 8, kCtasPerSm = 2;
 constexpr int kBatch = 4;  // 16-byte loads of a row in flight a thread
 
 // h + l, l the rounding error of h.
@@ -198,7 +198,7 @@ __device__ Place find(const Pair *w, int count, int lane, double before, Goal go
     return r;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a, int cluster)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const VerifyArgs a, int cluster)
 {
     __shared__ int sh_state;  // 0: go on, 1: skip the sequence
     __shared__ int sh_accepted;
@@ -381,11 +381,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
 
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t stream)
 {
-    // CTAs for a sequence: as many as run at once (two on an SM), up to a cluster of
-    // eight.  256 sequences of 151936 tokens: one each 54.8 us, two 60.2, four 67.1;
+    // CTAs for a sequence: as many as run at once, up to a cluster of eight.  256 sequences of 151936 tokens: one each 54.8 us, two 60.2, four 67.1;
     // 33 of 50257: eight 10.4 us, sixteen 6 us more.
+    int sms = 0;
+    const cudaError_t e = current_sms(&sms);
+    if (e != cudaSuccess)
+        return e;
     int cluster = kMaxCluster;
-    while (cluster > 1 && (long long)a.num_seqs * cluster > 304)
+    while (cluster > 1 && (long long)a.num_seqs * cluster > kCtasPerSm * sms)
         cluster /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.num_seqs * cluster);
