@@ -105,11 +105,13 @@ struct Geo {
 
 // Q comes by TMA as soon as the scores of the unit before are out, or by the softmax
 // threads, a row each, between two units (1100 to 3500 clocks, of 2400 a tile).  The
-// first is faster at head_dim 128 (8192 bf16 tokens 451 against 480 us, fp16 381 against
-// 394) and for fp16 (mixed chunks over q8_0 32.8 against 33.4, four short prompts 10.2
-// against 10.6; 8192 tokens 137 against 134), the second for bf16 at 64 (packed prompts 86
-// against 92, long chunks over q8_0 156 against 160): there the two query tiles' softmax
-// bounds the call, and the later Q of one keeps them out of step.
+// first against the second, in one run: head_dim 128, fp16, packed prompts 177 against 198
+// us, 8192 tokens 407 against 422, four short prompts 13.8 against 15.4, bf16 packed 214
+// against 222 and 8192 tokens 492 against 485; head_dim 64, fp16, packed 66.9 against 69.4,
+// four short ones 9.4 against 10.3, mixed chunks over q8_0 32.1 against 32.4, 8192 tokens
+// 134.8 against 134.2; bf16 at 64, packed 81.0 against 77.0, four short ones 10.7 against
+// 10.4, 8192 tokens 146.7 against 149.1: many units gain there from the threads, since the
+// two query tiles' softmax bounds the call and the later Q of one keeps them out of step.
 constexpr bool q_by_tma(int D, bool bf16) { return D == 128 || !bf16; }
 
 // A CTA's part of a unit: key tiles [t0, t1).
@@ -310,11 +312,31 @@ __device__ __forceinline__ void hold32(float *v)
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
-// Largest magnitude pattern of the eight 16-bit values of w, both halves.
-__device__ __forceinline__ uint32_t top16(uint4 w, uint32_t t)
+// The larger magnitudes of two pairs of values, with signs of no meaning; a NaN beside
+// a number is left out.
+__device__ __forceinline__ uint32_t larger_bf16(uint32_t a, uint32_t b)
 {
-    constexpr uint32_t kMag = 0x7fff7fffu;
-    return __vmaxu2(__vmaxu2(__vmaxu2(w.x & kMag, w.y & kMag), __vmaxu2(w.z & kMag, w.w & kMag)), t);
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t larger_f16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t larger_bf16(uint4 w, uint32_t t)
+{
+    return larger_bf16(larger_bf16(larger_bf16(w.x, w.y), larger_bf16(w.z, w.w)), t);
+}
+
+// Largest magnitude of a pair.
+__device__ __forceinline__ uint32_t top_of(uint32_t pair)
+{
+    return max(pair & 0x7fffu, (pair >> 16) & 0x7fffu);
 }
 
 // bf16 pair -> fp16 pair of the value times f.
@@ -356,6 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int KT = GG::KT, REG = GG::REG, ST = GG::STAGES;
     constexpr bool BF = T::code == NS_BF16;
     constexpr bool SCALED = Q8 || BF;  // V tiles carry an exponent
+    // The softmax reads that exponent with the scores, which then wait for the tile's V, or
+    // only before it touches O.  The second is faster at head_dim 128, where the conversion
+    // is behind (8192 bf16 tokens 480 us against 488, packed prompts 209 against 214), the
+    // first at 64 (149 against 150, packed 76.9 against 77.1; drafts over q8_0 18.5 against 19.2).
+    constexpr bool LATE = BF && D == 128;
     constexpr bool Q_TMA = q_by_tma(D, BF);
     extern __shared__ unsigned char smem_raw[];
     Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -384,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.q_ready[t], Q_TMA ? 1 : kTileWarps);
             mbar_init(&sm.q_empty[t], 1);
-            mbar_init(&sm.s_full[t], SCALED ? 2 : 1);
+            mbar_init(&sm.s_full[t], LATE ? 1 : SCALED ? 2 : 1);
             mbar_init(&sm.s_free[t], kTileWarps);
             mbar_init(&sm.p_full[t], kTileWarps);
             mbar_init(&sm.pv_done[t], 1);
@@ -528,8 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t m = 0;
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
-                    m = top16(w[c], m);
-                const int e = max((int)(max(m & 0xffffu, m >> 16) >> 7), 15);
+                    m = larger_bf16(w[c], m);
+                const int e = max((int)(top_of(m) >> 7), 15);
                 const float f = pow2(141 - e);
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
@@ -573,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int NG = Q8 ? 4 : 1, NS = SCALED ? 4 : 1, GK = KT / NS;
                 const int tile = vtile + j - t0;
                 float sc[NG];
-                const float ev = SCALED ? sm.ev[tile % ST] : 0.f;
+                float ev = SCALED && !LATE ? sm.ev[tile % ST] : 0.f;
                 uint32_t loaded = 0xffffffffu;
                 sc[0] = row_scale;
                 if (Q8) {
@@ -641,7 +668,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 
                 // P is free, and O at rest, once the previous tile's value products are done
-                warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u, ok);
+                if (LATE) {
+                    warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u, &sm.v_ready[tile % ST],
+                              (uint32_t)(tile / ST) & 1u, ok);
+                    ev = sm.ev[tile % ST];
+                } else {
+                    warp_wait(&sm.pv_done[t], (uint32_t)(count - 1) & 1u, ok);
+                }
                 tc::fence_after_sync();
                 const bool moved = j > t0 && (up || (SCALED && ev != o_ev));
                 const float fall = SCALED ? drop + (o_ev - ev) : drop;
@@ -759,9 +792,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             x[c] = live ? lds128(row + ((c ^ turn) << 4)) : make_uint4(0u, 0u, 0u, 0u);
-                            top = top16(x[c], top);
+                            top = larger_bf16(x[c], top);
                         }
-                        top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+                        top = __reduce_max_sync(0xffffffffu, top_of(top));
                         // the tile's largest value: the warps' own, exchanged
                         if (lane == 0)
                             sm.top[tile & 1][group] = top;
@@ -793,17 +826,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool have = live && ((loaded >> (key / 16)) & 1u);
                     const uint32_t *scales = reinterpret_cast<const uint32_t *>(raw + 2 * KT * 64);
                     const uint32_t d[2] = {have ? scales[key] : 0u, have ? scales[KT + key] : 0u};
-                    // the tile's largest scale of V, four keys a lane
+                    // the tile's largest scale of V, four keys a lane (those that are there)
                     const int key4 = 4 * lane;
-                    const bool have4 = (loaded >> (key4 / 16)) & 1u;
-                    const uint4 v4 = lds128(scales + KT + key4);
-                    uint32_t vmag = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = (i == 0 ? v4.x : i == 1 ? v4.y : i == 2 ? v4.z : v4.w) & 0x7fff7fffu;
-                        if (have4 && j * KT + key4 + i < u.L)
-                            vmag = __vmaxu2(vmag, w);
+                    const int there = (loaded >> (key4 / 16)) & 1u ? u.L - j * KT - key4 : 0;
+                    uint4 w4 = lds128(scales + KT + key4);
+                    if (there < 4) {
+                        w4.w = 0u;
+                        w4.z = there > 2 ? w4.z : 0u;
+                        w4.y = there > 1 ? w4.y : 0u;
+                        w4.x = there > 0 ? w4.x : 0u;
                     }
+                    const uint32_t vmag = larger_f16(larger_f16(w4.x, w4.y), larger_f16(w4.z, w4.w));
                     // code chunks in an order in which neither the reads (64-byte rows) nor the
                     // writes (swizzled 128-byte rows) of eight lanes share a bank
                     const int half = (key >> 1) & 3, first = (half << 1) ^ ((half >> 1) * 7);
@@ -818,9 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // the largest scale of these keys' K goes just below 2^8, its codes below
                         // 2^15; the unit's largest of V so far there or up to 2^kRoom lower
                         if (x == 1)
-                            raise((int)(__reduce_max_sync(0xffffffffu, max(vmag & 0xffffu, vmag >> 16)) >> 10));
-                        const uint32_t mag = d[x] & 0x7fff7fffu;
-                        const int e = x == 0 ? (int)(__reduce_max_sync(0xffffffffu, max(mag & 0xffffu, mag >> 16)) >> 10) : most;
+                            raise((int)(__reduce_max_sync(0xffffffffu, top_of(vmag)) >> 10));
+                        const int e = x == 0 ? (int)(__reduce_max_sync(0xffffffffu, top_of(d[0])) >> 10) : most;
                         const float2 ds = unpack2<F16>(d[x]);
                         const float f = pow2(22 - e);
                         const __half2 dd[2] = {__float2half2_rn(ds.x * f), __float2half2_rn(ds.y * f)};
@@ -985,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (Q_TMA && i == mine - 1)
                             tc::mma_commit_warp(&sm.q_empty[t]);
                         ++count;
-                        if (SCALED) {
+                        if (SCALED && !LATE) {
                             // the softmax reads the exponents of this tile, too: they are in
                             // place when its V is
                             warp_wait(&sm.v_ready[ks], kpar, ok);
