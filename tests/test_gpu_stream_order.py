@@ -145,3 +145,60 @@ def test_the_prefill_alone_is_right(prefill):
         want = w @ v[:, j // 7]
         _gpu.compare(prefill.out[0, j], want.cpu().numpy(), wl.F16, "long row")
     _gpu.assert_no_device_status()
+
+
+def calls():
+    """Each entry point on inputs of its own: (call, the buffers it reads that a copy can fill, outputs)."""
+    g = torch.Generator().manual_seed(9)
+    q, k, v = (torch.randn(700, h, D, generator=g).half().cuda() for h in (HQ, HKV, HKV))
+    out, ws, starts = torch.empty_like(q), nb.alloc_span_workspace(64), _gpu.dev_ints([0, 600, 700], np.int32)
+    yield "prompt", lambda: nb.ns_prompt_attn(q, k, v, starts, 0.125, out, ws), q, [out]
+    c = Chunks([(2, 40), (1, 900)], wl.BF16, HQ, HKV, seed=10)
+    yield "chunk", c.call, c.q, [c.out]
+    p = Pool16([10, 11], HKV, 16, D, seed=11)
+    kp, vp, t = _gpu.to_dev(p.k, wl.F16), _gpu.to_dev(p.v, wl.F16), _gpu.dev_ints(p.tables, np.int32)
+    ko, vo = (torch.zeros(21, HKV, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    gs = _gpu.dev_ints([0, 10, 21], np.int32)
+    yield "gather", lambda: nb.ns_kv_gather(kp, vp, t, gs, ko, vo), kp, [ko, vo]
+    d = Drafts([3] * 4, 500, seed=12).dev()
+    tokens, num = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (16, 4))
+    yield "verify", lambda: nb.ns_verify_drafts(*d, tokens, num), d[0], [tokens, num]
+
+
+@pytest.mark.parametrize("front", ["copy", "memset", "join", "nothing"])
+def test_captured_behind_other_nodes(front):
+    """A captured call whose input comes from a copy, or that stands behind a memset, or where two streams
+    join, or first in its graph."""
+    for what, call, src, outs in calls():
+        call()
+        torch.cuda.synchronize()
+        want, kept = [o.clone() for o in outs], src.clone()
+        side = torch.cuda.Stream()
+        big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            main = torch.cuda.current_stream()
+            if front == "copy":
+                big[:1 << 27].copy_(big[1 << 27:])
+                src.copy_(kept)
+            elif front == "memset":
+                outs[0].view(torch.uint8).zero_()
+            elif front == "join":
+                side.wait_stream(main)
+                with torch.cuda.stream(side):
+                    big.fill_(1)
+                    src.copy_(kept)
+                outs[0].fill_(0)
+                main.wait_stream(side)
+            call()
+        for _ in range(2):
+            if front in ("copy", "join"):
+                src.zero_()
+            for o in outs:
+                o.fill_(5)
+            graph.replay()
+            torch.cuda.synchronize()
+            for o, w in zip(outs, want):
+                assert torch.equal(o.view(torch.int16), w.view(torch.int16)), (what, front)
+            src.copy_(kept)
+    _gpu.assert_no_device_status()
