@@ -181,12 +181,12 @@ ns_status ns_paged_attn_decode(const void *q, const void *k_pool, const void *v_
  *   overlap_prologue    nonzero = launch as a programmatic dependent of the
  *                       kernel before it on the stream (CUDA programmatic
  *                       dependent launch): the decode may start while that
- *                       kernel drains, reads context_lens and block_tables,
- *                       then waits for it to finish before it touches q, the
- *                       pools, k_new/v_new, slot_mapping, out or the
+ *                       kernel drains, reads context_lens, block_tables and
+ *                       slot_mapping, then waits for it to finish before it
+ *                       touches q, the pools, k_new/v_new, out or the
  *                       workspace.  The caller guarantees that the kernel just
- *                       before it on the stream does not write context_lens or
- *                       block_tables.  It also lets the kernel after it start
+ *                       before it on the stream does not write context_lens,
+ *                       block_tables or slot_mapping.  It also lets the kernel after it start
  *                       early.  Not a policy override: the split stays automatic.
  *   wait_limit_ns       0 = default (about one second); else the limit, in ns, of
  *                       each wait of a computing warp for its next K/V step.  On
@@ -537,7 +537,8 @@ ns_status ns_paged_attn_prefill_q8_0(const void *q, const int32_t *query_start_l
  *                they were
  *   k_out, v_out [total_tokens][num_kv_heads][head_dim], dense (written)
  * A sequence whose entries break that order is skipped
- * (NS_DEV_BAD_QUERY_SPAN), one with more tokens than its table row holds too
+ * (NS_DEV_BAD_QUERY_SPAN; rows of sequences beside it may then be left out as
+ * well), one with more tokens than its table row holds too
  * (NS_DEV_BAD_CONTEXT_LEN); the rows of a block id outside the pool are left
  * as they were (NS_DEV_BAD_BLOCK_ID).
  */
@@ -573,9 +574,10 @@ ns_status ns_kv_gather_q8_0(const void *k_codes, const void *k_scales, const voi
  *   y = the smallest v with w(0) + .. + w(v) > sample_uniforms[s] * sum w
  * The packed rows draft_start_loc[s]+s .. +n of out_tokens get x_0 .. x_{a-1},
  * y, then -1; num_accepted[s] = a.  The tokens then follow the target's
- * distribution whatever the drafts were.  Products, sums and comparisons are
- * exact or carry at least 45 bits, so that a value next to a border decides
- * as it does in fp64.  A NaN or negative probability, the target's or the
+ * distribution whatever the drafts were.  Products, weights and comparisons are
+ * exact and sums are pairs of floats (relative error 2^-45 at 151936 tokens, 2^-40
+ * at 2^23), so that a value decides as it does in fp64 unless it is as near to a
+ * border as that.  A NaN or negative probability, the target's or the
  * draft's, counts as 0; without any positive weight y = -1.  vocab_size is at most 2^30.
  *
  *   target_probs  float [total_drafts+num_seqs][vocab_size], rows
@@ -590,6 +592,8 @@ ns_status ns_kv_gather_q8_0(const void *k_codes, const void *k_scales, const voi
  *                 <= total_drafts (read)
  *   accept_uniforms, sample_uniforms  float [total_drafts], [num_seqs], in
  *                 [0, 1) (read)
+ * The rows may lie at any element; the tensors' first elements are 16-byte
+ * aligned, as those of every pointer.
  * A sequence whose entries of draft_start_loc break that is skipped
  * (NS_DEV_BAD_QUERY_SPAN); one with a drafted token outside the vocabulary
  * gets -1 everywhere (NS_DEV_BAD_TOKEN).

@@ -45,8 +45,8 @@ __device__ __forceinline__ uint4 dequantise(uint4 w)
 // A CTA copies `tokens` packed rows.  Its first threads look their rows up (owner,
 // table entry) once; then a thread moves 16 bytes of K and of V (8 elements) at a
 // time, kBatch of them loaded before the first is stored.  Bound by memory once
-// the rows fill the GPU: 256 sequences of q8_0 (381 MB) 62.7 us, 6.1 TB/s; 32 of
-// 16 bits at head_dim 128 (165 MB) 27.9 us, 5.9 TB/s.  (A thread that looked its own
+// the rows fill the GPU: 256 sequences of q8_0 (381 MB) 62.1 us, 6.1 TB/s; 32 of
+// 16 bits at head_dim 128 (165 MB) 27.5 us, 6.0 TB/s.  (A thread that looked its own
 // row up and divided by the heads for every 16 bytes: 4.1 and 5.0 TB/s.)  Five CTAs an
 // SM cap the registers at 48: 66.0 us at four, 90.8 at six, which spills.
 constexpr int kBatch = 4;

@@ -39,12 +39,13 @@
 // half of it the output's own rounding; two products for each would undo that at
 // twice the tensor work.  Everything else (scores, sums, O) is fp32.
 //
-// What bounds it.  At head_dim 128 the tensor cores: 8192 tokens, 32 / 8 heads, 398 us,
-// 1.38 PFLOP/s, 75% of the measured peak.  At head_dim 64 the softmax: a pair of 128 x
+// What bounds it.  At head_dim 128 the tensor cores: 8192 fp16 tokens, 32 / 8 heads, 397 us,
+// 1.38 PFLOP/s, 75% of the measured peak (394 to 411 us on different GPUs); bf16 470 us, its
+// conversion of V on top.  At head_dim 64 the softmax: a pair of 128 x
 // 128 tiles takes ~2370 clocks, against 1050 of products and 1024 of exponentials; two
 // softmax warps a scheduler issue half of the time and wait on TMEM, barriers and
-// each other's use of the exponential unit for the rest (137 us for 8192 fp16 tokens of
-// 14 / 2 heads, 0.88 PFLOP/s; bf16 152 us, its exponents by group on top).  Short
+// each other's use of the exponential unit for the rest (135 us for 8192 fp16 tokens of
+// 14 / 2 heads, 0.90 PFLOP/s; bf16 148 us, its conversion on top).  Short
 // calls: launch, the plan, one unit's chain of copy, product, softmax, product and
 // the join (four prompts of up to 200 tokens 10 us; 32 spans of drafts 19 us).
 //

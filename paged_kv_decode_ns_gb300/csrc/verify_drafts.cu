@@ -12,14 +12,15 @@
 // goal falls into reads that run again, a stretch a warp, and one warp narrows the
 // stretch down to the token.  One pass over one row of p and one of q is all the
 // memory traffic and bounds a large batch: 256 sequences of 151936 tokens (311 MB)
-// 54.8 us, 5.7 TB/s.  Four sequences take 11 us, a chain of dependent reads.
+// 54.0 us, 5.8 TB/s.  Four sequences take 10.6 us, a chain of dependent reads.
 //
 // Precision: neighbouring cumulative weights differ by single probabilities, so
 // fp32 sums would move the drawn token.  fp64 additions (about two a clock on an SM)
 // would cost more than the memory pass (one CTA a sequence with fp64 sums: 798 us
 // for 256 sequences of 151936 tokens); here w is split exactly into a float and its
-// rounding error (w > 0 implies p > q >= 0, so (p - s) - q is exact) and sums are
-// pairs of floats (48 bits).  fp64 joins the few sums that are compared.
+// rounding error (0 <= q <= p, so (p - w) - q is exact) and sums are pairs of
+// floats (a run's is off by 2^-45 of itself at 151936 tokens, 2^-40 at 2^23, by
+// emulation).  fp64 joins the few sums that are compared.
 #include "ns_common.cuh"
 #include "ns_internal.h"
 #include "tcgen05.cuh"
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
 
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t stream)
 {
-    // CTAs for a sequence: as many as run at once, up to a cluster of eight.  256 sequences of 151936 tokens: one each 54.8 us, two 60.2, four 67.1;
+    // CTAs for a sequence: as many as run at once, up to a cluster of eight.  256 sequences of 151936 tokens: one each 54 us, two 60, four 67;
     // 33 of 50257: eight 10.4 us, sixteen 6 us more.
     int sms = 0;
     const cudaError_t e = current_sms(&sms);
