@@ -27,7 +27,7 @@
  *               must stay valid until the work completes.
  *  Elements     K, V, q and out are fp16 or bf16 (`ns_dtype`), all of one type.
  *  Shapes       head_dim is 64, or 128 with block_size 16 (the q8_0 pools
- *               and the allocation-free entry point take 64).
+ *               and the allocation-free entry point take 64; q4_0 pools both).
  *               num_q_heads must be a multiple of num_kv_heads; query head
  *               j reads KV head j / G, G = num_q_heads / num_kv_heads.  G is
  *               at most 8, or up to 64 when it is a multiple of
@@ -89,6 +89,7 @@ typedef enum ns_dtype { NS_F16 = 0, NS_BF16 = 1 } ns_dtype;
 #define NS_DEV_BAD_QUERY_SPAN 0x20u  /* prefill: query span longer than the context, or negative */
 #define NS_DEV_MERGE_QUEUE 0x40u     /* decode: a CTA's merge queue overflowed (a merge was skipped) */
 #define NS_DEV_BAD_TOKEN 0x80u       /* verification: a drafted token outside [0, vocab_size) */
+#define NS_DEV_BAD_POSITION 0x100u   /* rotary append: a position outside [0, max_positions) */
 
 /* Human-readable name of a status code (static string). */
 const char *ns_status_string(ns_status status);
@@ -446,8 +447,8 @@ ns_status ns_kv_append_paged_attn_decode_q8_0(const void *q, const void *k_new, 
                                              size_t workspace_bytes);
 
 /*
- * Workspace of the span attention calls (ns_prompt_attn and
- * ns_paged_attn_prefill_q8_0): partial rows of the query tiles that were cut
+ * Workspace of the span attention calls (ns_prompt_attn,
+ * ns_paged_attn_prefill_q8_0 and _q4_0): partial rows of the query tiles that were cut
  * across CTAs.  Its size depends on head_dim alone (64 or 128; 0 for others),
  * its contents need no initialisation and carry nothing from one call to the
  * next.  Two calls that share a workspace must not run concurrently, nor may
@@ -603,6 +604,146 @@ ns_status ns_verify_drafts(const float *target_probs, const float *draft_probs, 
                            const float *sample_uniforms, int num_seqs, int total_drafts, int vocab_size,
                            int64_t target_row_stride, int64_t draft_row_stride, int32_t *out_tokens,
                            int32_t *num_accepted, ns_stream_t stream);
+
+/*
+ * 4-bit (q4_0) KV cache, a quarter of the 16-bit cache's elements and an eighth more
+ * for the scales (36 bytes a 64-wide row instead of 128).  In the q4_0 block format:
+ *   - a block is 32 consecutive elements of one token's head row; m is its element
+ *     of largest magnitude (of +a and -a the positive one);
+ *   - its step d = -m / 8 in fp32 is stored as fp16 (nearest even, saturating at
+ *     65504);
+ *   - code = min(15, floor(x * (1/d) + 8.5)), every step rounded to fp32; the code
+ *     c stands for fp16(d) * (c - 8).  So m is code 0;
+ *   - a block whose step fp16 rounds to 0 has all codes 8 (value 0); one that holds
+ *     an infinity or NaN has the step NaN and all codes 8.
+ * Pools: k_codes, v_codes uint8 [num_blocks][num_kv_heads][block_size]
+ * [head_dim / 2], byte j of a row holding element 2j in its low four bits and
+ * 2j + 1 in its high ones; k_scales, v_scales fp16 [num_blocks][num_kv_heads]
+ * [block_size][head_dim / 32].  All four 16-byte aligned.  head_dim 64, or 128
+ * with block_size 16.
+ */
+
+/*
+ * ns_kv_append_q4_0 -- ns_kv_append into a q4_0 pool: each new token's K and V
+ * rows (fp16 or bf16, [num_tokens][num_kv_heads][head_dim]) are quantised as
+ * above and written at slot_mapping (negative: skipped; outside the pool:
+ * skipped, NS_DEV_BAD_SLOT).  Codes and steps match the definition bit for bit.
+ */
+ns_status ns_kv_append_q4_0(const void *k, const void *v, const int64_t *slot_mapping, void *k_codes,
+                            void *k_scales, void *v_codes, void *v_scales, int num_tokens, int num_kv_heads,
+                            int head_dim, int block_size, int64_t num_blocks, ns_dtype dtype,
+                            ns_stream_t stream);
+
+/*
+ * ns_kv_gather_q4_0 -- ns_kv_gather from a q4_0 pool: each value is fp16(d) *
+ * (code - 8) rounded once to dtype.
+ */
+ns_status ns_kv_gather_q4_0(const void *k_codes, const void *k_scales, const void *v_codes,
+                            const void *v_scales, const int32_t *block_tables, const int32_t *start_loc,
+                            int num_seqs, int total_tokens, int num_kv_heads, int head_dim,
+                            int block_size, void *k_out, void *v_out, ns_stream_t stream,
+                            int max_blocks_per_seq, int64_t num_blocks, ns_dtype dtype);
+
+/*
+ * ns_paged_attn_decode_q4_0 -- ns_paged_attn_decode over a q4_0 pool: the same
+ * definition with K_s[p] and V_s[p] the dequantised rows (fp16(d) * (code - 8)).
+ * block_size 4, 8, 16 or 32 (head_dim 128: 16); num_q_heads / num_kv_heads any
+ * whole number up to 64.  workspace: as for ns_paged_attn_decode
+ * (ns_paged_attn_workspace_bytes, zero-filled once; the same workspace serves
+ * both), whose plan record this call leaves alone.  A context length that is
+ * negative or beyond the table row counts as 0 or as the row's tokens
+ * (NS_DEV_BAD_CONTEXT_LEN); tokens of a block id outside the pool are left out
+ * (NS_DEV_BAD_BLOCK_ID).  q is rounded to fp16 for the product, scaled by a power
+ * of two first (off by at most 2^-39 of the row's largest element), and so is each
+ * softmax weight times its step of V (off by 2^-11 of itself, or 2^-32 of the largest
+ * weight times the largest step); scores, sums and outputs are fp32 until the last rounding.  A NaN
+ * step reaches the rows that see its token.
+ */
+ns_status ns_paged_attn_decode_q4_0(const void *q, const void *k_codes, const void *k_scales,
+                                    const void *v_codes, const void *v_scales,
+                                    const int32_t *block_tables, const int32_t *context_lens, int num_seqs,
+                                    int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                    float scale, void *out, ns_stream_t stream, int max_blocks_per_seq,
+                                    int64_t num_blocks, ns_dtype dtype, void *workspace,
+                                    size_t workspace_bytes);
+
+/*
+ * ns_paged_attn_prefill_q4_0 -- ns_paged_attn_prefill_q8_0 over a q4_0 pool, with
+ * the same shapes (head_dim 64, block_size 16), checks and workspace.  (At head_dim
+ * 128 the cached rows come back through ns_kv_gather_q4_0, and ns_prompt_attn
+ * takes them as the prefix.)  Scales far below the largest of the sequence and kv
+ * head lose bits as there (their values are off by up to 2^-32 of the largest value).
+ */
+ns_status ns_paged_attn_prefill_q4_0(const void *q, const int32_t *query_start_loc, const void *k_codes,
+                                     const void *k_scales, const void *v_codes, const void *v_scales,
+                                     const int32_t *block_tables, const int32_t *context_lens,
+                                     int num_seqs, int total_q_tokens, int num_q_heads,
+                                     int num_kv_heads, int head_dim, int block_size, float scale,
+                                     void *out, ns_stream_t stream, int max_blocks_per_seq,
+                                     int64_t num_blocks, ns_dtype dtype, void *workspace,
+                                     size_t workspace_bytes);
+
+/*
+ * ns_rope_kv_append -- the rotation of the new tokens' queries and keys by their
+ * positions, and ns_kv_append of the rotated keys and the values, in one pass over
+ * the rows of a fused projection.
+ *
+ * For token t with slot_mapping[t] >= 0 at position p = positions[t], with
+ * c_i = cos_sin[p][i] and s_i = cos_sin[p][rotary_dim/2 + i], i = 0 ..
+ * rotary_dim/2 - 1, the pair (x, y) of elements (i, i + rotary_dim/2) of every
+ * query and key head, or (2i, 2i + 1) when `interleaved` is nonzero, becomes
+ *   (x c_i - y s_i, y c_i + x s_i);
+ * elements from rotary_dim on pass unchanged.  Products and sums are rounded to
+ * fp32 each, then
+ *   q_out[t], k_out[t] and the 16-bit pool's row: once to dtype
+ *   q8_0, q4_0 pools: codes and scales of the fp32 values, bit for bit
+ * A negative slot marks a padding token: nothing of it is read or written.  A
+ * token whose slot lies outside the pool (NS_DEV_BAD_SLOT) or whose position lies
+ * outside [0, max_positions) (NS_DEV_BAD_POSITION) is skipped in the same way.  Two
+ * tokens with the same slot race (one of them wins, row by row).
+ *
+ *   q, k, v     [num_tokens][heads][head_dim], rows q_row_stride, k_row_stride and
+ *               v_row_stride elements apart (read): slices of a fused projection
+ *               need no copy
+ *   positions   int32 [num_tokens] (read)
+ *   cos_sin     float [max_positions][rotary_dim], dense (read)
+ *   q_out       rows q_out_row_stride apart (written); k_out the same with
+ *               k_out_row_stride, or NULL when only the cache takes the rotated
+ *               keys.  q_out may be q, and k_out k, at the same stride: the rows
+ *               are then rotated in place.  No other overlap is allowed.
+ *   pools       as in ns_kv_append, ns_kv_append_q8_0 and ns_kv_append_q4_0
+ *               (written)
+ * Strides are multiples of 8 and at least the heads' width.  rotary_dim is a
+ * multiple of 16, 16 .. head_dim.  num_q_heads need not be a multiple of
+ * num_kv_heads.  head_dim is 64, or 128 with block_size 16 (q8_0 pools: 64).
+ */
+ns_status ns_rope_kv_append(const void *q, const void *k, const void *v, const int32_t *positions,
+                            const float *cos_sin, const int64_t *slot_mapping, void *q_out, void *k_out,
+                            void *k_pool, void *v_pool, int num_tokens, int num_q_heads, int num_kv_heads,
+                            int head_dim, int rotary_dim, int interleaved, int max_positions,
+                            int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                            int64_t q_out_row_stride, int64_t k_out_row_stride, int block_size,
+                            int64_t num_blocks, ns_dtype dtype, ns_stream_t stream);
+
+/* ns_rope_kv_append into a q8_0 pool (head_dim 64). */
+ns_status ns_rope_kv_append_q8_0(const void *q, const void *k, const void *v, const int32_t *positions,
+                                 const float *cos_sin, const int64_t *slot_mapping, void *q_out, void *k_out,
+                                 void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                                 int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int rotary_dim, int interleaved, int max_positions, int64_t q_row_stride,
+                                 int64_t k_row_stride, int64_t v_row_stride, int64_t q_out_row_stride,
+                                 int64_t k_out_row_stride, int block_size, int64_t num_blocks,
+                                 ns_dtype dtype, ns_stream_t stream);
+
+/* ns_rope_kv_append into a q4_0 pool. */
+ns_status ns_rope_kv_append_q4_0(const void *q, const void *k, const void *v, const int32_t *positions,
+                                 const float *cos_sin, const int64_t *slot_mapping, void *q_out, void *k_out,
+                                 void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                                 int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int rotary_dim, int interleaved, int max_positions, int64_t q_row_stride,
+                                 int64_t k_row_stride, int64_t v_row_stride, int64_t q_out_row_stride,
+                                 int64_t k_out_row_stride, int block_size, int64_t num_blocks,
+                                 ns_dtype dtype, ns_stream_t stream);
 
 /*
  * Device status word of the current device: OR of NS_DEV_* bits raised by

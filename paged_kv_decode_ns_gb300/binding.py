@@ -32,6 +32,7 @@ DEV_BITS = {
     0x20: "NS_DEV_BAD_QUERY_SPAN",
     0x40: "NS_DEV_MERGE_QUEUE",
     0x80: "NS_DEV_BAD_TOKEN",
+    0x100: "NS_DEV_BAD_POSITION",
 }
 
 
@@ -92,6 +93,13 @@ _SIGNATURES = {
     "ns_paged_attn_prefill_q8_0": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, I, I64, I, P, SZ]),
     "ns_kv_gather": (I, [P, P, P, P, I, I, I, I, I, P, P, P, I, I64, I]),
     "ns_kv_gather_q8_0": (I, [P, P, P, P, P, P, I, I, I, I, I, P, P, P, I, I64, I]),
+    "ns_kv_append_q4_0": (I, [P, P, P, P, P, P, P, I, I, I, I, I64, I, P]),
+    "ns_kv_gather_q4_0": (I, [P, P, P, P, P, P, I, I, I, I, I, P, P, P, I, I64, I]),
+    "ns_paged_attn_prefill_q4_0": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, I, I64, I, P, SZ]),
+    "ns_paged_attn_decode_q4_0": (I, [P, P, P, P, P, P, P, I, I, I, I, I, F, P, P, I, I64, I, P, SZ]),
+    "ns_rope_kv_append": (I, [P] * 10 + [I] * 7 + [I64] * 5 + [I, I64, I, P]),
+    "ns_rope_kv_append_q8_0": (I, [P] * 12 + [I] * 7 + [I64] * 5 + [I, I64, I, P]),
+    "ns_rope_kv_append_q4_0": (I, [P] * 12 + [I] * 7 + [I64] * 5 + [I, I64, I, P]),
     "ns_verify_drafts": (I, [P, P, P, P, P, P, I, I, I, I64, I64, P, P, P]),
 }
 
@@ -213,7 +221,7 @@ class PreparedCall:
 def prepare(fn, *args, **kwargs) -> PreparedCall:
     """``fn`` (a launching entry point of this module: ns_kv_append,
     ns_paged_attn_decode, ns_kv_append_paged_attn_decode, ns_paged_attn_prefill,
-    a q8_0 one, ns_prompt_attn, ns_kv_gather or ns_verify_drafts) with these
+    a q8_0 or q4_0 one, ns_rope_kv_append, ns_prompt_attn, ns_kv_gather or ns_verify_drafts) with these
     arguments, checked now and run by calling the returned object.  It is what a
     serving loop that calls the same step on the same buffers every iteration
     uses, so that a call costs the host one foreign call."""
@@ -430,7 +438,7 @@ def ns_span_attn_workspace_bytes(head_dim: int = 64) -> int:
 
 
 def alloc_span_workspace(head_dim: int = 64, device=None) -> torch.Tensor:
-    """A workspace for ns_prompt_attn and ns_paged_attn_prefill_q8_0 (its contents need no initialisation)."""
+    """A workspace for ns_prompt_attn and ns_paged_attn_prefill_q8_0 and _q4_0 (its contents need no initialisation)."""
     return torch.empty(ns_span_attn_workspace_bytes(head_dim), dtype=torch.uint8, device=device or "cuda")
 
 
@@ -515,6 +523,127 @@ def ns_kv_gather_q8_0(k_codes, k_scales, v_codes, v_scales, block_tables, start_
                  _dev(start_loc, "start_loc", torch.int32), S, T, hkv, d, bs, _dev(k_out, "k_out"),
                  _dev(v_out, "v_out"), _stream(stream), width, nb, _dtype_code(k_out))
     _check(st, "ns_kv_gather_q8_0")
+
+
+def _q4_pools(k_codes, k_scales, v_codes, v_scales):
+    codes = k_codes.shape
+    nb, hkv, bs, half = codes
+    if v_codes.shape != codes or k_scales.shape != (nb, hkv, bs, half // 16) or v_scales.shape != k_scales.shape:
+        raise ValueError("q4_0 pools: codes [NB, Hkv, bs, D/2] uint8, scales [NB, Hkv, bs, D/32] fp16")
+    return (nb, hkv, bs, 2 * half, _dev(k_codes, "k_codes", torch.uint8), _dev(k_scales, "k_scales", torch.float16),
+            _dev(v_codes, "v_codes", torch.uint8), _dev(v_scales, "v_scales", torch.float16))
+
+
+def ns_kv_append_q4_0(k, v, slot_mapping, k_codes, k_scales, v_codes, v_scales, stream=None):
+    """Quantise k/v [T, Hkv, D] to q4_0 and write codes and scales at slot_mapping [T] (int64)."""
+    T, hkv, d = k.shape
+    nb, hkv2, bs, d2, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    if v.shape != k.shape or hkv2 != hkv or d2 != d or slot_mapping.shape != (T,):
+        raise ValueError("shape mismatch")
+    st = _invoke("ns_kv_append_q4_0", _dev(k, "k"), _dev(v, "v", k.dtype),
+                 _dev(slot_mapping, "slot_mapping", torch.int64), kc, ks, vc, vs, T, hkv, d,
+                 bs, nb, _dtype_code(k), _stream(stream))
+    _check(st, "ns_kv_append_q4_0")
+
+
+def ns_kv_gather_q4_0(k_codes, k_scales, v_codes, v_scales, block_tables, start_loc, k_out, v_out, stream=None):
+    """ns_kv_gather from a q4_0 pool: the dequantised rows, rounded to k_out's type."""
+    nb, hkv, bs, d, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    S, width, T, _ = _gather_shapes(hkv, d, block_tables, start_loc, k_out, v_out)
+    st = _invoke("ns_kv_gather_q4_0", kc, ks, vc, vs, _dev(block_tables, "block_tables", torch.int32),
+                 _dev(start_loc, "start_loc", torch.int32), S, T, hkv, d, bs, _dev(k_out, "k_out"),
+                 _dev(v_out, "v_out"), _stream(stream), width, nb, _dtype_code(k_out))
+    _check(st, "ns_kv_gather_q4_0")
+
+
+def ns_paged_attn_decode_q4_0(q, k_codes, k_scales, v_codes, v_scales, block_tables, context_lens, scale, out,
+                              workspace, stream=None):
+    """Decode attention of q [S, Hq, D] over a q4_0 pool; the workspace is alloc_workspace's."""
+    rows, tables = q.shape, block_tables.shape
+    S, hq, d = rows
+    nb, hkv, bs, d2, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    if d2 != d or out.shape != rows or context_lens.shape != (S,) or len(tables) != 2 or tables[0] != S:
+        raise ValueError("shape mismatch")
+    dtype = q.dtype
+    st = _invoke("ns_paged_attn_decode_q4_0",
+                 _dev(q, "q"), kc, ks, vc, vs, _dev(block_tables, "block_tables", torch.int32),
+                 _dev(context_lens, "context_lens", torch.int32), S, hq, hkv, d, bs, float(scale),
+                 _dev(out, "out", dtype), _stream(stream), tables[1], nb, _dtype_code(q),
+                 _dev(workspace, "workspace", torch.uint8), workspace.numel())
+    _check(st, "ns_paged_attn_decode_q4_0")
+
+
+def ns_paged_attn_prefill_q4_0(q, query_start_loc, k_codes, k_scales, v_codes, v_scales, block_tables,
+                               context_lens, scale, out, workspace, stream=None):
+    """Attention of the query spans ``query_start_loc`` over a q4_0 pool (head_dim 64, block size 16); the
+    workspace is alloc_span_workspace's."""
+    rows, tables = q.shape, block_tables.shape
+    T, hq, d = rows
+    nb, hkv, bs, d2, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    S = context_lens.shape[0]
+    if d2 != d or out.shape != rows or query_start_loc.shape != (S + 1,) or len(tables) != 2 or tables[0] != S:
+        raise ValueError("shape mismatch")
+    st = _invoke("ns_paged_attn_prefill_q4_0",
+                 _dev(q, "q"), _dev(query_start_loc, "query_start_loc", torch.int32), kc, ks, vc, vs,
+                 _dev(block_tables, "block_tables", torch.int32), _dev(context_lens, "context_lens", torch.int32),
+                 S, T, hq, hkv, d, bs, float(scale), _dev(out, "out", q.dtype), _stream(stream), tables[1], nb,
+                 _dtype_code(q), _dev(workspace, "workspace", torch.uint8), workspace.numel())
+    _check(st, "ns_paged_attn_prefill_q4_0")
+
+
+def _rope_append(name, q, k, v, positions, cos_sin, slot_mapping, q_out, pools, nb, hkv, bs, d, k_out, interleaved,
+                 stream):
+    rows, keys, table = q.shape, k.shape, cos_sin.shape
+    if len(rows) != 3 or len(keys) != 3 or v.shape != keys or keys[0] != rows[0] or keys[1:] != (hkv, d) \
+            or rows[2] != d:
+        raise ValueError("q must be [T, Hq, D], k and v [T, Hkv, D], with the pools' heads and head_dim")
+    T, hq, _ = rows
+    if q_out.shape != rows or (k_out is not None and k_out.shape != keys):
+        raise ValueError("q_out must have q's shape, k_out k's")
+    if positions.shape != (T,) or slot_mapping.shape != (T,) or len(table) != 2:
+        raise ValueError("positions and slot_mapping must be [T], cos_sin [max_positions, rotary_dim]")
+    dtype = q.dtype
+    dt = _dtype_code(q)
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", dtype, rows), _rows(k, "k", dtype, keys), _rows(v, "v", dtype, keys)
+    qo, qos = _rows(q_out, "q_out", dtype, rows)
+    ko, kos = (None, 0) if k_out is None else _rows(k_out, "k_out", dtype, keys)
+    st = _invoke(name, qp, kp, vp, _dev(positions, "positions", torch.int32), _dev(cos_sin, "cos_sin", torch.float32),
+                 _dev(slot_mapping, "slot_mapping", torch.int64), qo, ko, *pools, T, hq, hkv, d, table[1],
+                 1 if interleaved else 0, table[0], qs, ks, vs, qos, kos, bs, nb, dt, _stream(stream))
+    _check(st, name)
+
+
+def ns_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, q_out, k_pool, v_pool, k_out=None, interleaved=False,
+                      stream=None):
+    """Rotate q [T, Hq, D] and k [T, Hkv, D] by positions [T] (int32) and write q_out, the rotated keys and
+    v into k_pool/v_pool [NB, Hkv, bs, D] at slot_mapping [T] (int64), and the keys into k_out when given.
+
+    Rows of q, k, v, q_out and k_out may lie any stride apart; q_out may be q and k_out k.  cos_sin float32
+    [max_positions, rotary_dim]: cosines, then sines; interleaved: pairs (2i, 2i + 1) instead of halves.
+    """
+    pool = k_pool.shape
+    if len(pool) != 4 or v_pool.shape != pool:
+        raise ValueError("k_pool and v_pool must be [NB, Hkv, bs, D]")
+    nb, hkv, bs, d = pool
+    pools = (_dev(k_pool, "k_pool", q.dtype), _dev(v_pool, "v_pool", q.dtype))
+    _rope_append("ns_rope_kv_append", q, k, v, positions, cos_sin, slot_mapping, q_out, pools, nb, hkv, bs, d, k_out,
+                 interleaved, stream)
+
+
+def ns_rope_kv_append_q8_0(q, k, v, positions, cos_sin, slot_mapping, q_out, k_codes, k_scales, v_codes, v_scales,
+                           k_out=None, interleaved=False, stream=None):
+    """ns_rope_kv_append into a q8_0 pool."""
+    nb, hkv, bs, d, *pools = _q8_pools(k_codes, k_scales, v_codes, v_scales)
+    _rope_append("ns_rope_kv_append_q8_0", q, k, v, positions, cos_sin, slot_mapping, q_out, pools, nb, hkv, bs, d,
+                 k_out, interleaved, stream)
+
+
+def ns_rope_kv_append_q4_0(q, k, v, positions, cos_sin, slot_mapping, q_out, k_codes, k_scales, v_codes, v_scales,
+                           k_out=None, interleaved=False, stream=None):
+    """ns_rope_kv_append into a q4_0 pool."""
+    nb, hkv, bs, d, *pools = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    _rope_append("ns_rope_kv_append_q4_0", q, k, v, positions, cos_sin, slot_mapping, q_out, pools, nb, hkv, bs, d,
+                 k_out, interleaved, stream)
 
 
 def _prob_rows(t, name, shape):

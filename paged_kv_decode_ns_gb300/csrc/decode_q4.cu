@@ -1,0 +1,830 @@
+// decode_q4.cu -- decode attention over a q4_0 (4-bit) paged cache.
+//
+// out = sum_p 2^(z_p - m) v_p / sum_p 2^(z_p - m), z in log2 units, in one pass over the
+// keys with a running reference m.  K_p = dk_p (c - 8) and V_p = dv_p (c - 8) by group of 32
+// elements, so that with integer codes c
+//   z_p = scale sum_g dk_pg (q_g . (c_pg - 8)),   out_g = sum_p (w_p dv_pg) (c_pg - 8):
+// the codes less 8 are exact in fp16, and the steps are applied to the scores and to the weights,
+// 8 heads wide, instead of to 64 or 128 elements.  Both sums are small matrix products
+// (mma.m16n8k16: 16 tokens or elements by the 8 query heads of a group, fp32 sums).  A tcgen05
+// product has 128 rows at least and its operands in shared memory, where each code would
+// be four times as large as in the cache; here they go from the codes to the product in registers.
+//
+// Only two factors are rounded: q to fp16, scaled by a power of two (exact down to 2^-28 of the
+// row's largest element, off by 2^-39 of that below) and w dv to fp16 (2^-11 of itself, or 2^-32
+// of the largest weight times the largest step so far).
+//
+// Work.  The pairs (sequence, kv head, 8 query heads) lie end to end on a line, in chunks of
+// 32 tokens and one more for a pair's own cost, and each warp of a persistent grid takes an
+// equal run of it.  A pair cut by warps of one CTA is joined in shared memory, one cut by
+// CTAs through records in the workspace, by the CTA that arrives last; in the order of the
+// keys, so results do not depend on timing.
+#include <algorithm>
+
+#include "ns_internal.h"
+#include "q4_decode.h"
+#include "quantise.cuh"
+
+namespace ns {
+
+namespace {
+
+constexpr int kChunk = 32;     // tokens of a step: one a lane
+constexpr int kPairCost = 1;   // chunks that a pair counts besides its own
+constexpr int kMinShare = 2;   // chunks a warp is given at least
+constexpr float kNone = -3.402823466e38f;
+// m is set so that the largest w dv is just below 2^kLift, and moves when one would pass
+// that by 2^kSlack: fp16 has room up to 2^16 and steps of 2^-24.
+constexpr float kLift = 7.0f, kSlack = 8.0f;
+
+template <int D>
+struct Geo {
+    static constexpr int R = D / 32;                       // groups of 32 elements
+    static constexpr int WARPS = D == 64 ? 16 : 12;
+    static constexpr int STAGES = D == 64 ? 4 : 3;         // chunks of a warp, one of them in use
+    static constexpr int CODES = kChunk * D / 2;           // bytes of a chunk's K or V
+    static constexpr int SCALES = kChunk * R * 2;
+    static constexpr int STAGE = 2 * (CODES + SCALES);
+    static constexpr int RECORD = 8 * (D + 2);             // floats: m, l, O of 8 heads
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int SLOTS = 2 * D;                    // float4s of 8 heads' O
+};
+
+template <int D>
+struct alignas(16) Smem {
+    using GG = Geo<D>;
+    uint8_t ring[GG::WARPS][GG::STAGES][GG::STAGE];  // afterwards a warp's last record
+    float first[GG::WARPS][GG::RECORD];              // its first one
+    uint32_t live[GG::WARPS][GG::STAGES];            // tokens of a chunk that count
+    int before[GG::THREADS];                         // chunks in front of a thread's sequences
+    int scan[GG::WARPS];
+    // what a warp left: the pair of its first and last record (-1: none) and whether the first
+    // one goes to its pair's end
+    int first_pair[GG::WARPS], first_ends[GG::WARPS], last_pair[GG::WARPS];
+    int arrived_last[2], pieces[2], first_cta[2];
+    float weight[kMaxQ4Ctas][8];
+    float inv[8];
+    static_assert(GG::STAGES * GG::STAGE >= GG::RECORD * 4, "a record fits a warp's ring");
+};
+
+struct Params {
+    Q4DecodeArgs a;
+    int heads;      // pairs of a sequence
+    int subs;       // of a kv head
+    int group;      // query heads of a kv head
+    int shift;      // log2 of the block size
+    float scale_log2;
+    int *counters;
+    float *records;
+};
+
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void load_matrices_turned(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t turn_matrix(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void product(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes 0 .. 15 of a word, four bits each -> fp16 pairs of code - 8: code i beside code i + 4.
+// A code in the low bits of an fp16 1024 is 1024 + c, four bits higher 1024 + 16 c.
+__device__ __forceinline__ void codes_less_8(uint32_t (&p)[4], uint32_t w)
+{
+    auto place = [](uint32_t x, uint32_t mask) {
+        uint32_t r;  // (x & mask) | 1024 in both halves
+        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "r"(0x64006400u));
+        return r;
+    };
+    auto low = [](uint32_t x) {
+        const __half2 h = __hsub2(*reinterpret_cast<__half2 *>(&x), __half2half2(__ushort_as_half(0x6408)));  // 1032
+        return *reinterpret_cast<const uint32_t *>(&h);
+    };
+    auto high = [](uint32_t x) {
+        const __half2 h = __hfma2(*reinterpret_cast<__half2 *>(&x), __half2half2(__ushort_as_half(0x2c00)),  // 1/16
+                                  __half2half2(__ushort_as_half(0xd480)));                                  // -72
+        return *reinterpret_cast<const uint32_t *>(&h);
+    };
+    const uint32_t v = w >> 8;
+    p[0] = low(place(w, 0x000f000fu));
+    p[1] = high(place(w, 0x00f000f0u));
+    p[2] = low(place(v, 0x000f000fu));
+    p[3] = high(place(v, 0x00f000f0u));
+}
+
+__device__ __forceinline__ uint32_t larger_f16(uint32_t a, uint32_t b)  // magnitudes, signs of no meaning
+{
+    uint32_t r;
+    asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ float2 halves(uint32_t w) { return unpack2<F16>(w); }
+
+// ---------------------------------------------------------------------------
+// Walk over the pieces of a warp's run.
+// ---------------------------------------------------------------------------
+struct Piece {
+    int s, h;       // sequence, pair of it
+    int L;          // keys of the sequence
+    int c, c1;      // chunks
+    int whole;      // the piece is its whole pair
+    int ends;       // it goes to the pair's end
+};
+
+struct Walk {
+    int s, h, off;  // where the next piece starts
+    int left;       // chunks of the run still to come
+};
+
+__device__ __forceinline__ int keys_of(const Q4DecodeArgs &a, int shift, int s)
+{
+    const int L = a.context_lens[s];
+    const long long cap = (long long)a.max_blocks_per_seq << shift;
+    return L < 0 ? 0 : L > cap ? (int)cap : L;
+}
+
+__device__ __forceinline__ int length_of(int L) { return (L + kChunk - 1) / kChunk + kPairCost; }
+
+// The next piece of a run that is not over.
+__device__ __forceinline__ Piece next_piece(const Params &P, Walk &w)
+{
+    Piece p;
+    p.s = w.s;
+    p.h = w.h;
+    p.L = keys_of(P.a, P.shift, w.s);
+    const int len = length_of(p.L), take = min(w.left, len - w.off);
+    p.c = max(w.off - kPairCost, 0);
+    p.c1 = max(w.off + take - kPairCost, 0);
+    p.ends = w.off + take == len;
+    p.whole = p.ends && w.off == 0;
+    w.left -= take;
+    w.off = 0;
+    if (p.ends && ++w.h == P.heads) {
+        w.h = 0;
+        ++w.s;
+    }
+    return p;
+}
+
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __grid_constant__ Params P)
+{
+    using GG = Geo<D>;
+    constexpr int R = GG::R, ST = GG::STAGES, W = GG::WARPS;
+    constexpr int PARTS = R;                    // 16-byte parts of a token's codes: one a group
+    constexpr int COPIES = kChunk * PARTS / 32; // of a lane, for K and again for V
+    constexpr int SPAN = 16 / (2 * R);          // tokens whose scales are 16 bytes
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+    const Q4DecodeArgs &a = P.a;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;  // row and column pair of the products' fragments
+    if (tid < W) {
+        sm.first_pair[tid] = -1;
+        sm.last_pair[tid] = -1;
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ---- the line: each thread measures a share of the sequences
+    const int per = (a.num_seqs + GG::THREADS - 1) / GG::THREADS;
+    const int s0 = min(a.num_seqs, tid * per), s1 = min(a.num_seqs, s0 + per);
+    int mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        const int L = a.context_lens[s];
+        if (blockIdx.x == 0 && (L < 0 || L > ((long long)a.max_blocks_per_seq << P.shift)))
+            raise_status(a.status, NS_DEV_BAD_CONTEXT_LEN);
+        mine += length_of(keys_of(a, P.shift, s));
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += y;
+    }
+    if (lane == 31)
+        sm.scan[warp] = incl;
+    __syncthreads();
+    int total = 0, ahead = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const int x = sm.scan[i];
+        ahead += i < warp ? x : 0;
+        total += x;
+    }
+    sm.before[tid] = ahead + incl - mine;
+    total *= P.heads;
+    __syncthreads();
+    // runs: the first `rest` of `runs` warps take share + 1 chunks, the others share
+    const int runs = min((int)gridDim.x * W, (total + kMinShare - 1) / kMinShare);
+    const int share = total / runs, rest = total - share * runs;
+    const int me = blockIdx.x * W + warp;
+    if ((int)blockIdx.x * W >= runs)
+        return;
+    Walk next;
+    next.s = next.h = next.off = 0;
+    next.left = me < runs ? share + (me < rest ? 1 : 0) : 0;
+    const int x0 = me * share + min(me, rest);
+    if (me < runs) {
+        // the last thread whose sequences start at x0 or before: every `step`th, then each
+        auto starts = [&](int i) { return i < GG::THREADS && (long long)i * per < a.num_seqs && sm.before[i] * P.heads <= x0; };
+        constexpr int step = GG::THREADS / 32;
+        int lo = (__popc(__ballot_sync(0xffffffffu, starts(lane * step))) - 1) * step;
+        lo += __popc(__ballot_sync(0xffffffffu, lane < step && starts(lo + lane))) - 1;
+        int s = lo * per, y = x0 - sm.before[lo] * P.heads;
+        for (;; ++s) {
+            const int len = length_of(keys_of(a, P.shift, s));
+            if (y < len * P.heads || s + 1 >= a.num_seqs) {
+                next.s = s;
+                next.h = y / len;
+                next.off = y - next.h * len;
+                break;
+            }
+            y -= len * P.heads;
+        }
+    }
+    Walk ahead_walk = next;  // the copies' walk, up to ST - 1 chunks ahead of the arithmetic
+
+    // ---- copies: a chunk's codes and scales of K and V by 16 bytes a lane
+    const uint32_t ring = smem_addr(sm.ring[warp][0]);
+    const int bs1 = (1 << P.shift) - 1;
+    Piece ip;
+    ip.c = ip.c1 = 0;
+    ip.s = ip.h = ip.L = 0;
+    int entry = -1;      // the block of this lane's token in the next chunk to copy
+    int issued = 0;      // chunks, modulo ST
+    const uint32_t row_bytes = D / 2, block_rows = (uint32_t)a.num_kv_heads << P.shift;
+    auto look_up = [&]() {  // the next chunk's blocks, whose piece may be another one
+        while (ip.c == ip.c1 && ahead_walk.left > 0)
+            ip = next_piece(P, ahead_walk);
+        entry = -1;
+        if (ip.c < ip.c1) {
+            const int tok = ip.c * kChunk + lane;
+            if (tok < ip.L)
+                entry = a.block_tables[(long long)ip.s * a.max_blocks_per_seq + (tok >> P.shift)];
+        }
+    };
+    auto issue = [&]() {
+        if (ip.c < ip.c1) {
+            const int tok = ip.c * kChunk + lane;
+            const bool have = tok < ip.L, ok = have && entry >= 0 && entry < a.num_blocks;
+            if (have && !ok)
+                raise_status(a.status, NS_DEV_BAD_BLOCK_ID);
+            const uint32_t live = __ballot_sync(0xffffffffu, ok);
+            if (lane == 0)
+                sm.live[warp][issued] = live;
+            const uint32_t to = ring + issued * GG::STAGE;
+            const int kv = P.subs == 1 ? ip.h : ip.h / P.subs;
+            const uint32_t head_row = (uint32_t)kv << P.shift;
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) {
+                const int idx = lane + 32 * i, tau = idx / PARTS, part = idx % PARTS;
+                const int id = __shfl_sync(0xffffffffu, entry, tau);
+                if ((live >> tau) & 1u) {
+                    const long long at = ((long long)id * block_rows + head_row + (tau & bs1)) * row_bytes + part * 16;
+                    // eight rows of one part are eight different banks of 16 bytes
+                    const int turned = D == 64 ? part ^ ((tau >> 2) & 1) : part ^ ((tau >> 1) & 3);
+                    const uint32_t dst = to + tau * row_bytes + turned * 16;
+                    copy16(dst, static_cast<const uint8_t *>(a.k_codes) + at);
+                    copy16(dst + GG::CODES, static_cast<const uint8_t *>(a.v_codes) + at);
+                }
+            }
+            {
+                constexpr int N = kChunk / SPAN;  // lanes for K, and again for V
+                const int tau = (lane % N) * SPAN;
+                const int id = __shfl_sync(0xffffffffu, entry, tau);
+                if (lane < 2 * N && ((live >> tau) & 1u)) {
+                    const long long at = ((long long)id * block_rows + head_row + (tau & bs1)) * (2 * R);
+                    const void *src = lane < N ? a.k_scales : a.v_scales;
+                    copy16(to + 2 * GG::CODES + lane * 16, static_cast<const uint8_t *>(src) + at);
+                }
+            }
+            ++ip.c;
+            issued = issued + 1 == ST ? 0 : issued + 1;
+            look_up();
+        }
+        copies_commit();
+    };
+
+    look_up();
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i)
+        issue();
+
+    // ---- arithmetic
+    int used = 0;  // chunks, modulo ST
+    while (next.left > 0) {
+        const int off0 = next.off;
+        const Piece p = next_piece(P, next);
+        const int kv = P.subs == 1 ? p.h : p.h / P.subs, sub = p.h - kv * P.subs;
+        const int head0 = kv * P.group + sub * 8, heads = min(8, P.group - sub * 8);
+        // q of head g, elements 8 t .. 8 t + 7 of each group, as the products' second operand
+        uint32_t q[R][4];
+        float q_unit;  // 2^-e: what a unit of the products is worth
+        {
+            uint4 w[R];
+            float top = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                w[r] = make_uint4(0u, 0u, 0u, 0u);
+                if (g < heads)
+                    w[r] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) +
+                                                            (((long long)p.s * a.num_q_heads + head0 + g) * D + 32 * r + 8 * t) * 2);
+                const uint32_t x[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack2<T>(x[i]);
+                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the row's largest goes to [2^14, 2^15); the factor stays a normal number
+            const int e = top > 0.f && top < INFINITY ? min(max(141 - (int)(__float_as_uint(top) >> 23), -113), 113) : 0;
+            const float f = __uint_as_float((uint32_t)(127 + e) << 23);
+            q_unit = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t x[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 y = unpack2<T>(x[i]);
+                    v[2 * i] = y.x * f;
+                    v[2 * i + 1] = y.y * f;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[r][i] = pack2<F16>(v[i], v[i + 4]);
+            }
+        }
+        // of the two heads of this lane's columns
+        const float2 unit = make_float2(P.scale_log2 * __shfl_sync(0xffffffffu, q_unit, 8 * t),
+                                        P.scale_log2 * __shfl_sync(0xffffffffu, q_unit, 8 * t + 4));
+
+        float O[R][2][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    O[r][u][i] = 0.f;
+        float2 l = make_float2(0.f, 0.f), m = make_float2(kNone, kNone), limit = m;
+        int top_e = -1;            // exponent field of the largest V step so far
+        uint32_t step_limit = 0u;  // and the largest fp16 of that exponent
+
+        for (int c = p.c; c < p.c1; ++c) {
+            copies_wait<ST - 2>();
+            __syncwarp();
+            issue();  // into the stage that the last turn has read
+            const uint32_t from = ring + used * GG::STAGE;
+            const uint8_t *stage = sm.ring[warp][used];
+            const uint32_t live = sm.live[warp][used];
+            used = used + 1 == ST ? 0 : used + 1;
+
+            // ---- scores: 16 tokens at a time, by group
+            float2 z[2][2];  // [tile][token g or g + 8] of the two heads
+            uint32_t dv[2][2][R / 2];
+            uint32_t largest = 0u;
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                uint32_t dk[2][R / 2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint8_t *at = stage + 2 * GG::CODES + (tile * 16 + i * 8 + g) * (2 * R);
+                    if constexpr (R == 2) {
+                        dk[i][0] = *reinterpret_cast<const uint32_t *>(at);
+                        dv[tile][i][0] = *reinterpret_cast<const uint32_t *>(at + GG::SCALES);
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(at), y = *reinterpret_cast<const uint2 *>(at + GG::SCALES);
+                        dk[i][0] = x.x, dk[i][1] = x.y;
+                        dv[tile][i][0] = y.x, dv[tile][i][1] = y.y;
+                    }
+                    if (live != 0xffffffffu && !((live >> (tile * 16 + i * 8 + g)) & 1u))
+#pragma unroll
+                        for (int j = 0; j < R / 2; ++j)
+                            dv[tile][i][j] = 0u;
+#pragma unroll
+                    for (int j = 0; j < R / 2; ++j)
+                        largest = larger_f16(largest, dv[tile][i][j]);
+                }
+                z[tile][0] = z[tile][1] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int r2 = 0; r2 < R; r2 += 2) {
+                    uint32_t w[4];
+                    {
+                        const int tau = tile * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), part = r2 + (lane >> 4);
+                        const int turned = D == 64 ? part ^ ((tau >> 2) & 1) : part ^ ((tau >> 1) & 3);
+                        load_matrices(w, from + tau * row_bytes + turned * 16);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = r2 + j;
+                        uint32_t lo[4], hi[4];
+                        codes_less_8(lo, w[2 * j]);
+                        codes_less_8(hi, w[2 * j + 1]);
+                        float s[4] = {0.f, 0.f, 0.f, 0.f};
+                        product(s, lo[0], hi[0], lo[1], hi[1], q[r][0], q[r][1]);
+                        product(s, lo[2], hi[2], lo[3], hi[3], q[r][2], q[r][3]);
+                        const float2 d0 = halves(dk[0][r2 / 2]), d1 = halves(dk[1][r2 / 2]);
+                        const float e0 = j == 0 ? d0.x : d0.y, e1 = j == 0 ? d1.x : d1.y;
+                        z[tile][0] = ffma2(make_float2(s[0], s[1]), make_float2(e0, e0), z[tile][0]);
+                        z[tile][1] = ffma2(make_float2(s[2], s[3]), make_float2(e1, e1), z[tile][1]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    z[tile][i] = fmul2(z[tile][i], unit);
+                    if (live != 0xffffffffu && !((live >> (tile * 16 + i * 8 + g)) & 1u))
+                        z[tile][i] = make_float2(-INFINITY, -INFINITY);
+                }
+            }
+
+            // ---- the reference moves when a weight times a step would leave fp16's range
+            const float za = fmaxf(fmaxf(z[0][0].x, z[0][1].x), fmaxf(z[1][0].x, z[1][1].x));
+            const float zb = fmaxf(fmaxf(z[0][0].y, z[0][1].y), fmaxf(z[1][0].y, z[1][1].y));
+            const uint32_t big = max(largest & 0x7fffu, (largest >> 16) & 0x7fffu);
+            if (__any_sync(0xffffffffu, za > limit.x || zb > limit.y || big > step_limit)) {
+                float2 top = make_float2(za, zb);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, o));
+                    top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, o));
+                }
+                const int e = max(top_e, (int)(__reduce_max_sync(0xffffffffu, big) >> 10));
+                const float rise = top_e < 0 ? 0.f : (float)(e - top_e), size = (float)(e - 14);  // steps are below 2^size
+                top_e = e;
+                step_limit = ((uint32_t)(e + 1) << 10) - 1u;
+                // a head's reference follows its own scores alone, whatever the heads beside it hold
+                const float2 to = make_float2(top.x > limit.x ? fmaxf(m.x + rise, top.x + size - kLift) : m.x + rise,
+                                              top.y > limit.y ? fmaxf(m.y + rise, top.y + size - kLift) : m.y + rise);
+                const float2 f = make_float2(fast_exp2(m.x - to.x), fast_exp2(m.y - to.y));
+                m = to;
+                limit = make_float2(m.x - size + kLift + kSlack, m.y - size + kLift + kSlack);
+                l = fmul2(l, f);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        O[r][u][0] *= f.x;
+                        O[r][u][1] *= f.y;
+                        O[r][u][2] *= f.x;
+                        O[r][u][3] *= f.y;
+                    }
+            }
+
+            // ---- weights, and the values' product
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                float2 w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    w[i] = make_float2(fast_exp2(z[tile][i].x - m.x), fast_exp2(z[tile][i].y - m.y));
+                    l = fadd2(l, w[i]);
+                }
+#pragma unroll
+                for (int r2 = 0; r2 < R; r2 += 2) {
+                    uint32_t v[4];
+                    {
+                        const int tau = tile * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), part = r2 + (lane >> 4);
+                        const int turned = D == 64 ? part ^ ((tau >> 2) & 1) : part ^ ((tau >> 1) & 3);
+                        load_matrices_turned(v, from + GG::CODES + tau * row_bytes + turned * 16);
+                    }
+                    const float2 d0 = halves(dv[tile][0][r2 / 2]), d1 = halves(dv[tile][1][r2 / 2]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float e0 = j == 0 ? d0.x : d0.y, e1 = j == 0 ? d1.x : d1.y;
+                        const float2 w0 = fmul2(w[0], make_float2(e0, e0)), w1 = fmul2(w[1], make_float2(e1, e1));
+                        const uint32_t b0 = turn_matrix(pack2<F16>(w0.x, w0.y)), b1 = turn_matrix(pack2<F16>(w1.x, w1.y));
+                        uint32_t lo[4], hi[4];
+                        codes_less_8(lo, v[2 * j]);
+                        codes_less_8(hi, v[2 * j + 1]);
+                        product(O[r2 + j][0], lo[0], lo[1], hi[0], hi[1], b0, b1);
+                        product(O[r2 + j][1], lo[2], lo[3], hi[2], hi[3], b0, b1);
+                    }
+                }
+            }
+        }
+
+        // ---- the piece's end: this lane has elements 4 g .. 4 g + 3 of each group, heads 2 t, 2 t + 1
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            l.x += __shfl_xor_sync(0xffffffffu, l.x, o);
+            l.y += __shfl_xor_sync(0xffffffffu, l.y, o);
+        }
+        if (p.whole) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float sum = i == 0 ? l.x : l.y, inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+                if (2 * t + i < heads)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const uint2 y = make_uint2(pack2<T>(O[r][0][i] * inv, O[r][0][i + 2] * inv),
+                                                   pack2<T>(O[r][1][i] * inv, O[r][1][i + 2] * inv));
+                        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) +
+                                                   (((long long)p.s * a.num_q_heads + head0 + 2 * t + i) * D + 32 * r + 4 * g) * 2) = y;
+                    }
+            }
+        } else {
+            const bool is_first = off0 > 0;
+            if (!is_first) {  // the last piece of the run: its copies are all in, and the ring is free
+                copies_wait<0>();
+                __syncwarp();
+            }
+            float *rec = is_first ? sm.first[warp] : reinterpret_cast<float *>(sm.ring[warp][0]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int h = 2 * t + i;
+                if (g == 0) {
+                    rec[h] = i == 0 ? m.x : m.y;
+                    rec[8 + h] = i == 0 ? l.x : l.y;
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    *reinterpret_cast<float4 *>(rec + 16 + h * D + 32 * r + 4 * g) =
+                        make_float4(O[r][0][i], O[r][0][i + 2], O[r][1][i], O[r][1][i + 2]);
+            }
+            if (lane == 0) {
+                const int pair = p.s * P.heads + p.h;
+                if (is_first) {
+                    sm.first_pair[warp] = pair;
+                    sm.first_ends[warp] = p.ends;
+                } else {
+                    sm.last_pair[warp] = pair;
+                }
+            }
+        }
+    }
+    copies_wait<0>();
+    __syncthreads();
+
+    // ---- join the CTA's cut pairs.  Chain -1 starts with warp 0's first record (a pair that
+    // began in a CTA before), chain w with warp w's last one; the first records of the warps
+    // behind it follow, up to one that goes to the pair's end.
+    constexpr int DPL = D / 32;
+    for (int item = warp; item < (W + 1) * 8; item += W) {
+        const int chain = item / 8 - 1, h = item & 7;
+        const int pair = chain < 0 ? sm.first_pair[0] : sm.last_pair[chain];
+        if (pair < 0)
+            continue;
+        int n = 1;
+        bool ends = chain < 0 && sm.first_ends[0];
+        while (!ends && chain + n + (chain < 0 ? 1 : 0) < W) {
+            const int w = chain + n + (chain < 0 ? 1 : 0);
+            if (sm.first_pair[w] != pair)
+                break;
+            ends = sm.first_ends[w];
+            ++n;
+        }
+        auto record = [&](int i) -> const float * {
+            return chain < 0 ? sm.first[i] : i == 0 ? reinterpret_cast<const float *>(sm.ring[chain][0]) : sm.first[chain + i];
+        };
+        const float mi = lane < n ? record(lane)[h] : kNone, li = lane < n ? record(lane)[8 + h] : 0.f;
+        float top = mi;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float wi = fast_exp2(mi - top);
+        float sum = wi * li, acc[DPL];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+        for (int d = 0; d < DPL; ++d)
+            acc[d] = 0.f;
+        for (int i = 0; i < n; ++i) {
+            const float f = __shfl_sync(0xffffffffu, wi, i);
+            const float *src = record(i) + 16 + h * D + lane * DPL;
+#pragma unroll
+            for (int d = 0; d < DPL; ++d)
+                acc[d] = fmaf(f, src[d], acc[d]);
+        }
+        const int s = pair / P.heads, ph = pair - s * P.heads, kv = ph / P.subs, sub = ph - kv * P.subs;
+        if (chain >= 0 && ends) {
+            const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+            if (h < P.group - sub * 8) {
+                uint8_t *dst = static_cast<uint8_t *>(a.out) +
+                               (((long long)s * a.num_q_heads + kv * P.group + sub * 8 + h) * D + lane * DPL) * 2;
+#pragma unroll
+                for (int d = 0; d < DPL; d += 2)
+                    *reinterpret_cast<uint32_t *>(dst + 2 * d) = pack2<T>(acc[d] * inv, acc[d + 1] * inv);
+            }
+        } else {
+            float *rec = P.records + (size_t)(2 * blockIdx.x + (chain < 0 ? 0 : 1)) * GG::RECORD;
+            if (lane == 0) {
+                rec[h] = top;
+                rec[8 + h] = sum;
+            }
+#pragma unroll
+            for (int d = 0; d < DPL; ++d)
+                rec[16 + h * D + lane * DPL + d] = acc[d];
+            __threadfence();
+        }
+    }
+    __syncthreads();
+
+    // ---- pairs that other CTAs have parts of: the last to arrive joins them
+    if (tid < 2) {
+        int pair = -1;
+        if (tid == 0) {
+            pair = sm.first_pair[0];
+        } else {
+            // the chain that runs over the CTA's end
+            int w = W - 1;
+            while (w >= 0 && sm.last_pair[w] < 0 && sm.first_pair[w] >= 0 && !sm.first_ends[w])
+                --w;
+            if (w >= 0)
+                pair = sm.last_pair[w];
+        }
+        sm.arrived_last[tid] = -1;
+        if (pair >= 0) {
+            const int s = pair / P.heads, ph = pair - s * P.heads;
+            const int len = length_of(keys_of(a, P.shift, s)), i = s / per;
+            int y = sm.before[i];
+            for (int k = i * per; k < s; ++k)
+                y += length_of(keys_of(a, P.shift, k));
+            const int begin = y * P.heads + ph * len, end = begin + len - 1;
+            auto cta_of = [&](int x) {
+                const int w = x < rest * (share + 1) ? x / (share + 1) : rest + (x - rest * (share + 1)) / share;
+                return w / W;
+            };
+            const int c0 = cta_of(begin), c1 = cta_of(end);
+            sm.first_cta[tid] = c0;
+            sm.pieces[tid] = c1 - c0 + 1;
+            if (c1 > c0) {
+                __threadfence();
+                if (atomicAdd(P.counters + pair, 1) == c1 - c0) {
+                    P.counters[pair] = 0;
+                    sm.arrived_last[tid] = pair;
+                    __threadfence();
+                }
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int slot = 0; slot < 2; ++slot) {
+        const int pair = sm.arrived_last[slot];
+        if (pair < 0)
+            continue;
+        const int n = sm.pieces[slot], c0 = sm.first_cta[slot];
+        // record i: the first CTA's last slot, then the others' first ones
+        auto record = [&](int i) -> const float * { return P.records + (size_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * GG::RECORD; };
+        if (warp < 8) {
+            float mi[(kMaxQ4Ctas + 31) / 32], li[(kMaxQ4Ctas + 31) / 32], top = kNone, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < (kMaxQ4Ctas + 31) / 32; ++k) {
+                const int i = k * 32 + lane;
+                mi[k] = i < n ? __ldcg(record(i) + warp) : kNone;
+                li[k] = i < n ? __ldcg(record(i) + 8 + warp) : 0.f;
+                top = fmaxf(top, mi[k]);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+            for (int k = 0; k < (kMaxQ4Ctas + 31) / 32; ++k) {
+                const float f = fast_exp2(mi[k] - top);
+                sum = fmaf(f, li[k], sum);
+                if (k * 32 + lane < n)
+                    sm.weight[k * 32 + lane][warp] = f;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0)
+                sm.inv[warp] = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+        }
+        __syncthreads();
+        // a thread adds up four elements over every LANESth record
+        constexpr int LANES = GG::THREADS / GG::SLOTS;
+        float4 *part = reinterpret_cast<float4 *>(sm.ring[0][0]);
+        const int at = tid % GG::SLOTS, first = tid / GG::SLOTS, h = at / (D / 4);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (first < LANES) {
+            for (int i = first; i < n; i += 4 * LANES) {
+                float4 x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[k] = i + k * LANES < n ? __ldcg(reinterpret_cast<const float4 *>(record(i + k * LANES) + 16) + at)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (i + k * LANES >= n)
+                        break;
+                    const float f = sm.weight[i + k * LANES][h];
+                    acc.x = fmaf(f, x[k].x, acc.x), acc.y = fmaf(f, x[k].y, acc.y);
+                    acc.z = fmaf(f, x[k].z, acc.z), acc.w = fmaf(f, x[k].w, acc.w);
+                }
+            }
+            if (first > 0)
+                part[(first - 1) * GG::SLOTS + at] = acc;
+        }
+        __syncthreads();
+        if (first == 0) {
+#pragma unroll
+            for (int k = 1; k < LANES; ++k) {
+                const float4 x = part[(k - 1) * GG::SLOTS + at];
+                acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+            }
+            const int s = pair / P.heads, ph = pair - s * P.heads, kv = ph / P.subs, sub = ph - kv * P.subs;
+            if (h < P.group - sub * 8) {
+                const float inv = sm.inv[h];
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) +
+                                           (((long long)s * a.num_q_heads + kv * P.group + sub * 8 + h) * D + (at % (D / 4)) * 4) * 2) =
+                    make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch(const Params &P, cudaStream_t stream)
+{
+    int sms = 0;
+    cudaError_t e = current_sms(&sms);
+    if (e != cudaSuccess)
+        return e;
+    const void *kern = (const void *)decode_q4_kernel<T, D>;
+    static unsigned long long ready = 0;  // devices whose kernel has its shared memory
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !((__atomic_load_n(&ready, __ATOMIC_RELAXED) >> dev) & 1ull)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELAXED);
+    }
+    // no more CTAs than the tables' rows could fill
+    const long long most = (long long)P.a.num_seqs * P.heads *
+                           ((((long long)P.a.max_blocks_per_seq << P.shift) + kChunk - 1) / kChunk + kPairCost);
+    const long long runs = (most + kMinShare - 1) / kMinShare;
+    const int ctas = (int)std::min<long long>(std::min(sms, kMaxQ4Ctas), (runs + Geo<D>::WARPS - 1) / Geo<D>::WARPS);
+    Params p = P;
+    void *args[] = {&p};
+    return launch_early(kern, dim3(ctas), Geo<D>::THREADS, sizeof(Smem<D>), stream, args);
+}
+
+}  // namespace
+
+bool q4_decode_fits(long long num_seqs, long long pairs, long long max_blocks, int block_size)
+{
+    return num_seqs * pairs * ((max_blocks * block_size + kChunk - 1) / kChunk + kPairCost) <= 0x7fffffffLL;
+}
+
+cudaError_t launch_decode_q4(const Q4DecodeArgs &a, cudaStream_t stream)
+{
+    Params P;
+    P.a = a;
+    P.group = a.num_q_heads / a.num_kv_heads;
+    P.subs = (P.group + 7) / 8;
+    P.heads = a.num_kv_heads * P.subs;
+    P.shift = a.block_size == 4 ? 2 : a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
+    P.scale_log2 = a.scale * 1.4426950408889634f;
+    P.counters = a.counters;
+    P.records = a.records;
+    if (a.head_dim == 64)
+        return a.dtype == NS_BF16 ? launch<BF16, 64>(P, stream) : launch<F16, 64>(P, stream);
+    return a.dtype == NS_BF16 ? launch<BF16, 128>(P, stream) : launch<F16, 128>(P, stream);
+}
+
+}  // namespace ns

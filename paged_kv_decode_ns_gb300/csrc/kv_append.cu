@@ -5,8 +5,8 @@
 // block s / bs, offset s % bs.  A bit-exact copy: one thread moves 16 bytes,
 // eight threads move one 64-element head row, so both the reads of the new
 // rows and the writes into the pool are whole 128-byte lines.
-#include "ns_common.cuh"
 #include "ns_internal.h"
+#include "quantise.cuh"
 
 namespace ns {
 
@@ -43,32 +43,14 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const uint4 *__restrict_
 
 // q8_0 append: eight threads per (token, kv head) row, thread i holding
 // elements 8i..8i+7 of K and of V; four threads make a 32-element block.  The
-// block's scale d = max|x| / 127 and every code rint(x * (1/d)) (ties to even,
-// clamped to +-127) are rounded to fp32 at each step, and d is stored as fp16
-// (nearest even, saturating): the decisions the CPU oracle takes.  The threads
-// of a block always run together (whole rows per warp), so a row that is
+// threads of a block always run together (whole rows per warp), so a row that is
 // skipped still takes part in the shuffles.
 template <typename T>
 __device__ __forceinline__ void q8_quantize8(const uint4 w, uint2 &codes, uint16_t &d16)
 {
     const float2 x0 = unpack2<T>(w.x), x1 = unpack2<T>(w.y), x2 = unpack2<T>(w.z), x3 = unpack2<T>(w.w);
     const float x[8] = {x0.x, x0.y, x1.x, x1.y, x2.x, x2.y, x3.x, x3.y};
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        amax = fmaxf(amax, fabsf(x[i]));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const float d = __fdiv_rn(amax, 127.f);
-    const float inv = d > 0.f ? __fdiv_rn(1.f, d) : 0.f;
-    uint32_t packed[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int code = max(-127, min(127, __float2int_rn(__fmul_rn(x[i], inv))));
-        packed[i >> 2] |= (uint32_t)(code & 0xff) << (8 * (i & 3));
-    }
-    codes = make_uint2(packed[0], packed[1]);
-    d16 = __half_as_ushort(__float2half_rn(fminf(d, 65504.f)));
+    q8_quantize8(x, codes, d16);
 }
 
 template <typename T>

@@ -1,11 +1,11 @@
 // kv_gather.cu -- read sequences back from the pool into packed rows.
 //
 // k_out[start[s] + p][h][:] = K_s[p][h][:], a copy for 16-bit pools and
-// fp16(d) * code rounded once for q8_0 pools.
+// fp16(d) * code (q8_0) or fp16(d) * (code - 8) (q4_0) rounded once for the others.
 #include <algorithm>
 
-#include "ns_common.cuh"
 #include "ns_internal.h"
+#include "quantise.cuh"
 
 namespace ns {
 
@@ -52,7 +52,7 @@ __device__ __forceinline__ uint4 dequantise(uint4 w)
 constexpr int kBatch = 4;
 constexpr int kMaxTokens = 256;
 
-template <typename T, bool Q8>
+template <typename T, int POOL>
 __global__ void __launch_bounds__(kThreads, 5) kv_gather_kernel(const GatherArgs a, int tokens, int row_chunks, int head_chunks)
 {
     grid_dependency_wait();
@@ -101,9 +101,14 @@ __global__ void __launch_bounds__(kThreads, 5) kv_gather_kernel(const GatherArgs
             if (!on[b])
                 continue;
             const long long prow = row + (long long)h * a.block_size;
-            if (!Q8) {
+            if constexpr (POOL == 16) {
                 k[b] = static_cast<const uint4 *>(a.k)[prow * head_chunks + chunk];
                 v[b] = static_cast<const uint4 *>(a.v)[prow * head_chunks + chunk];
+            } else if constexpr (POOL == 4) {
+                // the codes of 8 elements, and their group's scale
+                const long long at = prow * head_chunks + chunk;
+                k[b] = make_uint4(static_cast<const uint32_t *>(a.k)[at], static_cast<const uint16_t *>(a.k_scales)[at >> 2], 0u, 0u);
+                v[b] = make_uint4(static_cast<const uint32_t *>(a.v)[at], static_cast<const uint16_t *>(a.v_scales)[at >> 2], 0u, 0u);
             } else {
                 const uint2 kc = static_cast<const uint2 *>(a.k)[prow * 8 + chunk],
                             vc = static_cast<const uint2 *>(a.v)[prow * 8 + chunk];
@@ -116,9 +121,12 @@ __global__ void __launch_bounds__(kThreads, 5) kv_gather_kernel(const GatherArgs
             if (!on[b])
                 continue;
             const long long o = out0 + i0 + b * kThreads;
-            if (Q8) {
+            if constexpr (POOL == 8) {
                 k[b] = dequantise<T>(k[b]);
                 v[b] = dequantise<T>(v[b]);
+            } else if constexpr (POOL == 4) {
+                k[b] = q4_elements<T>(k[b].x, (uint16_t)k[b].y);
+                v[b] = q4_elements<T>(v[b].x, (uint16_t)v[b].y);
             }
             static_cast<uint4 *>(a.k_out)[o] = k[b];
             static_cast<uint4 *>(a.v_out)[o] = v[b];
@@ -128,18 +136,28 @@ __global__ void __launch_bounds__(kThreads, 5) kv_gather_kernel(const GatherArgs
 
 }  // namespace
 
-cudaError_t launch_kv_gather(const GatherArgs &a, bool q8, cudaStream_t stream)
+cudaError_t launch_kv_gather(const GatherArgs &in, int pool, cudaStream_t stream)
 {
-    const int head_chunks = a.head_dim / 8, row_chunks = a.num_kv_heads * head_chunks;
+    GatherArgs a = in;
+    int head_chunks = a.head_dim / 8, row_chunks = a.num_kv_heads * head_chunks;
     // a batch for every thread, two of the smaller reads from q8_0 (71 us with one);
     // at least eight rows, so that the look-ups are shared
-    const int tokens = std::min(kMaxTokens, std::max(8, (q8 ? 2 : 1) * kThreads * kBatch / row_chunks));
+    int tokens = std::min(kMaxTokens, std::max(8, (pool == 16 ? 1 : 2) * kThreads * kBatch / row_chunks));
     const unsigned grid = (unsigned)((a.total_tokens + tokens - 1) / tokens);
-    auto kern = !q8 ? kv_gather_kernel<F16, false>
-                    : a.dtype == NS_BF16 ? kv_gather_kernel<BF16, true> : kv_gather_kernel<F16, true>;
+    const bool bf16 = a.dtype == NS_BF16;
+    const void *kern = pool == 16  ? (const void *)kv_gather_kernel<F16, 16>
+                       : pool == 8 ? (bf16 ? (const void *)kv_gather_kernel<BF16, 8> : (const void *)kv_gather_kernel<F16, 8>)
+                                   : (bf16 ? (const void *)kv_gather_kernel<BF16, 4> : (const void *)kv_gather_kernel<F16, 4>);
+    void *args[] = {&a, &tokens, &row_chunks, &head_chunks};
+    return launch_early(kern, dim3(grid), kThreads, 0, stream, args);
+}
+
+cudaError_t launch_early(const void *kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, void **args)
+{
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     // its set-up overlaps the end of the kernel before, which it waits for
     cudaLaunchAttribute attr[1];
@@ -147,7 +165,7 @@ cudaError_t launch_kv_gather(const GatherArgs &a, bool q8, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, tokens, row_chunks, head_chunks);
+    return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
 }  // namespace ns

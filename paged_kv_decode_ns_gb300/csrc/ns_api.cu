@@ -8,6 +8,7 @@
 
 #include "ns_internal.h"
 #include "paged_decode.cuh"
+#include "q4_decode.h"
 
 namespace {
 
@@ -537,8 +538,10 @@ size_t ns_paged_attn_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
     (void)num_q_heads;
     if (num_seqs < 0 || num_kv_heads <= 0)
         return 0;
-    const int sub = kv_sub(num_q_heads, num_kv_heads);
-    return ws_layout(num_seqs, num_kv_heads * (sub > 0 ? sub : 1), head_dim == 128 ? 128 : 64).total;
+    // as many counters as the q4_0 decode needs too, whose groups need not be cut evenly
+    const int group = num_q_heads > 0 ? num_q_heads / num_kv_heads : 1;
+    const int sub = std::max(1, (group + ns::kMaxGroup - 1) / ns::kMaxGroup);
+    return ws_layout(num_seqs, num_kv_heads * sub, head_dim == 128 ? 128 : 64).total;
 }
 
 ns_status ns_paged_attn_workspace_init(void *workspace, size_t workspace_bytes, ns_stream_t stream)
@@ -805,6 +808,50 @@ ns_status ns_kv_append_paged_attn_decode_q8_0(const void *q, const void *k_new, 
     return decode_q8_0(q, k_new, v_new, slot_mapping, k_codes, k_scales, v_codes, v_scales, block_tables,
                        context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, scale, out,
                        stream, max_blocks_per_seq, num_blocks, dtype, workspace, workspace_bytes, nullptr);
+}
+
+ns_status ns_paged_attn_decode_q4_0(const void *q, const void *k_codes, const void *k_scales, const void *v_codes,
+                                    const void *v_scales, const int32_t *block_tables, const int32_t *context_lens,
+                                    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                    float scale, void *out, ns_stream_t stream, int max_blocks_per_seq,
+                                    int64_t num_blocks, ns_dtype dtype, void *workspace, size_t workspace_bytes)
+{
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0)
+        return NS_ERR_INVALID_ARG;
+    if (dtype != NS_F16 && dtype != NS_BF16)
+        return NS_ERR_UNSUPPORTED;
+    if ((head_dim != 64 && head_dim != 128) || bs_index(block_size) < 0 || (head_dim == 128 && block_size != 16))
+        return NS_ERR_UNSUPPORTED;
+    if (num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > kMaxLargeGroup)
+        return NS_ERR_UNSUPPORTED;
+    if (max_blocks_per_seq < 1 || num_blocks < 1 || !std::isfinite(scale))
+        return NS_ERR_INVALID_ARG;
+    const int subs = (num_q_heads / num_kv_heads + ns::kMaxGroup - 1) / ns::kMaxGroup;  // 8 query heads at a time
+    if ((long long)max_blocks_per_seq * block_size > 0x7fffffffLL - 1024 ||  // positions are 32-bit
+        !ns::q4_decode_fits(num_seqs, (long long)num_kv_heads * subs, max_blocks_per_seq, block_size))
+        return NS_ERR_UNSUPPORTED;
+    if (num_seqs == 0)
+        return NS_OK;
+    if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !block_tables || !context_lens || !out || !workspace)
+        return NS_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
+        !aligned16(out) || !aligned16(workspace))
+        return NS_ERR_INVALID_ARG;
+    if (workspace_bytes < ns_paged_attn_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim))
+        return NS_ERR_INVALID_ARG;
+    int dev = 0;
+    if (current_device(&dev) != cudaSuccess)
+        return NS_ERR_CUDA;
+    unsigned *status = status_word(dev);
+    if (status == nullptr)
+        return NS_ERR_CUDA;
+    const WsLayout L = ws_layout(num_seqs, num_kv_heads * subs, head_dim);
+    char *ws = static_cast<char *>(workspace);
+    const ns::Q4DecodeArgs a = {q, k_codes, k_scales, v_codes, v_scales, block_tables, context_lens, num_seqs,
+                                num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale,
+                                out, dtype, reinterpret_cast<int *>(ws + L.counters),
+                                reinterpret_cast<float *>(ws + L.partials), status};
+    return ns::launch_decode_q4(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? NS_OK : NS_ERR_CUDA;
 }
 
 ns_status ns_get_device_status(ns_stream_t stream, uint32_t *bits, int clear)

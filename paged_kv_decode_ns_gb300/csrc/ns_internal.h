@@ -18,6 +18,28 @@ cudaError_t launch_kv_append_q8(const void *k, const void *v, const int64_t *slo
                                 int block_size, long long num_blocks, ns_dtype dtype, unsigned *status,
                                 cudaStream_t stream);
 
+// New tokens' K and V rows into a pool; with `positions` their q and k rows are rotated on
+// the way.  pool: bits of a cached element (16, 8 or 4).
+struct RopeAppendArgs {
+    const void *q, *k, *v;
+    const int32_t *positions;  // nullptr: no rotation (and no q)
+    const float *cos_sin;
+    const int64_t *slot_mapping;
+    void *q_out, *k_out;  // k_out: nullptr when not wanted
+    void *k_pool, *v_pool;  // elements or codes
+    void *k_scales, *v_scales;
+    int num_tokens, num_q_heads, num_kv_heads, head_dim, rotary_dim, interleaved, max_positions, block_size;
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // elements from row to row
+    long long num_blocks;
+    ns_dtype dtype;
+    unsigned *status;
+};
+cudaError_t launch_rope_append(const RopeAppendArgs &a, int pool, cudaStream_t stream);
+
+// Launch as a programmatic dependent of the kernel in front: `kernel` starts while that one
+// ends, and waits for it (grid_dependency_wait) before it touches memory.
+cudaError_t launch_early(const void *kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, void **args);
+
 // Query spans -> per-row table row and key count (prefill through the decode
 // walk).  Rows of spans with at least `tc_min_span` tokens (tc_min_span > 0)
 // are marked for the tensor-core kernel: table row -1, key count 0.
@@ -48,7 +70,7 @@ cudaError_t launch_tc_prefill(const void *q, const int32_t *query_start_loc, con
                               cudaStream_t stream);
 
 // Attention of query spans over contiguous K/V rows (ns_prompt_attn) or a
-// q8_0 pool (ns_paged_attn_prefill_q8_0).
+// q8_0 or q4_0 pool (ns_paged_attn_prefill_q8_0, _q4_0).
 struct SpanAttnArgs {
     const void *q;
     const int32_t *query_start_loc;
@@ -64,7 +86,7 @@ struct SpanAttnArgs {
     const int32_t *key_start_loc;
     int total_k_tokens;
     long long k_row_stride, v_row_stride;
-    // q8_0 pool
+    // q8_0 or q4_0 pool
     const void *k_codes, *k_scales, *v_codes, *v_scales;
     const int32_t *block_tables, *context_lens;
     int max_blocks_per_seq;
@@ -74,12 +96,13 @@ struct SpanAttnArgs {
 cudaError_t current_sms(int *sms);
 constexpr int kMaxSpanGroup = 64;  // query heads per kv head
 size_t span_attn_workspace_bytes(int head_dim);
-cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream);
+// pool: 0 contiguous rows, 8 and 4 the bits of a pool's codes
+cudaError_t launch_span_attn(const SpanAttnArgs &a, int pool, cudaStream_t stream);
 
 // Pool rows of the sequences start_loc, packed: 16-bit copies or q8_0 values.
 struct GatherArgs {
     const void *k, *v;                // 16-bit pools, or codes
-    const void *k_scales, *v_scales;  // q8_0 only
+    const void *k_scales, *v_scales;  // 8- and 4-bit pools only
     const int32_t *block_tables, *start_loc;
     int num_seqs, total_tokens, num_kv_heads, head_dim, block_size, max_blocks_per_seq;
     long long num_blocks;
@@ -87,7 +110,7 @@ struct GatherArgs {
     ns_dtype dtype;
     unsigned *status;
 };
-cudaError_t launch_kv_gather(const GatherArgs &a, bool q8, cudaStream_t stream);
+cudaError_t launch_kv_gather(const GatherArgs &a, int pool, cudaStream_t stream);  // bits of an element
 
 struct VerifyArgs {
     const float *target, *draft;

@@ -29,7 +29,7 @@ cudaError_t current_sms(int *sms)
     return e;
 }
 
-cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream)
+cudaError_t launch_span_attn(const SpanAttnArgs &a, int pool, cudaStream_t stream)
 {
     int sms = 0;
     const cudaError_t e = current_sms(&sms);
@@ -52,10 +52,10 @@ cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream
         if (!encode_tensor_map(&tm.q, a.dtype, 3, a.q, dims, strides, box))
             return cudaErrorInvalidValue;
     }
-    if (!q8) {
+    if (pool == 0) {
         // K, V: [token][kv head][element], boxes of one head's 64 elements of a tile of
         // tokens; without a single key nothing is ever copied
-        const int kt = a.head_dim == 64 ? span::Geo<64, false>::KT : span::Geo<128, false>::KT;
+        const int kt = a.head_dim == 64 ? span::Geo<64, 0>::KT : span::Geo<128, 0>::KT;
         const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.num_kv_heads,
                                     (cuuint64_t)std::max(a.total_k_tokens, 1)};
         const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kt};
@@ -69,8 +69,8 @@ cudaError_t launch_span_attn(const SpanAttnArgs &a, bool q8, cudaStream_t stream
     }
     const int ctas = std::min(sms, span::kMaxCtas);
     const bool bf16 = a.dtype == NS_BF16;
-    if (q8)
-        return launch_span_q8(bf16, tm, P, ctas, stream);
+    if (pool != 0)
+        return pool == 4 ? launch_span_q4(bf16, tm, P, ctas, stream) : launch_span_q8(bf16, tm, P, ctas, stream);
     return a.head_dim == 64 ? launch_span_d64(bf16, tm, P, ctas, stream)
                             : launch_span_d128(bf16, tm, P, ctas, stream);
 }

@@ -1,6 +1,6 @@
 // span_attn.cuh -- causal attention of query spans on the tcgen05 tensor cores:
-// whole packed prompts over contiguous K/V rows, or new tokens over a q8_0
-// paged cache.
+// whole packed prompts over contiguous K/V rows, or new tokens over a q8_0 or
+// q4_0 paged cache.
 //
 // Row i of a span of n tokens over L keys sits at position L-n+i and sees the
 // keys p <= L-n+i: out = sum_p 2^(z_p - m) v_p / sum_p 2^(z_p - m) with z in
@@ -86,20 +86,22 @@ constexpr float kLift = 7.0f, kSlack = 8.0f;
 constexpr int kRoom = 3;   // the exponent of bf16 and q8_0 values is set for values 2^3 larger
 constexpr int kLeast = 54; // and not below this field: a sum times 2^84 stays in fp32
 
-template <int D, bool Q8>
+template <int D, int POOL>
 struct Geo {
+    static constexpr bool PAGED = POOL != 0;
+    static constexpr int CODES = POOL == 4 ? 32 : 64;  // bytes of a key's codes (head_dim 64)
     static constexpr int KT = D == 64 ? 128 : 64;  // keys of a tile
     static constexpr int REG = D / 64;             // panels of a row
     static constexpr int TILE = REG * KT * kPanel; // bytes of a K or V tile
     static constexpr int GROUP = KT / 4;           // keys of a conversion warp
-    static constexpr int STAGES = Q8 ? 3 : 4;
-    static constexpr int RAW = Q8 ? 3 : 1;         // q8_0 tiles in flight (4 measured 2 to 4 % slower)
+    static constexpr int STAGES = PAGED ? 3 : 4;
+    static constexpr int RAW = PAGED ? 3 : 1;         // q8_0 tiles in flight (4 measured 2 to 4 % slower)
     // TMEM columns: S of tile t at KT t, O at 2 KT + D t, P at 2 KT + 2 D + KT / 2 t
     static constexpr int O = 2 * KT, P = 2 * KT + 2 * D;
     static_assert(P + KT <= 512, "tensor memory");
     // cost of a unit besides its keys (laying out Q, filling the pipe, the epilogue)
     // and the least cost that a CTA is given, in keys
-    static constexpr int OVERHEAD = D == 128 ? 11 * KT / 2 : Q8 ? 5 * KT / 2 : 3 * KT;
+    static constexpr int OVERHEAD = D == 128 ? 11 * KT / 2 : PAGED ? 5 * KT / 2 : 3 * KT;
     static constexpr int SHARE = OVERHEAD;  // at most one short unit a CTA while there are CTAs
     static constexpr int WHOLE = 4;  // units of so few key tiles are not cut
 };
@@ -148,13 +150,13 @@ struct Maps {
     CUtensorMap q, k, v;  // k, v: contiguous rows only
 };
 
-template <int D, bool Q8>
+template <int D, int POOL>
 struct alignas(1024) Smem {
-    using GG = Geo<D, Q8>;
+    using GG = Geo<D, POOL>;
     uint8_t q[2][GG::REG * kRows * kPanel];
     uint8_t k[GG::STAGES][GG::TILE];
     uint8_t v[GG::STAGES][GG::TILE];
-    uint8_t raw[GG::RAW][Q8 ? 2 * GG::KT * 64 + 2 * GG::KT * 4 : 16];  // codes of K, of V, scales of K, of V
+    uint8_t raw[GG::RAW][GG::PAGED ? 2 * GG::KT * GG::CODES + 2 * GG::KT * 4 : 16];  // codes of K, of V, scales of K, of V
     uint64_t raw_full[GG::RAW], raw_empty[GG::RAW];
     uint64_t v_full[GG::STAGES];
     uint64_t k_ready[GG::STAGES], v_ready[GG::STAGES], k_empty[GG::STAGES], v_empty[GG::STAGES];
@@ -175,10 +177,10 @@ struct alignas(1024) Smem {
     uint32_t tmem_base;
 };
 
-template <int D, bool Q8>
+template <int D, int POOL>
 constexpr size_t smem_bytes()
 {
-    return sizeof(Smem<D, Q8>) + 1024;
+    return sizeof(Smem<D, POOL>) + 1024;
 }
 
 // ---------------------------------------------------------------------------
@@ -188,7 +190,7 @@ struct Seq {
     int q0, n, k0, L;  // n = 0: nothing to do
 };
 
-template <bool Q8>
+template <bool PAGED>
 __device__ __forceinline__ Seq read_seq(const SpanAttnArgs &a, int s, unsigned *status)
 {
     Seq r;
@@ -196,7 +198,7 @@ __device__ __forceinline__ Seq read_seq(const SpanAttnArgs &a, int s, unsigned *
     const int q1 = a.query_start_loc[s + 1];
     r.n = q1 - r.q0;
     unsigned bad = r.q0 < 0 || q1 < r.q0 || q1 > a.total_q_tokens ? NS_DEV_BAD_QUERY_SPAN : 0u;
-    if (Q8) {
+    if (PAGED) {
         r.k0 = 0;
         r.L = a.context_lens[s];
         if (r.L < r.n)
@@ -368,17 +370,33 @@ __device__ __forceinline__ uint2 codes_to_f16(uint32_t w, __half2 d)
     return r;
 }
 
+// Eight q4_0 codes (a word) -> four fp16 pairs of (code - 8) * d, the product rounded once.
+__device__ __forceinline__ uint4 nibbles_to_f16(uint32_t w, __half2 d)
+{
+    const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+    const uint32_t a = __byte_perm(even, odd, 0x5140), b = __byte_perm(even, odd, 0x7362);  // elements 0-3, 4-7
+    const __half2 off = __half2half2(__ushort_as_half(0x6408));  // 1032
+    uint4 r = make_uint4(__byte_perm(a, 0x64646464u, 0x4140), __byte_perm(a, 0x64646464u, 0x4342),
+                         __byte_perm(b, 0x64646464u, 0x4140), __byte_perm(b, 0x64646464u, 0x4342));
+    __half2 *h = reinterpret_cast<__half2 *>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = __hmul2(__hsub2(h[i], off), d);
+    return r;
+}
+
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
-template <typename T, int D, bool Q8>
+template <typename T, int D, int POOL>
 __global__ void __launch_bounds__(kThreads, 1)
     span_attn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params P)
 {
-    using GG = Geo<D, Q8>;
-    constexpr int KT = GG::KT, REG = GG::REG, ST = GG::STAGES;
+    using GG = Geo<D, POOL>;
+    constexpr bool PAGED = GG::PAGED;
+    constexpr int KT = GG::KT, REG = GG::REG, ST = GG::STAGES, CODES = GG::CODES;
     constexpr bool BF = T::code == NS_BF16;
-    constexpr bool SCALED = Q8 || BF;  // V tiles carry an exponent
+    constexpr bool SCALED = PAGED || BF;  // V tiles carry an exponent
     // The softmax reads that exponent with the scores, which then wait for the tile's V, or
     // only before it touches O.  The second is faster at head_dim 128, where the conversion
     // is behind (8192 bf16 tokens 480 us against 488, packed prompts 209 against 214), the
@@ -386,12 +404,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool LATE = BF && D == 128;
     constexpr bool Q_TMA = q_by_tma(D, BF);
     extern __shared__ unsigned char smem_raw[];
-    Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem<D, POOL> &sm = *reinterpret_cast<Smem<D, POOL> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const SpanAttnArgs &a = P.a;
     const int qt = P.qt, R = 2 * P.qt;
 
-    if (!Q8 && threadIdx.x == kProducerWarp * 32) {
+    if (!PAGED && threadIdx.x == kProducerWarp * 32) {
         tc::prefetch_tensormap(&maps.k);
         tc::prefetch_tensormap(&maps.v);
     }
@@ -399,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::prefetch_tensormap(&maps.q);
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&sm.k_ready[i], Q8 ? 4 : 1);
+            mbar_init(&sm.k_ready[i], PAGED ? 4 : 1);
             mbar_init(&sm.v_full[i], 1);
             mbar_init(&sm.v_ready[i], 4);
             mbar_init(&sm.k_empty[i], 2);  // both tiles' products
@@ -437,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // CTA more of them, a share for every thread
     {
         auto cost = [&](int s, unsigned *status) -> long long {
-            const Seq q = read_seq<Q8>(a, s, status);
+            const Seq q = read_seq<PAGED>(a, s, status);
             if (q.n == 0)
                 return 0;
             const long long units = ceil_div(q.n, R), each = GG::OVERHEAD + max(q.L - q.n, 0);
@@ -550,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
                 w[c] = on ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-            if (Q8 && BF) {
+            if (PAGED && BF) {
                 // fp16 for the product with fp16 keys: the row's largest value goes
                 // just below 2^15, its power of two into the score's scale
                 uint32_t m = 0;
@@ -598,13 +616,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // scale of the scores, by group of keys, and exponent of the values; the
                 // weights are summed by groups of four for all but fp16 values (bf16 packed
                 // prompts 78.9 us, 80.2 in one)
-                constexpr int NG = Q8 ? 4 : 1, NS = SCALED ? 4 : 1, GK = KT / NS;
+                constexpr int NG = PAGED ? 4 : 1, NS = SCALED ? 4 : 1, GK = KT / NS;
                 const int tile = vtile + j - t0;
                 float sc[NG];
                 float ev = SCALED && !LATE ? sm.ev[tile % ST] : 0.f;
                 uint32_t loaded = 0xffffffffu;
                 sc[0] = row_scale;
-                if (Q8) {
+                if (PAGED) {
                     const float4 k4 = *reinterpret_cast<const float4 *>(sm.ek[tile % kMeta]);
                     const float k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
@@ -626,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < KT; ++c)
                         sv[c] = c <= lim ? sv[c] : -INFINITY;
                 }
-                if (Q8 && (loaded & 0xffu) != 0xffu) {  // blocks that are not in the pool count for nothing
+                if (PAGED && (loaded & 0xffu) != 0xffu) {  // blocks that are not in the pool count for nothing
 #pragma unroll
                     for (int c = 0; c < KT; ++c)
                         sv[c] = (loaded >> (c / 16)) & 1u ? sv[c] : -INFINITY;
@@ -639,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)  // a quarter of the columns each
                             tm[e] = max3(tm[e], sv[e * (KT / 4) + c], sv[e * (KT / 4) + c + 1]);
-                    if (Q8) {
+                    if (PAGED) {
 #pragma unroll
                         for (int g = 0; g < NG; ++g)
                             top = fmaxf(top, tm[g] * sc[g]);
@@ -772,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ conversion
         regs_shrink<kConvertRegs>();
         // a warp a group of keys; a lane a key (D 64) or one panel of a key
+        constexpr int STEP = POOL == 4 ? 26 : 22;  // exponent field that a step is scaled to
         const int group = warp - kConvertWarp;
         const int key = group * GG::GROUP + lane / REG, pan = lane % REG;
         const int panel = pan * (KT * kPanel) + key * kPanel;
@@ -784,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int stage = tile % ST;
                 const uint32_t par = (uint32_t)(tile / ST) & 1u;
                 const bool live = j * KT + key < u.L;  // a row behind the last key is zero
-                if (!Q8) {
+                if (!PAGED) {
                     warp_wait(&sm.v_full[stage], par, ok);
                     uint8_t *row = sm.v[stage] + panel;
                     if (BF) {
@@ -825,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint8_t *raw = sm.raw[rs];
                     const uint32_t loaded = sm.raw_loaded[rs];
                     const bool have = live && ((loaded >> (key / 16)) & 1u);
-                    const uint32_t *scales = reinterpret_cast<const uint32_t *>(raw + 2 * KT * 64);
+                    const uint32_t *scales = reinterpret_cast<const uint32_t *>(raw + 2 * KT * CODES);
                     const uint32_t d[2] = {have ? scales[key] : 0u, have ? scales[KT + key] : 0u};
                     // the tile's largest scale of V, four keys a lane (those that are there)
                     const int key4 = 4 * lane;
@@ -839,43 +858,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t vmag = larger_f16(larger_f16(w4.x, w4.y), larger_f16(w4.z, w4.w));
                     // code chunks in an order in which neither the reads (64-byte rows) nor the
-                    // writes (swizzled 128-byte rows) of eight lanes share a bank
-                    const int half = (key >> 1) & 3, first = (half << 1) ^ ((half >> 1) * 7);
-                    uint4 code[2][4];
+                    // writes (swizzled 128-byte rows) of eight lanes share a bank (of the two reads
+                    // of 32-byte rows, four lanes and four do)
+                    constexpr int CHUNKS = CODES / 16;
+                    const int half = (key >> 1) & 3, first = CHUNKS == 4 ? (half << 1) ^ ((half >> 1) * 7) : 0;
+                    uint4 code[2][CHUNKS];
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            code[x][c] = lds128(raw + x * KT * 64 + key * 64 + ((c ^ first) << 4));
+                        for (int c = 0; c < CHUNKS; ++c)
+                            code[x][c] = lds128(raw + x * KT * CODES + key * CODES + ((c ^ first) << 4));
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        // the largest scale of these keys' K goes just below 2^8, its codes below
-                        // 2^15; the unit's largest of V so far there or up to 2^kRoom lower
+                        // the largest scale of these keys' K goes just below 2^8 (4 bits: 2^12), its
+                        // codes below 2^15; the unit's largest of V so far there or up to 2^kRoom lower
                         if (x == 1)
                             raise((int)(__reduce_max_sync(0xffffffffu, top_of(vmag)) >> 10));
                         const int e = x == 0 ? (int)(__reduce_max_sync(0xffffffffu, top_of(d[0])) >> 10) : most;
                         const float2 ds = unpack2<F16>(d[x]);
-                        const float f = pow2(22 - e);
+                        const float f = pow2(STEP - e);
                         const __half2 dd[2] = {__float2half2_rn(ds.x * f), __float2half2_rn(ds.y * f)};
                         warp_wait(x == 0 ? &sm.k_empty[stage] : &sm.v_empty[stage], par ^ 1u, ok);
                         if (lane == 0) {
                             if (x == 0)
-                                sm.ek[tile % kMeta][group] = pow2(e - 22);
+                                sm.ek[tile % kMeta][group] = pow2(e - STEP);
                             else if (group == 0)
-                                sm.ev[stage] = (float)(e - 22);
+                                sm.ev[stage] = (float)(e - STEP);
                             if (x == 0 && group == 0)
                                 sm.loaded[tile % kMeta] = loaded;
                         }
                         uint8_t *row = (x == 0 ? sm.k[stage] : sm.v[stage]) + panel;
 #pragma unroll
-                        for (int c0 = 0; c0 < 4; ++c0) {
+                        for (int c0 = 0; c0 < CHUNKS; ++c0) {
                             const int c = c0 ^ first;
                             const uint4 q = code[x][c0];
-                            const __half2 s2 = c < 2 ? dd[0] : dd[1];
-                            const uint2 e0 = codes_to_f16(q.x, s2), e1 = codes_to_f16(q.y, s2),
-                                        e2 = codes_to_f16(q.z, s2), e3 = codes_to_f16(q.w, s2);
-                            *reinterpret_cast<uint4 *>(row + (((2 * c) ^ (key & 7)) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
-                            *reinterpret_cast<uint4 *>(row + (((2 * c + 1) ^ (key & 7)) << 4)) = make_uint4(e2.x, e2.y, e3.x, e3.y);
+                            if constexpr (POOL == 4) {
+                                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    *reinterpret_cast<uint4 *>(row + (((4 * c + i) ^ (key & 7)) << 4)) = nibbles_to_f16(w[i], dd[c]);
+                            } else {
+                                const __half2 s2 = c < 2 ? dd[0] : dd[1];
+                                const uint2 e0 = codes_to_f16(q.x, s2), e1 = codes_to_f16(q.y, s2),
+                                            e2 = codes_to_f16(q.z, s2), e3 = codes_to_f16(q.w, s2);
+                                *reinterpret_cast<uint4 *>(row + (((2 * c) ^ (key & 7)) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
+                                *reinterpret_cast<uint4 *>(row + (((2 * c + 1) ^ (key & 7)) << 4)) = make_uint4(e2.x, e2.y, e3.x, e3.y);
+                            }
                         }
                         fence_async_smem();
                         __syncwarp();
@@ -893,11 +921,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------------------ producer
             int tile = 0;
             for (Unit u = next_unit(); ok && u.t1 >= 0; u = next_unit()) {
-                const int blocks = Q8 ? ceil_div(u.L, 16) : 0;
+                const int blocks = PAGED ? ceil_div(u.L, 16) : 0;
                 for (int j = u.t0; ok && j < u.t1; ++j, ++tile) {
                     const int stage = tile % ST;
                     const uint32_t par = ((uint32_t)(tile / ST) & 1u) ^ 1u;
-                    if (!Q8) {
+                    if (!PAGED) {
                         if (lane == 0) {
                             const int row = u.k0 + j * KT;
                             ok = mbar_wait(&sm.k_empty[stage], par);
@@ -941,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     mask |= ((fine >> (4 * i)) & 1u) << i;
                                 sm.raw_loaded[rs] = mask;
                                 mbar_arrive_expect_tx(&sm.raw_full[rs],
-                                                      (uint32_t)(__popc(have) / 4) * 2u * (16u * 64u + 16u * 4u));
+                                                      (uint32_t)(__popc(have) / 4) * 2u * (16u * CODES + 16u * 4u));
                             }
                         }
                         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -949,11 +977,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const long long row = ((long long)phys * a.num_kv_heads + u.h) * 16;
                             uint8_t *raw = sm.raw[rs];
                             if (what < 2)
-                                bulk_load(raw + what * KT * 64 + b * 1024,
-                                          static_cast<const uint8_t *>(what == 0 ? a.k_codes : a.v_codes) + row * 64, 1024u,
-                                          &sm.raw_full[rs]);
+                                bulk_load(raw + what * KT * CODES + b * 16 * CODES,
+                                          static_cast<const uint8_t *>(what == 0 ? a.k_codes : a.v_codes) + row * CODES,
+                                          16u * CODES, &sm.raw_full[rs]);
                             else
-                                bulk_load(raw + 2 * KT * 64 + (what - 2) * KT * 4 + b * 64,
+                                bulk_load(raw + 2 * KT * CODES + (what - 2) * KT * 4 + b * 64,
                                           static_cast<const uint8_t *>(what == 2 ? a.k_scales : a.v_scales) + row * 4, 64u,
                                           &sm.raw_full[rs]);
                         }
@@ -964,10 +992,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the last tile of every stage has arrived.
             if (lane == 0) {
                 bool drained = true;
-                const int depth = Q8 ? GG::RAW : ST;
+                const int depth = PAGED ? GG::RAW : ST;
                 for (int i = 1; drained && i <= depth && i <= tile; ++i) {
                     const int x = tile - i;
-                    if (Q8)
+                    if (PAGED)
                         drained = mbar_wait(&sm.raw_full[x % GG::RAW], (uint32_t)(x / GG::RAW) & 1u);
                     else
                         drained = mbar_wait(&sm.k_ready[x % ST], (uint32_t)(x / ST) & 1u) &&
@@ -983,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // of j were read, then the values of j as soon as its weights are there.  The
             // whole warp walks the tiles; operands are warp-uniform.
             const int t = warp - kProductWarp;
-            const uint32_t idesc_s = tc::idesc_f16(kRows, KT, BF && !Q8 ? 1 : 0, false) | (P.negate ? tc::kNegateA : 0u);
+            const uint32_t idesc_s = tc::idesc_f16(kRows, KT, BF && !PAGED ? 1 : 0, false) | (P.negate ? tc::kNegateA : 0u);
             const uint32_t idesc_o = tc::idesc_f16(kRows, D, 0, true);
             const uint64_t dk = tc::desc_sw128(0), dv = tc::desc_sw128_panels(0, KT * kPanel);
             auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
@@ -1107,7 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (held < 0 || s >= held + 32) {
                         held = s;
                         if (s + lane < a.num_seqs)
-                            mine = read_seq<Q8>(a, s + lane, nullptr);
+                            mine = read_seq<PAGED>(a, s + lane, nullptr);
                         else
                             mine.n = 0;
                     }
@@ -1276,10 +1304,10 @@ __global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // Launch
 // ---------------------------------------------------------------------------
-template <typename T, int D, bool Q8>
+template <typename T, int D, int POOL>
 cudaError_t launch(const Maps &tm, const Params &P, int ctas, cudaStream_t stream)
 {
-    const long long max_keys = Q8 ? (long long)P.a.max_blocks_per_seq * 16 : P.a.total_k_tokens;
+    const long long max_keys = POOL != 0 ? (long long)P.a.max_blocks_per_seq * 16 : P.a.total_k_tokens;
     // once for each device: the shared memory, and that the kernel has the registers
     // that its warpgroups share out (with fewer they would wait for ever)
     static unsigned long long ready = 0;
@@ -1289,12 +1317,12 @@ cudaError_t launch(const Maps &tm, const Params &P, int ctas, cudaStream_t strea
         return e;
     if (dev >= 64 || !((__atomic_load_n(&ready, __ATOMIC_RELAXED) >> dev) & 1ull)) {
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, span_attn_kernel<T, D, Q8>);
+        e = cudaFuncGetAttributes(&fa, span_attn_kernel<T, D, POOL>);
         if (e == cudaSuccess && fa.numRegs != kRegs)
             e = cudaErrorInvalidValue;
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(span_attn_kernel<T, D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)smem_bytes<D, Q8>());
+            e = cudaFuncSetAttribute(span_attn_kernel<T, D, POOL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)smem_bytes<D, POOL>());
         if (e != cudaSuccess)
             return e;
         if (dev < 64)
@@ -1305,17 +1333,17 @@ cudaError_t launch(const Maps &tm, const Params &P, int ctas, cudaStream_t strea
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<D, Q8>();
+    cfg.dynamicSmemBytes = smem_bytes<D, POOL>();
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, span_attn_kernel<T, D, Q8>, tm, P);
+    e = cudaLaunchKernelEx(&cfg, span_attn_kernel<T, D, POOL>, tm, P);
     // no sequence has the keys of a unit that may be cut (the second launch costs
     // 3 us of a small call)
-    if (e != cudaSuccess || max_keys <= Geo<D, Q8>::WHOLE * Geo<D, Q8>::KT)
+    if (e != cudaSuccess || max_keys <= Geo<D, POOL>::WHOLE * Geo<D, POOL>::KT)
         return e;
     cfg.gridDim = dim3(ctas * 8);
     cfg.blockDim = dim3(256);
@@ -1327,6 +1355,7 @@ cudaError_t launch(const Maps &tm, const Params &P, int ctas, cudaStream_t strea
 
 cudaError_t launch_span_d64(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
 cudaError_t launch_span_d128(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
+cudaError_t launch_span_q4(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
 cudaError_t launch_span_q8(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
 
 }  // namespace ns
