@@ -3,15 +3,18 @@
 // out = sum_p 2^(z_p - m) v_p / sum_p 2^(z_p - m), z in log2 units, in one pass over the
 // keys with a running reference m.  K_p = dk_p (c - 8) and V_p = dv_p (c - 8) by group of 32
 // elements, so that with integer codes c
-//   z_p = scale sum_g dk_pg (q_g . (c_pg - 8)),   out_g = sum_p (w_p dv_pg) (c_pg - 8):
-// the codes less 8 are exact in fp16, and the steps are applied to the scores and to the weights,
-// 8 heads wide, instead of to 64 or 128 elements.  Both sums are small matrix products
-// (mma.m16n8k16: 16 tokens or elements by the 8 query heads of a group, fp32 sums).  A tcgen05
+//   z_p = scale sum_g dk_pg (q_g . c_pg - 8 sum q_g),
+//   out_g = sum_p w_p' c_pg - 8 sum_p w_p',   w_p' = w_p dv_pg:
+// the steps are applied to the scores and to the weights, 8 heads wide, instead of to 64 or 128
+// elements, and the 8 once for a row of q, and once for the sum of a group's w'.  A code is
+// used as it lies: four bits at the bottom of an fp16 word are the (subnormal) number c 2^-24, or
+// c 2^-20 one place higher, so one AND makes two operands.  Both sums are small matrix
+// products (mma.m16n8k16: 16 tokens or elements by the 8 query heads of a group, fp32 sums).  A tcgen05
 // product has 128 rows at least and its operands in shared memory, where each code would
 // be four times as large as in the cache; here they go from the codes to the product in registers.
 //
-// Only two factors are rounded: q to fp16, scaled by a power of two (exact down to 2^-28 of the
-// row's largest element, off by 2^-39 of that below) and w dv to fp16 (2^-11 of itself, or 2^-32
+// Only two factors are rounded: q to fp16, scaled by a power of two (exact down to 2^-24 of the
+// row's largest element, off by 2^-35 of that below) and w dv to fp16 (2^-11 of itself, or 2^-32
 // of the largest weight times the largest step so far).
 //
 // Work.  The pairs (sequence, kv head, 8 query heads) lie end to end on a line, in chunks of
@@ -62,8 +65,6 @@ struct alignas(16) Smem {
     // one goes to its pair's end
     int first_pair[GG::WARPS], first_ends[GG::WARPS], last_pair[GG::WARPS];
     int arrived_last[2], pieces[2], first_cta[2];
-    float weight[kMaxQ4Ctas][8];
-    float inv[8];
     static_assert(GG::STAGES * GG::STAGE >= GG::RECORD * 4, "a record fits a warp's ring");
 };
 
@@ -118,36 +119,33 @@ __device__ __forceinline__ void product(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes 0 .. 15 of a word, four bits each -> fp16 pairs of code - 8: code i beside code i + 4.
-// A code in the low bits of an fp16 1024 is 1024 + c, four bits higher 1024 + 16 c.
-__device__ __forceinline__ void codes_less_8(uint32_t (&p)[4], uint32_t w)
+// Eight codes of a word -> fp16 pairs, code i beside code i + 4: c 2^-24 for i = 0 and 2,
+// c 2^-20 for i = 1 and 3.
+__device__ __forceinline__ void codes_in_place(uint32_t (&p)[4], uint32_t w)
 {
-    auto place = [](uint32_t x, uint32_t mask) {
-        uint32_t r;  // (x & mask) | 1024 in both halves
-        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "r"(0x64006400u));
-        return r;
-    };
-    auto low = [](uint32_t x) {
-        const __half2 h = __hsub2(*reinterpret_cast<__half2 *>(&x), __half2half2(__ushort_as_half(0x6408)));  // 1032
-        return *reinterpret_cast<const uint32_t *>(&h);
-    };
-    auto high = [](uint32_t x) {
-        const __half2 h = __hfma2(*reinterpret_cast<__half2 *>(&x), __half2half2(__ushort_as_half(0x2c00)),  // 1/16
-                                  __half2half2(__ushort_as_half(0xd480)));                                  // -72
-        return *reinterpret_cast<const uint32_t *>(&h);
-    };
     const uint32_t v = w >> 8;
-    p[0] = low(place(w, 0x000f000fu));
-    p[1] = high(place(w, 0x00f000f0u));
-    p[2] = low(place(v, 0x000f000fu));
-    p[3] = high(place(v, 0x00f000f0u));
+    p[0] = w & 0x000f000fu;
+    p[1] = w & 0x00f000f0u;
+    p[2] = v & 0x000f000fu;
+    p[3] = v & 0x00f000f0u;
 }
+constexpr float kCode = 16777216.f, kCodeHigh = 1048576.f;  // 2^24, 2^20
+constexpr uint32_t kOnes = 0x3c003c00u;                       // two fp16 ones
 
 __device__ __forceinline__ uint32_t larger_f16(uint32_t a, uint32_t b)  // magnitudes, signs of no meaning
 {
     uint32_t r;
     asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+// The same with a sum that starts elsewhere.
+__device__ __forceinline__ void product(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, float c0, float c1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
 __device__ __forceinline__ float2 halves(uint32_t w) { return unpack2<F16>(w); }
@@ -282,59 +280,72 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
     // ---- copies: a chunk's codes and scales of K and V by 16 bytes a lane
     const uint32_t ring = smem_addr(sm.ring[warp][0]);
     const int bs1 = (1 << P.shift) - 1;
+    constexpr uint32_t row_bytes = D / 2;
+    const uint32_t block_rows = (uint32_t)a.num_kv_heads << P.shift;  // the pool's row numbers have 32 bits
+    constexpr int N = kChunk / SPAN;  // lanes that copy the scales of K, and again of V
+    const uint8_t *k_from = static_cast<const uint8_t *>(a.k_codes) + lane % PARTS * 16,
+                  *v_from = static_cast<const uint8_t *>(a.v_codes) + lane % PARTS * 16,
+                  *s_from = static_cast<const uint8_t *>(lane < N ? a.k_scales : a.v_scales);
     Piece ip;
     ip.c = ip.c1 = 0;
     ip.s = ip.h = ip.L = 0;
-    int entry = -1;      // the block of this lane's token in the next chunk to copy
-    int issued = 0;      // chunks, modulo ST
-    const uint32_t row_bytes = D / 2, block_rows = (uint32_t)a.num_kv_heads << P.shift;
+    int entry = -1;           // the block of this lane's token in the next chunk to copy
+    uint32_t head_row = 0u;   // first row of the piece's kv head in a block
+    const int32_t *row_of = nullptr;  // its sequence's table row
+    uint32_t to = ring;
+    int issued = 0;           // chunks, modulo ST
     auto look_up = [&]() {  // the next chunk's blocks, whose piece may be another one
-        while (ip.c == ip.c1 && ahead_walk.left > 0)
-            ip = next_piece(P, ahead_walk);
-        entry = -1;
-        if (ip.c < ip.c1) {
-            const int tok = ip.c * kChunk + lane;
-            if (tok < ip.L)
-                entry = a.block_tables[(long long)ip.s * a.max_blocks_per_seq + (tok >> P.shift)];
+        if (ip.c == ip.c1) {
+            while (ip.c == ip.c1 && ahead_walk.left > 0)
+                ip = next_piece(P, ahead_walk);
+            if (ip.c < ip.c1) {
+                const int kv = P.subs == 1 ? ip.h : ip.h / P.subs;
+                head_row = (uint32_t)kv << P.shift;
+                row_of = a.block_tables + (long long)ip.s * a.max_blocks_per_seq;
+            }
         }
+        entry = -1;
+        const int tok = ip.c * kChunk + lane;
+        if (ip.c < ip.c1 && tok < ip.L)
+            entry = row_of[tok >> P.shift];
     };
     auto issue = [&]() {
         if (ip.c < ip.c1) {
-            const int tok = ip.c * kChunk + lane;
-            const bool have = tok < ip.L, ok = have && entry >= 0 && entry < a.num_blocks;
-            if (have && !ok)
+            const bool ok = entry >= 0 && entry < a.num_blocks;
+            if (!ok && ip.c * kChunk + lane < ip.L)
                 raise_status(a.status, NS_DEV_BAD_BLOCK_ID);
             const uint32_t live = __ballot_sync(0xffffffffu, ok);
             if (lane == 0)
                 sm.live[warp][issued] = live;
-            const uint32_t to = ring + issued * GG::STAGE;
-            const int kv = P.subs == 1 ? ip.h : ip.h / P.subs;
-            const uint32_t head_row = (uint32_t)kv << P.shift;
+            const int block = ok ? entry : -1;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i) {
-                const int idx = lane + 32 * i, tau = idx / PARTS, part = idx % PARTS;
-                const int id = __shfl_sync(0xffffffffu, entry, tau);
-                if ((live >> tau) & 1u) {
-                    const long long at = ((long long)id * block_rows + head_row + (tau & bs1)) * row_bytes + part * 16;
-                    // eight rows of one part are eight different banks of 16 bytes
-                    const int turned = D == 64 ? part ^ ((tau >> 2) & 1) : part ^ ((tau >> 1) & 3);
-                    const uint32_t dst = to + tau * row_bytes + turned * 16;
-                    copy16(dst, static_cast<const uint8_t *>(a.k_codes) + at);
-                    copy16(dst + GG::CODES, static_cast<const uint8_t *>(a.v_codes) + at);
+                const int tau = lane / PARTS + i * (32 / PARTS), part = lane % PARTS;
+                const int id = __shfl_sync(0xffffffffu, block, tau);
+                // eight rows of one part are eight different banks of 16 bytes
+                const int turned = D == 64 ? part ^ ((tau >> 2) & 1) : part ^ ((tau >> 1) & 3);
+                const uint32_t dst = to + tau * row_bytes + turned * 16;
+                if (id >= 0) {
+                    const uint32_t row = (uint32_t)id * block_rows + (head_row + (tau & bs1));
+                    copy16(dst, k_from + (unsigned long long)row * row_bytes);
+                    copy16(dst + GG::CODES, v_from + (unsigned long long)row * row_bytes);
                 }
             }
             {
-                constexpr int N = kChunk / SPAN;  // lanes for K, and again for V
                 const int tau = (lane % N) * SPAN;
-                const int id = __shfl_sync(0xffffffffu, entry, tau);
-                if (lane < 2 * N && ((live >> tau) & 1u)) {
-                    const long long at = ((long long)id * block_rows + head_row + (tau & bs1)) * (2 * R);
-                    const void *src = lane < N ? a.k_scales : a.v_scales;
-                    copy16(to + 2 * GG::CODES + lane * 16, static_cast<const uint8_t *>(src) + at);
+                const int id = __shfl_sync(0xffffffffu, block, tau);
+                if (id >= 0 && lane < 2 * N) {
+                    const uint32_t row = (uint32_t)id * block_rows + (head_row + (tau & bs1));
+                    copy16(to + 2 * GG::CODES + lane * 16, s_from + (unsigned long long)row * (2 * R));
                 }
             }
             ++ip.c;
-            issued = issued + 1 == ST ? 0 : issued + 1;
+            ++issued;
+            to += GG::STAGE;
+            if (issued == ST) {
+                issued = 0;
+                to = ring;
+            }
             look_up();
         }
         copies_commit();
@@ -354,7 +365,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
         const int head0 = kv * P.group + sub * 8, heads = min(8, P.group - sub * 8);
         // q of head g, elements 8 t .. 8 t + 7 of each group, as the products' second operand
         uint32_t q[R][4];
-        float q_unit;  // 2^-e: what a unit of the products is worth
+        float q_unit;      // 2^-e: what a unit of q is worth
+        float q_sum[R];    // -8 times the sum of a group, as the products count
         {
             uint4 w[R];
             float top = 0.f;
@@ -387,14 +399,27 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                     v[2 * i] = y.x * f;
                     v[2 * i + 1] = y.y * f;
                 }
+                // elements i and i + 4, less four binary places where the code is that much higher
+                float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    q[r][i] = pack2<F16>(v[i], v[i + 4]);
+                for (int i = 0; i < 4; ++i) {
+                    const float less = i & 1 ? 0.0625f : 1.f;
+                    q[r][i] = pack2<F16>(v[i] * less, v[i + 4] * less);
+                    const float2 y = halves(q[r][i]);
+                    sum = fmaf(y.x + y.y, i & 1 ? 16.f : 1.f, sum);
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                q_sum[r] = sum * (-8.f / kCode);
             }
         }
-        // of the two heads of this lane's columns
-        const float2 unit = make_float2(P.scale_log2 * __shfl_sync(0xffffffffu, q_unit, 8 * t),
-                                        P.scale_log2 * __shfl_sync(0xffffffffu, q_unit, 8 * t + 4));
+        // of the two heads of this lane's columns: a unit of the products, and where they start
+        const float2 unit = make_float2(P.scale_log2 * (__shfl_sync(0xffffffffu, q_unit, 8 * t) * kCode),
+                                        P.scale_log2 * (__shfl_sync(0xffffffffu, q_unit, 8 * t + 4) * kCode));
+        float2 base[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            base[r] = make_float2(__shfl_sync(0xffffffffu, q_sum[r], 8 * t), __shfl_sync(0xffffffffu, q_sum[r], 8 * t + 4));
 
         float O[R][2][4];
 #pragma unroll
@@ -404,6 +429,12 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     O[r][u][i] = 0.f;
+        float sums[R][4];  // of a group's weights times steps, of either head (twice over)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sums[r][i] = 0.f;
         float2 l = make_float2(0.f, 0.f), m = make_float2(kNone, kNone), limit = m;
         int top_e = -1;            // exponent field of the largest V step so far
         uint32_t step_limit = 0u;  // and the largest fp16 of that exponent
@@ -420,7 +451,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
             // ---- scores: 16 tokens at a time, by group
             float2 z[2][2];  // [tile][token g or g + 8] of the two heads
             uint32_t dv[2][2][R / 2];
-            uint32_t largest = 0u;
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
                 uint32_t dk[2][R / 2];
@@ -435,15 +465,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                         dk[i][0] = x.x, dk[i][1] = x.y;
                         dv[tile][i][0] = y.x, dv[tile][i][1] = y.y;
                     }
-                    if (live != 0xffffffffu && !((live >> (tile * 16 + i * 8 + g)) & 1u))
-#pragma unroll
-                        for (int j = 0; j < R / 2; ++j)
-                            dv[tile][i][j] = 0u;
-#pragma unroll
-                    for (int j = 0; j < R / 2; ++j)
-                        largest = larger_f16(largest, dv[tile][i][j]);
                 }
-                z[tile][0] = z[tile][1] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int r2 = 0; r2 < R; r2 += 2) {
                     uint32_t w[4];
@@ -456,24 +478,36 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                     for (int j = 0; j < 2; ++j) {
                         const int r = r2 + j;
                         uint32_t lo[4], hi[4];
-                        codes_less_8(lo, w[2 * j]);
-                        codes_less_8(hi, w[2 * j + 1]);
-                        float s[4] = {0.f, 0.f, 0.f, 0.f};
-                        product(s, lo[0], hi[0], lo[1], hi[1], q[r][0], q[r][1]);
+                        codes_in_place(lo, w[2 * j]);
+                        codes_in_place(hi, w[2 * j + 1]);
+                        float s[4];
+                        product(s, lo[0], hi[0], lo[1], hi[1], q[r][0], q[r][1], base[r].x, base[r].y);
                         product(s, lo[2], hi[2], lo[3], hi[3], q[r][2], q[r][3]);
                         const float2 d0 = halves(dk[0][r2 / 2]), d1 = halves(dk[1][r2 / 2]);
                         const float e0 = j == 0 ? d0.x : d0.y, e1 = j == 0 ? d1.x : d1.y;
-                        z[tile][0] = ffma2(make_float2(s[0], s[1]), make_float2(e0, e0), z[tile][0]);
-                        z[tile][1] = ffma2(make_float2(s[2], s[3]), make_float2(e1, e1), z[tile][1]);
+                        const float2 y0 = make_float2(s[0], s[1]), y1 = make_float2(s[2], s[3]);
+                        z[tile][0] = r == 0 ? fmul2(y0, make_float2(e0, e0)) : ffma2(y0, make_float2(e0, e0), z[tile][0]);
+                        z[tile][1] = r == 0 ? fmul2(y1, make_float2(e1, e1)) : ffma2(y1, make_float2(e1, e1), z[tile][1]);
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    z[tile][i] = fmul2(z[tile][i], unit);
-                    if (live != 0xffffffffu && !((live >> (tile * 16 + i * 8 + g)) & 1u))
-                        z[tile][i] = make_float2(-INFINITY, -INFINITY);
-                }
+                z[tile][0] = fmul2(z[tile][0], unit);
+                z[tile][1] = fmul2(z[tile][1], unit);
             }
+            if (live != 0xffffffffu)  // a token that is not there has neither a weight nor a step
+#pragma unroll
+                for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (!((live >> (tile * 16 + i * 8 + g)) & 1u)) {
+                            z[tile][i] = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+                            for (int j = 0; j < R / 2; ++j)
+                                dv[tile][i][j] = 0u;
+                        }
+            uint32_t largest = dv[0][0][0];
+#pragma unroll
+            for (int x = 1; x < 4 * (R / 2); ++x)
+                largest = larger_f16(largest, dv[x / (R / 2) / 2][x / (R / 2) % 2][x % (R / 2)]);
 
             // ---- the reference moves when a weight times a step would leave fp16's range
             const float za = fmaxf(fmaxf(z[0][0].x, z[0][1].x), fmaxf(z[1][0].x, z[1][1].x));
@@ -506,6 +540,11 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                         O[r][u][2] *= f.x;
                         O[r][u][3] *= f.y;
                     }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    sums[r][0] *= f.x;
+                    sums[r][1] *= f.y;
+                }
             }
 
             // ---- weights, and the values' product
@@ -514,7 +553,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                 float2 w[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    w[i] = make_float2(fast_exp2(z[tile][i].x - m.x), fast_exp2(z[tile][i].y - m.y));
+                    const float2 x = fadd2(z[tile][i], make_float2(-m.x, -m.y));
+                    w[i] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                     l = fadd2(l, w[i]);
                 }
 #pragma unroll
@@ -532,10 +572,11 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                         const float2 w0 = fmul2(w[0], make_float2(e0, e0)), w1 = fmul2(w[1], make_float2(e1, e1));
                         const uint32_t b0 = turn_matrix(pack2<F16>(w0.x, w0.y)), b1 = turn_matrix(pack2<F16>(w1.x, w1.y));
                         uint32_t lo[4], hi[4];
-                        codes_less_8(lo, v[2 * j]);
-                        codes_less_8(hi, v[2 * j + 1]);
+                        codes_in_place(lo, v[2 * j]);
+                        codes_in_place(hi, v[2 * j + 1]);
                         product(O[r2 + j][0], lo[0], lo[1], hi[0], hi[1], b0, b1);
                         product(O[r2 + j][1], lo[2], lo[3], hi[2], hi[3], b0, b1);
+                        product(sums[r2 + j], kOnes, kOnes, kOnes, kOnes, b0, b1);
                     }
                 }
             }
@@ -547,6 +588,13 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
             l.x += __shfl_xor_sync(0xffffffffu, l.x, o);
             l.y += __shfl_xor_sync(0xffffffffu, l.y, o);
         }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    O[r][u][i] = fmaf(O[r][u][i], i < 2 ? kCode : kCodeHigh, -8.f * sums[r][i & 1]);
         if (p.whole) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -566,7 +614,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                 copies_wait<0>();
                 __syncwarp();
             }
-            float *rec = is_first ? sm.first[warp] : reinterpret_cast<float *>(sm.ring[warp][0]);
+            // (a pair that the CTA's last warp leaves open goes on in the next CTA)
+            float *rec = is_first        ? sm.first[warp]
+                         : warp == W - 1 ? P.records + (size_t)(2 * blockIdx.x + 1) * GG::RECORD
+                                         : reinterpret_cast<float *>(sm.ring[warp][0]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int h = 2 * t + i;
@@ -595,82 +646,88 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
 
     // ---- join the CTA's cut pairs.  Chain -1 starts with warp 0's first record (a pair that
     // began in a CTA before), chain w with warp w's last one; the first records of the warps
-    // behind it follow, up to one that goes to the pair's end.
-    constexpr int DPL = D / 32;
-    for (int item = warp; item < (W + 1) * 8; item += W) {
-        const int chain = item / 8 - 1, h = item & 7;
-        const int pair = chain < 0 ? sm.first_pair[0] : sm.last_pair[chain];
-        if (pair < 0)
-            continue;
-        int n = 1;
-        bool ends = chain < 0 && sm.first_ends[0];
-        while (!ends && chain + n + (chain < 0 ? 1 : 0) < W) {
-            const int w = chain + n + (chain < 0 ? 1 : 0);
-            if (sm.first_pair[w] != pair)
-                break;
-            ends = sm.first_ends[w];
-            ++n;
-        }
+    // behind it follow, up to one that goes to the pair's end.  Warp w joins chain w - 1.
+    const bool has_first = lane < W && sm.first_pair[lane < W ? lane : 0] >= 0;
+    const uint32_t open = __ballot_sync(0xffffffffu, lane < W && sm.last_pair[lane < W ? lane : 0] >= 0),
+                   enders = __ballot_sync(0xffffffffu, has_first && sm.first_ends[lane]);
+    const bool from_before = sm.first_pair[0] >= 0;
+    const int opener = 31 - __clz(open);  // the last warp that leaves a pair open, or -1
+    const bool goes_on = opener >= 0 && (enders >> (opener + 1)) == 0u;
+    const int chain = warp - 1, pair0 = chain < 0 ? sm.first_pair[0] : sm.last_pair[chain];
+    if (pair0 >= 0) {
+        const uint32_t behind = chain < 0 ? enders : enders >> (chain + 1) << (chain + 1);
+        const bool ends = behind != 0u;
+        const int n = (ends ? __ffs(behind) - 1 : W - 1) - chain + (chain < 0 ? 0 : 1);
         auto record = [&](int i) -> const float * {
             return chain < 0 ? sm.first[i] : i == 0 ? reinterpret_cast<const float *>(sm.ring[chain][0]) : sm.first[chain + i];
         };
-        const float mi = lane < n ? record(lane)[h] : kNone, li = lane < n ? record(lane)[8 + h] : 0.f;
-        float top = mi;
+        // weights: lane 8 x + h has head h of the records x, x + 4, ..
+        constexpr int K = (W + 3) / 4, F = D / 16;  // F float4s of a lane
+        float wt[K], top = kNone, sum = 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float wi = fast_exp2(mi - top);
-        float sum = wi * li, acc[DPL];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-        for (int d = 0; d < DPL; ++d)
-            acc[d] = 0.f;
-        for (int i = 0; i < n; ++i) {
-            const float f = __shfl_sync(0xffffffffu, wi, i);
-            const float *src = record(i) + 16 + h * D + lane * DPL;
-#pragma unroll
-            for (int d = 0; d < DPL; ++d)
-                acc[d] = fmaf(f, src[d], acc[d]);
+        for (int k = 0; k < K; ++k) {
+            wt[k] = 4 * k + (lane >> 3) < n ? record(4 * k + (lane >> 3))[lane & 7] : kNone;
+            top = fmaxf(top, wt[k]);
         }
-        const int s = pair / P.heads, ph = pair - s * P.heads, kv = ph / P.subs, sub = ph - kv * P.subs;
-        if (chain >= 0 && ends) {
-            const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
-            if (h < P.group - sub * 8) {
-                uint8_t *dst = static_cast<uint8_t *>(a.out) +
-                               (((long long)s * a.num_q_heads + kv * P.group + sub * 8 + h) * D + lane * DPL) * 2;
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
 #pragma unroll
-                for (int d = 0; d < DPL; d += 2)
-                    *reinterpret_cast<uint32_t *>(dst + 2 * d) = pack2<T>(acc[d] * inv, acc[d + 1] * inv);
+        for (int k = 0; k < K; ++k) {
+            wt[k] = fast_exp2(wt[k] - top);
+            if (4 * k + (lane >> 3) < n)
+                sum = fmaf(wt[k], record(4 * k + (lane >> 3))[8 + (lane & 7)], sum);
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        float4 acc[F];
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if (4 * k + x >= n)
+                    break;
+                const float4 *src = reinterpret_cast<const float4 *>(record(4 * k + x) + 16) + lane;
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    const float c = __shfl_sync(0xffffffffu, wt[k], 8 * x + (32 * f + lane) / (D / 4));
+                    const float4 y = src[32 * f];
+                    acc[f].x = fmaf(c, y.x, acc[f].x), acc[f].y = fmaf(c, y.y, acc[f].y);
+                    acc[f].z = fmaf(c, y.z, acc[f].z), acc[f].w = fmaf(c, y.w, acc[f].w);
+                }
+            }
+        if (chain >= 0 && ends) {
+            const int s = pair0 / P.heads, ph = pair0 - s * P.heads, kv = ph / P.subs, sub = ph - kv * P.subs;
+            const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const int h = (32 * f + lane) / (D / 4);
+                const float c = __shfl_sync(0xffffffffu, inv, h);
+                if (h < P.group - sub * 8)
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) +
+                                               (((long long)s * a.num_q_heads + kv * P.group + sub * 8 + h) * D + lane % (D / 4) * 4) * 2) =
+                        make_uint2(pack2<T>(acc[f].x * c, acc[f].y * c), pack2<T>(acc[f].z * c, acc[f].w * c));
             }
         } else {
             float *rec = P.records + (size_t)(2 * blockIdx.x + (chain < 0 ? 0 : 1)) * GG::RECORD;
-            if (lane == 0) {
-                rec[h] = top;
-                rec[8 + h] = sum;
+            if (lane < 8) {
+                rec[lane] = top;
+                rec[8 + lane] = sum;
             }
 #pragma unroll
-            for (int d = 0; d < DPL; ++d)
-                rec[16 + h * D + lane * DPL + d] = acc[d];
-            __threadfence();
+            for (int f = 0; f < F; ++f)
+                reinterpret_cast<float4 *>(rec + 16)[32 * f + lane] = acc[f];
         }
     }
-    __syncthreads();
+    if (!from_before && !goes_on)
+        return;
 
     // ---- pairs that other CTAs have parts of: the last to arrive joins them
+    int count = 0;  // CTAs of the pair besides this one
     if (tid < 2) {
-        int pair = -1;
-        if (tid == 0) {
-            pair = sm.first_pair[0];
-        } else {
-            // the chain that runs over the CTA's end
-            int w = W - 1;
-            while (w >= 0 && sm.last_pair[w] < 0 && sm.first_pair[w] >= 0 && !sm.first_ends[w])
-                --w;
-            if (w >= 0)
-                pair = sm.last_pair[w];
-        }
+        const int pair = tid == 0 ? sm.first_pair[0] : goes_on ? sm.last_pair[opener] : -1;
         sm.arrived_last[tid] = -1;
         if (pair >= 0) {
             const int s = pair / P.heads, ph = pair - s * P.heads;
@@ -683,17 +740,20 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                 const int w = x < rest * (share + 1) ? x / (share + 1) : rest + (x - rest * (share + 1)) / share;
                 return w / W;
             };
-            const int c0 = cta_of(begin), c1 = cta_of(end);
+            const int c0 = cta_of(begin);
+            count = cta_of(end) - c0;
             sm.first_cta[tid] = c0;
-            sm.pieces[tid] = c1 - c0 + 1;
-            if (c1 > c0) {
-                __threadfence();
-                if (atomicAdd(P.counters + pair, 1) == c1 - c0) {
-                    P.counters[pair] = 0;
-                    sm.arrived_last[tid] = pair;
-                    __threadfence();
-                }
-            }
+            sm.pieces[tid] = count + 1;
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    if (count > 0) {
+        const int pair = tid == 0 ? sm.first_pair[0] : sm.last_pair[opener];
+        if (atomicAdd(P.counters + pair, 1) == count) {
+            P.counters[pair] = 0;
+            sm.arrived_last[tid] = pair;
+            __threadfence();
         }
     }
     __syncthreads();
@@ -703,68 +763,71 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
         if (pair < 0)
             continue;
         const int n = sm.pieces[slot], c0 = sm.first_cta[slot];
-        // record i: the first CTA's last slot, then the others' first ones
-        auto record = [&](int i) -> const float * { return P.records + (size_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * GG::RECORD; };
-        if (warp < 8) {
-            float mi[(kMaxQ4Ctas + 31) / 32], li[(kMaxQ4Ctas + 31) / 32], top = kNone, sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < (kMaxQ4Ctas + 31) / 32; ++k) {
-                const int i = k * 32 + lane;
-                mi[k] = i < n ? __ldcg(record(i) + warp) : kNone;
-                li[k] = i < n ? __ldcg(record(i) + 8 + warp) : 0.f;
-                top = fmaxf(top, mi[k]);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll
-            for (int k = 0; k < (kMaxQ4Ctas + 31) / 32; ++k) {
-                const float f = fast_exp2(mi[k] - top);
-                sum = fmaf(f, li[k], sum);
-                if (k * 32 + lane < n)
-                    sm.weight[k * 32 + lane][warp] = f;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0)
-                sm.inv[warp] = sum == 0.f ? 0.f : __fdividef(1.f, sum);
-        }
-        __syncthreads();
-        // a thread adds up four elements over every LANESth record
+        // A thread merges four elements over every LANESth record as they come, four at a
+        // time.  Record i: the first CTA's last slot, then the others' first ones.
         constexpr int LANES = GG::THREADS / GG::SLOTS;
-        float4 *part = reinterpret_cast<float4 *>(sm.ring[0][0]);
         const int at = tid % GG::SLOTS, first = tid / GG::SLOTS, h = at / (D / 4);
+        float top = kNone, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (first < LANES) {
+        if (first < LANES)
             for (int i = first; i < n; i += 4 * LANES) {
                 float4 x[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    x[k] = i + k * LANES < n ? __ldcg(reinterpret_cast<const float4 *>(record(i + k * LANES) + 16) + at)
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                float mi[4], li[4], higher = top;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if (i + k * LANES >= n)
-                        break;
-                    const float f = sm.weight[i + k * LANES][h];
+                    const int r = i + k * LANES;
+                    const float *rec = P.records + (size_t)(r == 0 ? 2 * c0 + 1 : 2 * (c0 + r)) * GG::RECORD;
+                    const bool on = r < n;
+                    mi[k] = on ? __ldcg(rec + h) : kNone;
+                    li[k] = on ? __ldcg(rec + 8 + h) : 0.f;
+                    x[k] = on ? __ldcg(reinterpret_cast<const float4 *>(rec + 16) + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    higher = fmaxf(higher, mi[k]);
+                const float f0 = fast_exp2(top - higher);
+                top = higher;
+                sum *= f0;
+                acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float f = fast_exp2(mi[k] - top);
+                    sum = fmaf(f, li[k], sum);
                     acc.x = fmaf(f, x[k].x, acc.x), acc.y = fmaf(f, x[k].y, acc.y);
                     acc.z = fmaf(f, x[k].z, acc.z), acc.w = fmaf(f, x[k].w, acc.w);
                 }
             }
-            if (first > 0)
+        if constexpr (LANES > 1) {
+            float4 *part = reinterpret_cast<float4 *>(sm.ring[0][0]);
+            float2 *part_top = reinterpret_cast<float2 *>(part + (LANES - 1) * GG::SLOTS);
+            if (first > 0) {
                 part[(first - 1) * GG::SLOTS + at] = acc;
-        }
-        __syncthreads();
-        if (first == 0) {
-#pragma unroll
-            for (int k = 1; k < LANES; ++k) {
-                const float4 x = part[(k - 1) * GG::SLOTS + at];
-                acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+                part_top[(first - 1) * GG::SLOTS + at] = make_float2(top, sum);
             }
+            __syncthreads();
+            if (first == 0) {
+                float higher = top;
+#pragma unroll
+                for (int k = 0; k < LANES - 1; ++k)
+                    higher = fmaxf(higher, part_top[k * GG::SLOTS + at].x);
+                const float f0 = fast_exp2(top - higher);
+                sum *= f0;
+                acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+#pragma unroll
+                for (int k = 0; k < LANES - 1; ++k) {
+                    const float2 y = part_top[k * GG::SLOTS + at];
+                    const float4 x = part[k * GG::SLOTS + at];
+                    const float f = fast_exp2(y.x - higher);
+                    sum = fmaf(f, y.y, sum);
+                    acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y);
+                    acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+                }
+            }
+        }
+        if (first == 0) {
             const int s = pair / P.heads, ph = pair - s * P.heads, kv = ph / P.subs, sub = ph - kv * P.subs;
             if (h < P.group - sub * 8) {
-                const float inv = sm.inv[h];
+                const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) +
                                            (((long long)s * a.num_q_heads + kv * P.group + sub * 8 + h) * D + (at % (D / 4)) * 4) * 2) =
                     make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
