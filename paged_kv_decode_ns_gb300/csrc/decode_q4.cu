@@ -3,12 +3,12 @@
 // out = sum_p 2^(z_p - m) v_p / sum_p 2^(z_p - m), z in log2 units, in one pass over the
 // keys with a running reference m.  K_p = dk_p (c - 8) and V_p = dv_p (c - 8) by group of 32
 // elements, so that with integer codes c
-//   z_p = scale sum_g dk_pg (q_g . c_pg - 8 sum q_g),
-//   out_g = sum_p w_p' c_pg - 8 sum_p w_p',   w_p' = w_p dv_pg:
+//   z_p = scale sum_g dk_pg (q_g . c_pg - 8 sum q_g),   out_g = sum_p (w_p dv_pg) (c_pg - 8):
 // the steps are applied to the scores and to the weights, 8 heads wide, instead of to 64 or 128
-// elements, and the 8 once for a row of q, and once for the sum of a group's w'.  A code is
-// used as it lies: four bits at the bottom of an fp16 word are the (subnormal) number c 2^-24, or
-// c 2^-20 one place higher, so one AND makes two operands.  Both sums are small matrix
+// elements, and the 8 of K once for a row of q.  A code is used as it lies: four bits at the
+// bottom of an fp16 word are the (subnormal) number c 2^-24, or c 2^-20 one place higher, so one
+// AND makes two operands.  (A sum of w_p dv_pg for V's 8 would cancel against a much larger
+// one, and a product for it took as long as the subtraction.)  Both sums are small matrix
 // products (mma.m16n8k16: 16 tokens or elements by the 8 query heads of a group, fp32 sums).  A tcgen05
 // product has 128 rows at least and its operands in shared memory, where each code would
 // be four times as large as in the cache; here they go from the codes to the product in registers.
@@ -23,6 +23,7 @@
 // CTAs through records in the workspace, by the CTA that arrives last; in the order of the
 // keys, so results do not depend on timing.
 #include <algorithm>
+#include <cmath>
 
 #include "ns_internal.h"
 #include "q4_decode.h"
@@ -34,7 +35,7 @@ namespace {
 
 constexpr int kChunk = 32;     // tokens of a step: one a lane
 constexpr int kPairCost = 1;   // chunks that a pair counts besides its own
-constexpr int kMinShare = 2;   // chunks a warp is given at least
+constexpr int kWarpJoin = 8;   // CTAs' records that a warp joins by itself
 constexpr float kNone = -3.402823466e38f;
 // m is set so that the largest w dv is just below 2^kLift, and moves when one would pass
 // that by 2^kSlack: fp16 has room up to 2^16 and steps of 2^-24.
@@ -44,7 +45,7 @@ template <int D>
 struct Geo {
     static constexpr int R = D / 32;                       // groups of 32 elements
     static constexpr int WARPS = D == 64 ? 16 : 12;
-    static constexpr int STAGES = D == 64 ? 4 : 3;         // chunks of a warp, one of them in use
+    static constexpr int STAGES = 3;                       // chunks of a warp, one of them in use
     static constexpr int CODES = kChunk * D / 2;           // bytes of a chunk's K or V
     static constexpr int SCALES = kChunk * R * 2;
     static constexpr int STAGE = 2 * (CODES + SCALES);
@@ -64,7 +65,9 @@ struct alignas(16) Smem {
     // what a warp left: the pair of its first and last record (-1: none) and whether the first
     // one goes to its pair's end
     int first_pair[GG::WARPS], first_ends[GG::WARPS], last_pair[GG::WARPS];
-    int arrived_last[2], pieces[2], first_cta[2];
+    // the pair that came from a CTA before and the one that goes on in the next: the CTAs that
+    // have parts of it, and the pair again when it is left to the whole CTA to join
+    int first_cta[2], pieces[2], to_join[2];
     static_assert(GG::STAGES * GG::STAGE >= GG::RECORD * 4, "a record fits a warp's ring");
 };
 
@@ -74,9 +77,11 @@ struct Params {
     int subs;       // of a kv head
     int group;      // query heads of a kv head
     int shift;      // log2 of the block size
-    float scale_log2;
+    float scale_log2, sign;  // of the scale
     int *counters;
     float *records;
+
+    __device__ __forceinline__ float *record(int i, int floats) const { return records + (size_t)i * floats; }
 };
 
 // ---------------------------------------------------------------------------
@@ -91,19 +96,25 @@ __device__ __forceinline__ void copies_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Four 8 x 8 matrices of 16-bit elements.  Without a memory clobber, so that the compiler is free
+// to place them among the arithmetic; their addresses come from read_behind, so not above it.
 __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr)
 {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+    asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(addr));
 }
 __device__ __forceinline__ void load_matrices_turned(uint32_t (&r)[4], uint32_t addr)
 {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+    asm("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(addr));
+}
+// What is read through this address is read behind this point.
+__device__ __forceinline__ uint32_t read_behind(uint32_t addr)
+{
+    asm volatile("" : "+r"(addr)::"memory");
+    return addr;
 }
 __device__ __forceinline__ uint32_t turn_matrix(uint32_t x)
 {
@@ -129,8 +140,16 @@ __device__ __forceinline__ void codes_in_place(uint32_t (&p)[4], uint32_t w)
     p[2] = v & 0x000f000fu;
     p[3] = v & 0x00f000f0u;
 }
+// Those of codes less 8 (subnormal too, or 0).
+__device__ __forceinline__ void less_8(uint32_t (&p)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __hadd2(*reinterpret_cast<__half2 *>(&p[i]), __half2half2(__ushort_as_half(i & 1 ? 0x8080 : 0x8008)));
+        p[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
 constexpr float kCode = 16777216.f, kCodeHigh = 1048576.f;  // 2^24, 2^20
-constexpr uint32_t kOnes = 0x3c003c00u;                       // two fp16 ones
 
 __device__ __forceinline__ uint32_t larger_f16(uint32_t a, uint32_t b)  // magnitudes, signs of no meaning
 {
@@ -153,6 +172,17 @@ __device__ __forceinline__ float2 halves(uint32_t w) { return unpack2<F16>(w); }
 // ---------------------------------------------------------------------------
 // Walk over the pieces of a warp's run.
 // ---------------------------------------------------------------------------
+// a / b, a >= 0, b > 0; by fp32 (2^-22 of the quotient) where that is off by one at most.
+__device__ __forceinline__ int quotient(int a, int b)
+{
+    if (a >= 1 << 22)
+        return a / b;
+    int q = (int)__fdividef((float)a, (float)b);
+    const int r = a - q * b;
+    q += r < 0 ? -1 : r >= b ? 1 : 0;
+    return q;
+}
+
 struct Piece {
     int s, h;       // sequence, pair of it
     int L;          // keys of the sequence
@@ -197,6 +227,107 @@ __device__ __forceinline__ Piece next_piece(const Params &P, Walk &w)
 }
 
 // ---------------------------------------------------------------------------
+// Records of a pair's parts, joined by a warp: lane i has float4s i, i + 32, .. of O, and the
+// reference and the sum of head i % 8.
+template <int D>
+struct Joined {
+    static constexpr int F = D / 16;
+    float4 acc[F];
+    float top, sum;
+
+    // n <= MOST records in the order of the keys; GLOBAL: they were written by other CTAs
+    template <int MOST, bool GLOBAL, typename Record>
+    __device__ __forceinline__ void join(int n, int lane, const Record &record)
+    {
+        constexpr int K = (MOST + 3) / 4, B = GLOBAL ? 16 / F : 4;  // records whose loads fly together
+        const int x = lane >> 3, h = lane & 7;
+        float m[K], l[K];
+        top = kNone;
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const bool on = 4 * k + x < n;
+            const float *r = record(on ? 4 * k + x : 0);
+            m[k] = on ? (GLOBAL ? __ldcg(r + h) : r[h]) : kNone;
+            l[k] = on ? (GLOBAL ? __ldcg(r + 8 + h) : r[8 + h]) : 0.f;
+        }
+        float4 y[B][F];
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const float4 *r = reinterpret_cast<const float4 *>(record(min(i0 + b, n - 1)) + 16) + lane;
+#pragma unroll
+                for (int f = 0; f < F; ++f)
+                    y[b][f] = GLOBAL ? __ldcg(r + 32 * f) : r[32 * f];
+            }
+        };
+        load(0);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            top = fmaxf(top, m[k]);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            m[k] = 4 * k + x < n ? fast_exp2(m[k] - top) : 0.f;
+            sum = fmaf(m[k], l[k], sum);
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i0 = 0; i0 < MOST; i0 += B) {
+            if (i0 > 0) {
+                if (i0 >= n)
+                    break;
+                load(i0);
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int i = i0 + b;
+                if (i >= MOST || i >= n)
+                    break;
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    const float c = __shfl_sync(0xffffffffu, m[i / 4], 8 * (i % 4) + (32 * f + lane) / (D / 4));
+                    acc[f].x = fmaf(c, y[b][f].x, acc[f].x), acc[f].y = fmaf(c, y[b][f].y, acc[f].y);
+                    acc[f].z = fmaf(c, y[b][f].z, acc[f].z), acc[f].w = fmaf(c, y[b][f].w, acc[f].w);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void keep(float *rec, int lane) const
+    {
+        if (lane < 8) {
+            rec[lane] = top;
+            rec[8 + lane] = sum;
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            reinterpret_cast<float4 *>(rec + 16)[32 * f + lane] = acc[f];
+    }
+
+    template <typename T>
+    __device__ __forceinline__ void put(const Params &P, int pair, int lane) const
+    {
+        const int s = pair / P.heads, ph = pair - s * P.heads, kv = ph / P.subs, sub = ph - kv * P.subs;
+        const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int h = (32 * f + lane) / (D / 4);
+            const float c = __shfl_sync(0xffffffffu, inv, h);
+            if (h < P.group - sub * 8)
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(P.a.out) +
+                                           (((long long)s * P.a.num_q_heads + kv * P.group + sub * 8 + h) * D + lane % (D / 4) * 4) * 2) =
+                    make_uint2(pack2<T>(acc[f].x * c, acc[f].y * c), pack2<T>(acc[f].z * c, acc[f].w * c));
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
 template <typename T, int D>
 __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __grid_constant__ Params P)
 {
@@ -214,12 +345,16 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
         sm.first_pair[tid] = -1;
         sm.last_pair[tid] = -1;
     }
+    if (tid < 2)
+        sm.to_join[tid] = -1;
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // ---- the line: each thread measures a share of the sequences
-    const int per = (a.num_seqs + GG::THREADS - 1) / GG::THREADS;
-    const int s0 = min(a.num_seqs, tid * per), s1 = min(a.num_seqs, s0 + per);
+    // ---- the line: each lane of a warp, or with more of them each thread of the CTA, measures a
+    // share of the sequences
+    const bool few = a.num_seqs <= 32;
+    const int per = few ? 1 : (a.num_seqs + GG::THREADS - 1) / GG::THREADS, who = few ? lane : tid;
+    const int s0 = min(a.num_seqs, who * per), s1 = min(a.num_seqs, s0 + per);
     int mine = 0;
     for (int s = s0; s < s1; ++s) {
         const int L = a.context_lens[s];
@@ -234,41 +369,56 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
         if (lane >= o)
             incl += y;
     }
-    if (lane == 31)
-        sm.scan[warp] = incl;
-    __syncthreads();
-    int total = 0, ahead = 0;
+    int total = __shfl_sync(0xffffffffu, incl, 31), ahead = 0;
+    if (!few) {
+        if (lane == 31)
+            sm.scan[warp] = incl;
+        __syncthreads();
+        total = 0;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const int x = sm.scan[i];
-        ahead += i < warp ? x : 0;
-        total += x;
+        for (int i = 0; i < W; ++i) {
+            const int x = sm.scan[i];
+            ahead += i < warp ? x : 0;
+            total += x;
+        }
+        sm.before[tid] = ahead + incl - mine;
+        __syncthreads();
     }
-    sm.before[tid] = ahead + incl - mine;
     total *= P.heads;
-    __syncthreads();
-    // runs: the first `rest` of `runs` warps take share + 1 chunks, the others share
-    const int runs = min((int)gridDim.x * W, (total + kMinShare - 1) / kMinShare);
-    const int share = total / runs, rest = total - share * runs;
+    // Runs: the first `rest` of `runs` warps take share + 1 chunks, the others share.  What one CTA
+    // can do with two chunks a warp stays in one (four short sequences 6.4 us, 7.6 by single chunks
+    // in two CTAs; 8 x 4096 tokens the other way round 10.0 and 9.2).
+    const int runs = min((int)gridDim.x * W, total <= 2 * W ? (total + 1) / 2 : total);
+    const int share = quotient(total, runs), rest = total - share * runs;
     const int me = blockIdx.x * W + warp;
     if ((int)blockIdx.x * W >= runs)
         return;
+    auto cta_of = [&](int x) {  // of the warp whose run has position x
+        const int y = x - rest * (share + 1);
+        return (y < 0 ? quotient(x, share + 1) : rest + quotient(y, share)) / W;
+    };
     Walk next;
     next.s = next.h = next.off = 0;
     next.left = me < runs ? share + (me < rest ? 1 : 0) : 0;
     const int x0 = me * share + min(me, rest);
     if (me < runs) {
-        // the last thread whose sequences start at x0 or before: every `step`th, then each
-        auto starts = [&](int i) { return i < GG::THREADS && (long long)i * per < a.num_seqs && sm.before[i] * P.heads <= x0; };
-        constexpr int step = GG::THREADS / 32;
-        int lo = (__popc(__ballot_sync(0xffffffffu, starts(lane * step))) - 1) * step;
-        lo += __popc(__ballot_sync(0xffffffffu, lane < step && starts(lo + lane))) - 1;
-        int s = lo * per, y = x0 - sm.before[lo] * P.heads;
-        for (;; ++s) {
+        // the last lane or thread whose sequences start at x0 or before
+        int lo, y;
+        if (few) {
+            lo = __popc(__ballot_sync(0xffffffffu, lane < a.num_seqs && (incl - mine) * P.heads <= x0)) - 1;
+            y = x0 - __shfl_sync(0xffffffffu, incl - mine, lo) * P.heads;
+        } else {  // of every `step`th, then of each
+            auto starts = [&](int i) { return i < GG::THREADS && (long long)i * per < a.num_seqs && sm.before[i] * P.heads <= x0; };
+            constexpr int step = GG::THREADS / 32;
+            lo = (__popc(__ballot_sync(0xffffffffu, starts(lane * step))) - 1) * step;
+            lo += __popc(__ballot_sync(0xffffffffu, lane < step && starts(lo + lane))) - 1;
+            y = x0 - sm.before[lo] * P.heads;
+        }
+        for (int s = lo * per;; ++s) {
             const int len = length_of(keys_of(a, P.shift, s));
             if (y < len * P.heads || s + 1 >= a.num_seqs) {
                 next.s = s;
-                next.h = y / len;
+                next.h = quotient(y, len);
                 next.off = y - next.h * len;
                 break;
             }
@@ -359,8 +509,13 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
     // ---- arithmetic
     int used = 0;  // chunks, modulo ST
     while (next.left > 0) {
-        const int off0 = next.off;
+        const int off0 = next.off, x = x0 + (share + (me < rest ? 1 : 0)) - next.left;  // the piece's position
         const Piece p = next_piece(P, next);
+        if (lane == 0 && (warp == 0 ? off0 > 0 : warp == W - 1 && !p.ends)) {
+            const int slot = warp == 0 ? 0 : 1, begin = x - off0, c0 = cta_of(begin);
+            sm.first_cta[slot] = c0;
+            sm.pieces[slot] = cta_of(begin + length_of(p.L) - 1) - c0 + 1;
+        }
         const int kv = P.subs == 1 ? p.h : p.h / P.subs, sub = p.h - kv * P.subs;
         const int head0 = kv * P.group + sub * 8, heads = min(8, P.group - sub * 8);
         // q of head g, elements 8 t .. 8 t + 7 of each group, as the products' second operand
@@ -396,8 +551,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 y = unpack2<T>(x[i]);
-                    v[2 * i] = y.x * f;
-                    v[2 * i + 1] = y.y * f;
+                    v[2 * i] = y.x * (f * P.sign);
+                    v[2 * i + 1] = y.y * (f * P.sign);
                 }
                 // elements i and i + 4, less four binary places where the code is that much higher
                 float sum = 0.f;
@@ -429,13 +584,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     O[r][u][i] = 0.f;
-        float sums[R][4];  // of a group's weights times steps, of either head (twice over)
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sums[r][i] = 0.f;
+        // the references and the limits of the scores, these in units of the products
         float2 l = make_float2(0.f, 0.f), m = make_float2(kNone, kNone), limit = m;
+        const float2 per_unit = make_float2(__fdividef(1.f, unit.x), __fdividef(1.f, unit.y));
         int top_e = -1;            // exponent field of the largest V step so far
         uint32_t step_limit = 0u;  // and the largest fp16 of that exponent
 
@@ -443,13 +594,13 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
             copies_wait<ST - 2>();
             __syncwarp();
             issue();  // into the stage that the last turn has read
-            const uint32_t from = ring + used * GG::STAGE;
+            const uint32_t from = read_behind(ring + used * GG::STAGE);
             const uint8_t *stage = sm.ring[warp][used];
             const uint32_t live = sm.live[warp][used];
             used = used + 1 == ST ? 0 : used + 1;
 
             // ---- scores: 16 tokens at a time, by group
-            float2 z[2][2];  // [tile][token g or g + 8] of the two heads
+            float2 z[2][2];  // [tile][token g or g + 8] of the two heads, in units of the products
             uint32_t dv[2][2][R / 2];
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
@@ -490,8 +641,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                         z[tile][1] = r == 0 ? fmul2(y1, make_float2(e1, e1)) : ffma2(y1, make_float2(e1, e1), z[tile][1]);
                     }
                 }
-                z[tile][0] = fmul2(z[tile][0], unit);
-                z[tile][1] = fmul2(z[tile][1], unit);
             }
             if (live != 0xffffffffu)  // a token that is not there has neither a weight nor a step
 #pragma unroll
@@ -525,11 +674,11 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                 top_e = e;
                 step_limit = ((uint32_t)(e + 1) << 10) - 1u;
                 // a head's reference follows its own scores alone, whatever the heads beside it hold
-                const float2 to = make_float2(top.x > limit.x ? fmaxf(m.x + rise, top.x + size - kLift) : m.x + rise,
-                                              top.y > limit.y ? fmaxf(m.y + rise, top.y + size - kLift) : m.y + rise);
+                const float2 to = make_float2(top.x > limit.x ? fmaxf(m.x + rise, fmaf(top.x, unit.x, size - kLift)) : m.x + rise,
+                                              top.y > limit.y ? fmaxf(m.y + rise, fmaf(top.y, unit.y, size - kLift)) : m.y + rise);
                 const float2 f = make_float2(fast_exp2(m.x - to.x), fast_exp2(m.y - to.y));
                 m = to;
-                limit = make_float2(m.x - size + kLift + kSlack, m.y - size + kLift + kSlack);
+                limit = fmul2(make_float2(m.x - size + kLift + kSlack, m.y - size + kLift + kSlack), per_unit);
                 l = fmul2(l, f);
 #pragma unroll
                 for (int r = 0; r < R; ++r)
@@ -540,11 +689,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                         O[r][u][2] *= f.x;
                         O[r][u][3] *= f.y;
                     }
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    sums[r][0] *= f.x;
-                    sums[r][1] *= f.y;
-                }
             }
 
             // ---- weights, and the values' product
@@ -553,7 +697,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                 float2 w[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float2 x = fadd2(z[tile][i], make_float2(-m.x, -m.y));
+                    const float2 x = ffma2(z[tile][i], unit, make_float2(-m.x, -m.y));
                     w[i] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                     l = fadd2(l, w[i]);
                 }
@@ -574,9 +718,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                         uint32_t lo[4], hi[4];
                         codes_in_place(lo, v[2 * j]);
                         codes_in_place(hi, v[2 * j + 1]);
+                        less_8(lo);
+                        less_8(hi);
                         product(O[r2 + j][0], lo[0], lo[1], hi[0], hi[1], b0, b1);
                         product(O[r2 + j][1], lo[2], lo[3], hi[2], hi[3], b0, b1);
-                        product(sums[r2 + j], kOnes, kOnes, kOnes, kOnes, b0, b1);
                     }
                 }
             }
@@ -594,7 +739,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    O[r][u][i] = fmaf(O[r][u][i], i < 2 ? kCode : kCodeHigh, -8.f * sums[r][i & 1]);
+                    O[r][u][i] *= i < 2 ? kCode : kCodeHigh;
         if (p.whole) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -616,7 +761,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
             }
             // (a pair that the CTA's last warp leaves open goes on in the next CTA)
             float *rec = is_first        ? sm.first[warp]
-                         : warp == W - 1 ? P.records + (size_t)(2 * blockIdx.x + 1) * GG::RECORD
+                         : warp == W - 1 ? P.record(2 * blockIdx.x + 1, GG::RECORD)
                                          : reinterpret_cast<float *>(sm.ring[warp][0]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -653,113 +798,65 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
     const bool from_before = sm.first_pair[0] >= 0;
     const int opener = 31 - __clz(open);  // the last warp that leaves a pair open, or -1
     const bool goes_on = opener >= 0 && (enders >> (opener + 1)) == 0u;
-    const int chain = warp - 1, pair0 = chain < 0 ? sm.first_pair[0] : sm.last_pair[chain];
-    if (pair0 >= 0) {
+    const uint32_t chains = open << 1 | (from_before ? 1u : 0u);  // bit w + 1: chain w
+    const int chain = warp - 1;
+    // the pair's CTAs have each counted themselves when the last of them does
+    auto arrive_last = [&](int slot, int pair) {
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) {
+            last = atomicAdd(P.counters + pair, 1) == sm.pieces[slot] - 1;
+            if (last)
+                P.counters[pair] = 0;
+            __threadfence();
+        }
+        last = __shfl_sync(0xffffffffu, last, 0);
+        __syncwarp();
+        return last != 0;
+    };
+    auto finish = [&](int slot, int pair) {  // this CTA's record of the pair is written
+        if (!arrive_last(slot, pair))
+            return;
+        const int n = sm.pieces[slot], c0 = sm.first_cta[slot];
+        if (n > kWarpJoin) {
+            if (lane == 0)
+                sm.to_join[slot] = pair;
+            return;
+        }
+        Joined<D> r;
+        r.template join<kWarpJoin, true>(n, lane, [&](int i) { return P.record(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i), GG::RECORD); });
+        r.template put<T>(P, pair, lane);
+    };
+    if ((chains >> warp) & 1u) {
+        const int pair = chain < 0 ? sm.first_pair[0] : sm.last_pair[chain];
         const uint32_t behind = chain < 0 ? enders : enders >> (chain + 1) << (chain + 1);
         const bool ends = behind != 0u;
         const int n = (ends ? __ffs(behind) - 1 : W - 1) - chain + (chain < 0 ? 0 : 1);
-        auto record = [&](int i) -> const float * {
+        Joined<D> r;
+        r.template join<W, false>(n, lane, [&](int i) -> const float * {
             return chain < 0 ? sm.first[i] : i == 0 ? reinterpret_cast<const float *>(sm.ring[chain][0]) : sm.first[chain + i];
-        };
-        // weights: lane 8 x + h has head h of the records x, x + 4, ..
-        constexpr int K = (W + 3) / 4, F = D / 16;  // F float4s of a lane
-        float wt[K], top = kNone, sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            wt[k] = 4 * k + (lane >> 3) < n ? record(4 * k + (lane >> 3))[lane & 7] : kNone;
-            top = fmaxf(top, wt[k]);
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            wt[k] = fast_exp2(wt[k] - top);
-            if (4 * k + (lane >> 3) < n)
-                sum = fmaf(wt[k], record(4 * k + (lane >> 3))[8 + (lane & 7)], sum);
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        float4 acc[F];
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-            acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                if (4 * k + x >= n)
-                    break;
-                const float4 *src = reinterpret_cast<const float4 *>(record(4 * k + x) + 16) + lane;
-#pragma unroll
-                for (int f = 0; f < F; ++f) {
-                    const float c = __shfl_sync(0xffffffffu, wt[k], 8 * x + (32 * f + lane) / (D / 4));
-                    const float4 y = src[32 * f];
-                    acc[f].x = fmaf(c, y.x, acc[f].x), acc[f].y = fmaf(c, y.y, acc[f].y);
-                    acc[f].z = fmaf(c, y.z, acc[f].z), acc[f].w = fmaf(c, y.w, acc[f].w);
-                }
-            }
+        });
         if (chain >= 0 && ends) {
-            const int s = pair0 / P.heads, ph = pair0 - s * P.heads, kv = ph / P.subs, sub = ph - kv * P.subs;
-            const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
-#pragma unroll
-            for (int f = 0; f < F; ++f) {
-                const int h = (32 * f + lane) / (D / 4);
-                const float c = __shfl_sync(0xffffffffu, inv, h);
-                if (h < P.group - sub * 8)
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) +
-                                               (((long long)s * a.num_q_heads + kv * P.group + sub * 8 + h) * D + lane % (D / 4) * 4) * 2) =
-                        make_uint2(pack2<T>(acc[f].x * c, acc[f].y * c), pack2<T>(acc[f].z * c, acc[f].w * c));
-            }
+            r.template put<T>(P, pair, lane);
         } else {
-            float *rec = P.records + (size_t)(2 * blockIdx.x + (chain < 0 ? 0 : 1)) * GG::RECORD;
-            if (lane < 8) {
-                rec[lane] = top;
-                rec[8 + lane] = sum;
-            }
-#pragma unroll
-            for (int f = 0; f < F; ++f)
-                reinterpret_cast<float4 *>(rec + 16)[32 * f + lane] = acc[f];
+            const int slot = chain < 0 ? 0 : 1;
+            r.keep(P.record(2 * blockIdx.x + slot, GG::RECORD), lane);
+            finish(slot, pair);
         }
     }
-    if (!from_before && !goes_on)
+    // the record that the last warp wrote itself is finished by a warp without a chain, if there is one
+    const uint32_t idle = ~chains & ((1u << W) - 1u);
+    if (opener == W - 1 && warp == (idle != 0u ? __ffs(idle) - 1 : W - 1))
+        finish(1, sm.last_pair[W - 1]);
+    if (!(from_before && sm.pieces[0] > kWarpJoin) && !(goes_on && sm.pieces[1] > kWarpJoin))
         return;
 
-    // ---- pairs that other CTAs have parts of: the last to arrive joins them
-    int count = 0;  // CTAs of the pair besides this one
-    if (tid < 2) {
-        const int pair = tid == 0 ? sm.first_pair[0] : goes_on ? sm.last_pair[opener] : -1;
-        sm.arrived_last[tid] = -1;
-        if (pair >= 0) {
-            const int s = pair / P.heads, ph = pair - s * P.heads;
-            const int len = length_of(keys_of(a, P.shift, s)), i = s / per;
-            int y = sm.before[i];
-            for (int k = i * per; k < s; ++k)
-                y += length_of(keys_of(a, P.shift, k));
-            const int begin = y * P.heads + ph * len, end = begin + len - 1;
-            auto cta_of = [&](int x) {
-                const int w = x < rest * (share + 1) ? x / (share + 1) : rest + (x - rest * (share + 1)) / share;
-                return w / W;
-            };
-            const int c0 = cta_of(begin);
-            count = cta_of(end) - c0;
-            sm.first_cta[tid] = c0;
-            sm.pieces[tid] = count + 1;
-        }
-    }
-    __threadfence();
-    __syncthreads();
-    if (count > 0) {
-        const int pair = tid == 0 ? sm.first_pair[0] : sm.last_pair[opener];
-        if (atomicAdd(P.counters + pair, 1) == count) {
-            P.counters[pair] = 0;
-            sm.arrived_last[tid] = pair;
-            __threadfence();
-        }
-    }
+    // ---- pairs of more CTAs: the whole CTA joins them
     __syncthreads();
 #pragma unroll 1
     for (int slot = 0; slot < 2; ++slot) {
-        const int pair = sm.arrived_last[slot];
+        const int pair = sm.to_join[slot];
         if (pair < 0)
             continue;
         const int n = sm.pieces[slot], c0 = sm.first_cta[slot];
@@ -776,7 +873,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int r = i + k * LANES;
-                    const float *rec = P.records + (size_t)(r == 0 ? 2 * c0 + 1 : 2 * (c0 + r)) * GG::RECORD;
+                    const float *rec = P.record(r == 0 ? 2 * c0 + 1 : 2 * (c0 + r), GG::RECORD);
                     const bool on = r < n;
                     mi[k] = on ? __ldcg(rec + h) : kNone;
                     li[k] = on ? __ldcg(rec + 8 + h) : 0.f;
@@ -860,8 +957,7 @@ cudaError_t launch(const Params &P, cudaStream_t stream)
     // no more CTAs than the tables' rows could fill
     const long long most = (long long)P.a.num_seqs * P.heads *
                            ((((long long)P.a.max_blocks_per_seq << P.shift) + kChunk - 1) / kChunk + kPairCost);
-    const long long runs = (most + kMinShare - 1) / kMinShare;
-    const int ctas = (int)std::min<long long>(std::min(sms, kMaxQ4Ctas), (runs + Geo<D>::WARPS - 1) / Geo<D>::WARPS);
+    const int ctas = (int)std::min<long long>(std::min(sms, kMaxQ4Ctas), (most + Geo<D>::WARPS - 1) / Geo<D>::WARPS);
     Params p = P;
     void *args[] = {&p};
     return launch_early(kern, dim3(ctas), Geo<D>::THREADS, sizeof(Smem<D>), stream, args);
@@ -882,7 +978,9 @@ cudaError_t launch_decode_q4(const Q4DecodeArgs &a, cudaStream_t stream)
     P.subs = (P.group + 7) / 8;
     P.heads = a.num_kv_heads * P.subs;
     P.shift = a.block_size == 4 ? 2 : a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
-    P.scale_log2 = a.scale * 1.4426950408889634f;
+    // a unit of the products has to be positive: q takes the scale's sign
+    P.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
+    P.sign = a.scale < 0.f ? -1.f : 1.f;
     P.counters = a.counters;
     P.records = a.records;
     if (a.head_dim == 64)
