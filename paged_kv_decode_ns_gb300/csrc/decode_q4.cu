@@ -172,17 +172,6 @@ __device__ __forceinline__ float2 halves(uint32_t w) { return unpack2<F16>(w); }
 // ---------------------------------------------------------------------------
 // Walk over the pieces of a warp's run.
 // ---------------------------------------------------------------------------
-// a / b, a >= 0, b > 0; by fp32 (2^-22 of the quotient) where that is off by one at most.
-__device__ __forceinline__ int quotient(int a, int b)
-{
-    if (a >= 1 << 22)
-        return a / b;
-    int q = (int)__fdividef((float)a, (float)b);
-    const int r = a - q * b;
-    q += r < 0 ? -1 : r >= b ? 1 : 0;
-    return q;
-}
-
 struct Piece {
     int s, h;       // sequence, pair of it
     int L;          // keys of the sequence

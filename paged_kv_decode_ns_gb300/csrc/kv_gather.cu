@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kThreads, 5) kv_gather_kernel(const GatherArgs
         src[threadIdx.x] = row;
     }
     __syncthreads();
+    const int head_shift = __ffs(head_chunks) - 1;  // 8 or 16 chunks
     const int n = nt * row_chunks;
     const long long out0 = (long long)t0 * row_chunks;
     for (int i0 = threadIdx.x; i0 < n; i0 += kThreads * kBatch) {
@@ -94,8 +95,8 @@ __global__ void __launch_bounds__(kThreads, 5) kv_gather_kernel(const GatherArgs
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int i = i0 + b * kThreads;
-            const int t = i / row_chunks, c = i - t * row_chunks;
-            const int h = c / head_chunks, chunk = c - h * head_chunks;
+            const int t = quotient(i, row_chunks), c = i - t * row_chunks;
+            const int h = c >> head_shift, chunk = c - (h << head_shift);
             const long long row = i < n ? src[t] : -1;
             on[b] = row >= 0;
             if (!on[b])
@@ -140,9 +141,10 @@ cudaError_t launch_kv_gather(const GatherArgs &in, int pool, cudaStream_t stream
 {
     GatherArgs a = in;
     int head_chunks = a.head_dim / 8, row_chunks = a.num_kv_heads * head_chunks;
-    // a batch for every thread, two of the smaller reads from q8_0 (71 us with one);
-    // at least eight rows, so that the look-ups are shared
-    int tokens = std::min(kMaxTokens, std::max(8, (pool == 16 ? 1 : 2) * kThreads * kBatch / row_chunks));
+    // a batch for every thread, two of the smaller reads from q8_0 (71 us with one; q4_0 is the
+    // other way round, 20.7 us against 21.3 for 32 sequences at head_dim 128, its arithmetic being
+    // more); at least eight rows, so that the look-ups are shared
+    int tokens = std::min(kMaxTokens, std::max(8, (pool == 8 ? 2 : 1) * kThreads * kBatch / row_chunks));
     const unsigned grid = (unsigned)((a.total_tokens + tokens - 1) / tokens);
     const bool bf16 = a.dtype == NS_BF16;
     const void *kern = pool == 16  ? (const void *)kv_gather_kernel<F16, 16>

@@ -282,6 +282,17 @@ __device__ __forceinline__ float fast_exp2(float x)
     return y;
 }
 
+// a / b, a >= 0, b > 0; by fp32 (2^-22 of the quotient) where that is off by one at most.
+__device__ __forceinline__ int quotient(int a, int b)
+{
+    if (a >= 1 << 22)
+        return a / b;
+    int q = (int)__fdividef((float)a, (float)b);
+    const int r = a - q * b;
+    q += r < 0 ? -1 : r >= b ? 1 : 0;
+    return q;
+}
+
 __device__ __forceinline__ uint4 lds128(const void *p)
 {
     return *reinterpret_cast<const uint4 *>(p);

@@ -67,16 +67,39 @@ __device__ __forceinline__ void q4_quantize8(const float *x, uint32_t &codes, ui
     }
 }
 
-// Eight q4_0 codes (a word) and their step -> eight elements: fp16(d) * (code - 8) is
-// exact in fp32 and rounds once.
+// Eight q4_0 codes (a word) and their step -> eight elements.  code - 8 is exact in either
+// type that the product is taken in, so fp16(d) * (code - 8) rounds once: a code in the low
+// bits of an fp16 1024 (an fp32 2^23), less that and 8, is code - 8.
 template <typename T>
-__device__ __forceinline__ uint4 q4_elements(uint32_t w, uint16_t d16)
+__device__ __forceinline__ uint4 q4_elements(uint32_t w, uint16_t d16);
+
+template <>
+__device__ __forceinline__ uint4 q4_elements<F16>(uint32_t w, uint16_t d16)
 {
+    const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+    const uint32_t a = __byte_perm(even, odd, 0x5140), b = __byte_perm(even, odd, 0x7362);  // elements 0-3, 4-7
+    const __half2 off = __half2half2(__ushort_as_half(0x6408)), d = __half2half2(__ushort_as_half(d16));  // 1032
+    uint4 r = make_uint4(__byte_perm(a, 0x64646464u, 0x4140), __byte_perm(a, 0x64646464u, 0x4342),
+                         __byte_perm(b, 0x64646464u, 0x4140), __byte_perm(b, 0x64646464u, 0x4342));
+    __half2 *h = reinterpret_cast<__half2 *>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = __hmul2(__hsub2(h[i], off), d);
+    return r;
+}
+
+template <>
+__device__ __forceinline__ uint4 q4_elements<BF16>(uint32_t w, uint16_t d16)
+{
+    const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
     const float d = __half2float(__ushort_as_half(d16));
-    auto pair = [&](int i) {
-        return pack2<T>(d * (float)((int)((w >> (4 * i)) & 15u) - 8), d * (float)((int)((w >> (4 * i + 4)) & 15u) - 8));
+    auto element = [&](uint32_t codes, int i) {
+        uint32_t x;
+        asm("prmt.b32 %0, %1, %2, %3;" : "=r"(x) : "r"(codes), "r"(0x4b000000u), "r"(0x7550u + i));
+        return d * (__uint_as_float(x) - 8388616.f);
     };
-    return make_uint4(pair(0), pair(2), pair(4), pair(6));
+    return make_uint4(pack2<BF16>(element(even, 0), element(odd, 0)), pack2<BF16>(element(even, 1), element(odd, 1)),
+                      pack2<BF16>(element(even, 2), element(odd, 2)), pack2<BF16>(element(even, 3), element(odd, 3)));
 }
 
 }  // namespace ns

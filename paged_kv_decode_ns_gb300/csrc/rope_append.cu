@@ -21,36 +21,67 @@ namespace ns {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 4;  // rows of a lane in flight
+
+// What a warp does is a run of steps, 32 / (D / 8) head rows each: a token's query rows, then its
+// key and value rows.
+template <int D>
+constexpr int step_rows() { return 32 / (D / 8); }
+// Query steps in flight: 18 rows of 64 elements are one batch and a step (13400 tokens 15.8 us, 16.8 by
+// three); wider rows fill the GPU sooner by smaller ones (256 tokens of 32 / 8 heads 3.1 us, 3.5 by four).
+template <int D>
+constexpr int batch_steps() { return D == 64 ? 4 : 3; }
 
 template <typename T, int D, int POOL, bool ROPE>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendArgs a, int parts, int part_rows)
+__global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const RopeAppendArgs a, int parts, int part_steps)
 {
     grid_dependency_wait();
     grid_launch_dependents();
-    constexpr int C = D / 8, ROWS = 32 / C;  // lanes of a row, rows of a warp at a time
+    constexpr int C = D / 8, ROWS = step_rows<D>(), kBatch = batch_steps<D>();  // lanes of a row, rows of a step
     const int lane = threadIdx.x & 31, c = lane % C, sub = lane / C;
     const long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const long long t = item / parts;
     const int part = (int)(item - t * parts);
     if (t >= a.num_tokens)
         return;
+    const int hq = ROPE ? a.num_q_heads : 0, hkv = a.num_kv_heads;
+    const int q_steps = (hq + ROWS - 1) / ROWS, steps = q_steps + (2 * hkv + ROWS - 1) / ROWS;
+    const int first = part * part_steps, last = min(steps, first + part_steps);
+
+    // the first rows are on their way before the slot and the position are known
     const long long slot = a.slot_mapping[t];
+    const int pos = ROPE ? a.positions[t] : 0;
+    const uint16_t *q_row = static_cast<const uint16_t *>(a.q) + t * a.q_stride + (sub * D + c * 8);
+    const uint16_t *k_row = static_cast<const uint16_t *>(a.k) + t * a.k_stride + c * 8,
+                   *v_row = static_cast<const uint16_t *>(a.v) + t * a.v_stride + c * 8;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    uint4 qw[kBatch], kw;
+    auto load_q = [&](int step) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            qw[b] = step + b < last && (step + b) * ROWS + sub < hq
+                        ? *reinterpret_cast<const uint4 *>(q_row + (step + b) * (ROWS * D))
+                        : none;
+    };
+    auto load_kv = [&](int step) {  // keys, then values
+        const int r = (step - q_steps) * ROWS + sub;
+        return step < last && r < 2 * hkv ? *reinterpret_cast<const uint4 *>(r < hkv ? k_row + r * D : v_row + (r - hkv) * D) : none;
+    };
+    if (first < q_steps)
+        load_q(first);
+    kw = load_kv(max(first, q_steps));
+
     if (slot < 0)
         return;
-    const int pos = ROPE ? a.positions[t] : 0;
     const bool bad_slot = slot >= a.num_blocks * a.block_size, bad_pos = ROPE && (pos < 0 || pos >= a.max_positions);
     if (bad_slot || bad_pos) {
         if (part == 0 && lane == 0)
             raise_status(a.status, (bad_slot ? NS_DEV_BAD_SLOT : 0u) | (bad_pos ? NS_DEV_BAD_POSITION : 0u));
         return;
     }
-    const long long blk = slot / a.block_size;
-    const int off = (int)(slot - blk * a.block_size);
 
     // this lane's cosines and sines (of the pair's lower element negative), and the lane
     // that holds the other elements of its pairs
-    float co[8], si[8];
+    float2 co[4], si[4];
     const int half = a.rotary_dim / 2, hc = half / 8;  // elements, lanes (halves)
     const bool turned = ROPE && c < 2 * hc;
     const bool pairs = ROPE && a.interleaved;
@@ -62,98 +93,102 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
             other = low ? lane + hc : lane - hc;
             const float *at = row + (low ? c : c - hc) * 8;
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(at + i), y = *reinterpret_cast<const float4 *>(at + half + i);
-                co[i] = x.x, co[i + 1] = x.y, co[i + 2] = x.z, co[i + 3] = x.w;
-                si[i] = low ? -y.x : y.x, si[i + 1] = low ? -y.y : y.y, si[i + 2] = low ? -y.z : y.z,
-                si[i + 3] = low ? -y.w : y.w;
+            for (int i = 0; i < 4; i += 2) {
+                const float4 x = *reinterpret_cast<const float4 *>(at + 2 * i), y = *reinterpret_cast<const float4 *>(at + half + 2 * i);
+                co[i] = make_float2(x.x, x.y), co[i + 1] = make_float2(x.z, x.w);
+                si[i] = low ? make_float2(-y.x, -y.y) : make_float2(y.x, y.y);
+                si[i + 1] = low ? make_float2(-y.z, -y.w) : make_float2(y.z, y.w);
             }
         } else {
             const float4 x = *reinterpret_cast<const float4 *>(row + c * 4), y = *reinterpret_cast<const float4 *>(row + half + c * 4);
-            co[0] = co[1] = x.x, co[2] = co[3] = x.y, co[4] = co[5] = x.z, co[6] = co[7] = x.w;
-            si[1] = y.x, si[3] = y.y, si[5] = y.z, si[7] = y.w;
-            si[0] = -y.x, si[2] = -y.y, si[4] = -y.z, si[6] = -y.w;
+            co[0] = make_float2(x.x, x.x), co[1] = make_float2(x.y, x.y), co[2] = make_float2(x.z, x.z), co[3] = make_float2(x.w, x.w);
+            si[0] = make_float2(-y.x, y.x), si[1] = make_float2(-y.y, y.y), si[2] = make_float2(-y.z, y.z), si[3] = make_float2(-y.w, y.w);
         }
     }
-
-    // rows of the token: queries, keys, values
-    const int hq = ROPE ? a.num_q_heads : 0, hkv = a.num_kv_heads, rows = hq + 2 * hkv;
-    const int first = part * part_rows, last = min(rows, first + part_rows);
-    for (int r0 = first; r0 < last; r0 += ROWS * kBatch) {
-        uint4 w[kBatch];
+    // x: this lane's elements, turned where `turn` says so; all lanes take part
+    auto rotate = [&](const uint4 &w, bool turn, float2 (&x)[4]) {
+        uint4 o;
+        if (pairs) {  // the other element of a pair is in the same word
+            o = make_uint4(__byte_perm(w.x, 0u, 0x1032), __byte_perm(w.y, 0u, 0x1032), __byte_perm(w.z, 0u, 0x1032),
+                           __byte_perm(w.w, 0u, 0x1032));
+        } else {
+            o.x = __shfl_sync(0xffffffffu, w.x, other);
+            o.y = __shfl_sync(0xffffffffu, w.y, other);
+            o.z = __shfl_sync(0xffffffffu, w.z, other);
+            o.w = __shfl_sync(0xffffffffu, w.w, other);
+        }
+        const uint32_t mine[4] = {w.x, w.y, w.z, w.w}, others[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + b * ROWS + sub;
-            w[b] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < last) {
-                const bool is_q = r < hq, is_k = r < hq + hkv;
-                const char *src = static_cast<const char *>(is_q ? a.q : is_k ? a.k : a.v);
-                const long long row = t * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride);
-                const int h = is_q ? r : is_k ? r - hq : r - hq - hkv;
-                w[b] = *reinterpret_cast<const uint4 *>(src + (row + (long long)h * D + c * 8) * 2);
+        for (int i = 0; i < 4; ++i) {
+            x[i] = unpack2<T>(mine[i]);
+            if (turn) {  // (the packed products and sum of fp32 pairs come out contracted)
+                const float2 y = unpack2<T>(others[i]);
+                x[i].x = __fadd_rn(__fmul_rn(x[i].x, co[i].x), __fmul_rn(y.x, si[i].x));
+                x[i].y = __fadd_rn(__fmul_rn(x[i].y, co[i].y), __fmul_rn(y.y, si[i].y));
             }
         }
+    };
+    auto packed = [](const float2 (&x)[4]) {
+        return make_uint4(pack2<T>(x[0].x, x[0].y), pack2<T>(x[1].x, x[1].y), pack2<T>(x[2].x, x[2].y), pack2<T>(x[3].x, x[3].y));
+    };
+
+    if (ROPE) {
+        uint16_t *to = static_cast<uint16_t *>(a.q_out) + t * a.q_out_stride + (sub * D + c * 8);
+        for (int s0 = first; s0 < min(last, q_steps); s0 += kBatch) {
+            if (s0 > first)
+                load_q(s0);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int top = r0 + b * ROWS;  // the warp's first row: the same in all lanes
-            if (top >= last)
-                break;
-            const int r = top + sub;
-            const bool on = r < last, is_q = r < hq, is_v = r >= hq + hkv;
-            float x[8];
-            {
-                const float2 p0 = unpack2<T>(w[b].x), p1 = unpack2<T>(w[b].y), p2 = unpack2<T>(w[b].z), p3 = unpack2<T>(w[b].w);
-                x[0] = p0.x, x[1] = p0.y, x[2] = p1.x, x[3] = p1.y, x[4] = p2.x, x[5] = p2.y, x[6] = p3.x, x[7] = p3.y;
+            for (int b = 0; b < kBatch; ++b) {
+                if (s0 + b >= min(last, q_steps))
+                    break;
+                float2 x[4];
+                rotate(qw[b], turned, x);
+                if ((s0 + b) * ROWS + sub < hq)
+                    *reinterpret_cast<uint4 *>(to + (s0 + b) * (ROWS * D)) = turned ? packed(x) : qw[b];
             }
-            if (ROPE && top < hq + hkv) {
-                uint4 o;
-                if (pairs) {  // the other element of a pair is in the same word
-                    o = make_uint4(__byte_perm(w[b].x, 0u, 0x1032), __byte_perm(w[b].y, 0u, 0x1032),
-                                   __byte_perm(w[b].z, 0u, 0x1032), __byte_perm(w[b].w, 0u, 0x1032));
-                } else {
-                    o.x = __shfl_sync(0xffffffffu, w[b].x, other);
-                    o.y = __shfl_sync(0xffffffffu, w[b].y, other);
-                    o.z = __shfl_sync(0xffffffffu, w[b].z, other);
-                    o.w = __shfl_sync(0xffffffffu, w[b].w, other);
-                }
-                if (turned && !is_v) {
-                    const float2 q0 = unpack2<T>(o.x), q1 = unpack2<T>(o.y), q2 = unpack2<T>(o.z), q3 = unpack2<T>(o.w);
-                    const float y[8] = {q0.x, q0.y, q1.x, q1.y, q2.x, q2.y, q3.x, q3.y};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = __fadd_rn(__fmul_rn(x[i], co[i]), __fmul_rn(y[i], si[i]));
-                    w[b] = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
-                }
-            }
-            if (on && is_q)
-                *reinterpret_cast<uint4 *>(static_cast<char *>(a.q_out) + (t * a.q_out_stride + (long long)r * D + c * 8) * 2) = w[b];
-            if (top + ROWS <= hq)  // no lane of the warp has a row for the cache
-                continue;
-            const int h = is_v ? r - hq - hkv : r - hq;
-            const bool store = on && !is_q;
-            if (ROPE && store && !is_v && a.k_out != nullptr)
-                *reinterpret_cast<uint4 *>(static_cast<char *>(a.k_out) + (t * a.k_out_stride + (long long)h * D + c * 8) * 2) = w[b];
-            const long long prow = (blk * hkv + (store ? h : 0)) * a.block_size + off;
-            void *pool = is_v ? a.v_pool : a.k_pool, *scales = is_v ? a.v_scales : a.k_scales;
-            if constexpr (POOL == 16) {
-                if (store)
-                    static_cast<uint4 *>(pool)[prow * C + c] = w[b];
+        }
+    }
+    if (last <= q_steps)
+        return;
+    const int shift = __ffs(a.block_size) - 1;  // a power of two
+    const long long row0 = (((slot >> shift) * hkv) << shift) + ((int)slot & (a.block_size - 1));  // of kv head 0
+    for (int step = max(first, q_steps); step < last; ++step) {
+        const int r = (step - q_steps) * ROWS + sub;
+        const bool on = r < 2 * hkv, is_v = r >= hkv;
+        const int h = is_v ? r - hkv : r;
+        uint4 w = kw;
+        kw = load_kv(step + 1);
+        float2 x[4];
+        if (ROPE) {
+            rotate(w, turned && !is_v, x);
+            if (turned && !is_v)
+                w = packed(x);
+        } else {
+            x[0] = unpack2<T>(w.x), x[1] = unpack2<T>(w.y), x[2] = unpack2<T>(w.z), x[3] = unpack2<T>(w.w);
+        }
+        if (ROPE && on && !is_v && a.k_out != nullptr)
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.k_out) + t * a.k_out_stride + (h * D + c * 8)) = w;
+        const long long prow = row0 + ((long long)h << shift);
+        void *pool = is_v ? a.v_pool : a.k_pool;
+        if constexpr (POOL == 16) {
+            if (on)
+                static_cast<uint4 *>(pool)[prow * C + c] = w;
+        } else {
+            const float y[8] = {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y};
+            uint16_t d16;
+            if constexpr (POOL == 8) {
+                uint2 codes;
+                q8_quantize8(y, codes, d16);
+                if (on)
+                    static_cast<uint2 *>(pool)[prow * C + c] = codes;
             } else {
-                uint16_t d16;
-                if constexpr (POOL == 8) {
-                    uint2 codes;
-                    q8_quantize8(x, codes, d16);
-                    if (store)
-                        static_cast<uint2 *>(pool)[prow * C + c] = codes;
-                } else {
-                    uint32_t codes;
-                    q4_quantize8(x, codes, d16);
-                    if (store)
-                        static_cast<uint32_t *>(pool)[prow * C + c] = codes;
-                }
-                if (store && (c & 3) == 0)
-                    static_cast<uint16_t *>(scales)[prow * (C / 4) + (c >> 2)] = d16;
+                uint32_t codes;
+                q4_quantize8(y, codes, d16);
+                if (on)
+                    static_cast<uint32_t *>(pool)[prow * C + c] = codes;
             }
+            if (on && (c & 3) == 0)
+                static_cast<uint16_t *>(is_v ? a.v_scales : a.k_scales)[prow * (C / 4) + (c >> 2)] = d16;
         }
     }
 }
@@ -180,17 +215,19 @@ cudaError_t launch_rope_append(const RopeAppendArgs &in, int pool, cudaStream_t 
     const cudaError_t e = current_sms(&sms);
     if (e != cudaSuccess)
         return e;
-    // A batch of rows is the least a warp takes; a token's batches are shared by as many
-    // warps as the GPU has room for (16 an SM), so that few tokens spread over it.
-    const int warp_rows = 32 / (a.head_dim / 8) * kBatch, rows = (rope ? a.num_q_heads : 0) + 2 * a.num_kv_heads;
-    const long long batches = (rows + warp_rows - 1) / warp_rows;
-    const long long room = std::max<long long>(1, (long long)sms * 16 / a.num_tokens);
+    // A batch of steps is the least a warp takes; a token's batches are shared by as many
+    // warps as the GPU has room for (32 an SM), so that few tokens spread over it.
+    const int rows = a.head_dim == 64 ? step_rows<64>() : step_rows<128>();
+    const int batch = a.head_dim == 64 ? batch_steps<64>() : batch_steps<128>();
+    const int steps = ((rope ? a.num_q_heads : 0) + rows - 1) / rows + (2 * a.num_kv_heads + rows - 1) / rows;
+    const long long batches = (steps + batch - 1) / batch;
+    const long long room = std::max<long long>(1, (long long)sms * 32 / a.num_tokens);
     const int per = (int)((batches + std::min(batches, room) - 1) / std::min(batches, room));
-    int part_rows = per * warp_rows, parts = (rows + part_rows - 1) / part_rows;
+    int part_steps = per * batch, parts = (steps + part_steps - 1) / part_steps;
     const long long warps = (long long)a.num_tokens * parts, grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (grid > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
-    void *args[] = {&a, &parts, &part_rows};
+    void *args[] = {&a, &parts, &part_steps};
     return launch_early(kern, dim3((unsigned)grid), kThreads, 0, stream, args);
 }
 
