@@ -422,6 +422,10 @@ def ns_kv_append_paged_attn_decode_q8_0(q, k_new, v_new, slot_mapping, k_codes, 
 def _rows(t: torch.Tensor, name: str, dtype, shape):
     """Pointer of [T, H, D] rows that are dense themselves, and elements from one to the next
     (with no next row, the row's own width)."""
+    if t.is_cuda and t.dtype is dtype:
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and s1 == shape[2] and shape[0] > 1:
+            return t.data_ptr(), s0
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
     if t.dtype is not dtype:
@@ -594,13 +598,13 @@ def ns_paged_attn_prefill_q4_0(q, query_start_loc, k_codes, k_scales, v_codes, v
 def _rope_append(name, q, k, v, positions, cos_sin, slot_mapping, q_out, pools, nb, hkv, bs, d, k_out, interleaved,
                  stream):
     rows, keys, table = q.shape, k.shape, cos_sin.shape
-    if len(rows) != 3 or len(keys) != 3 or v.shape != keys or keys[0] != rows[0] or keys[1:] != (hkv, d) \
-            or rows[2] != d:
+    if len(rows) != 3 or rows[2] != d or keys != (rows[0], hkv, d) or v.shape != keys:
         raise ValueError("q must be [T, Hq, D], k and v [T, Hkv, D], with the pools' heads and head_dim")
     T, hq, _ = rows
     if q_out.shape != rows or (k_out is not None and k_out.shape != keys):
         raise ValueError("q_out must have q's shape, k_out k's")
-    if positions.shape != (T,) or slot_mapping.shape != (T,) or len(table) != 2:
+    tokens = (T,)
+    if positions.shape != tokens or slot_mapping.shape != tokens or len(table) != 2:
         raise ValueError("positions and slot_mapping must be [T], cos_sin [max_positions, rotary_dim]")
     dtype = q.dtype
     dt = _dtype_code(q)

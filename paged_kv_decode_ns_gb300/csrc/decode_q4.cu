@@ -59,7 +59,6 @@ struct alignas(16) Smem {
     using GG = Geo<D>;
     uint8_t ring[GG::WARPS][GG::STAGES][GG::STAGE];  // afterwards a warp's last record
     float first[GG::WARPS][GG::RECORD];              // its first one
-    uint32_t live[GG::WARPS][GG::STAGES];            // tokens of a chunk that count
     int before[GG::THREADS];                         // chunks in front of a thread's sequences
     int scan[GG::WARPS];
     // what a warp left: the pair of its first and last record (-1: none) and whether the first
@@ -77,6 +76,7 @@ struct Params {
     int subs;       // of a kv head
     int group;      // query heads of a kv head
     int shift;      // log2 of the block size
+    uint32_t blocks;  // of the pool (entries have 31 bits)
     float scale_log2, sign;  // of the scale
     int *counters;
     float *records;
@@ -323,7 +323,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
     using GG = Geo<D>;
     constexpr int R = GG::R, ST = GG::STAGES, W = GG::WARPS;
     constexpr int PARTS = R;                    // 16-byte parts of a token's codes: one a group
-    constexpr int COPIES = kChunk * PARTS / 32; // of a lane, for K and again for V
     constexpr int SPAN = 16 / (2 * R);          // tokens whose scales are 16 bytes
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
@@ -416,30 +415,38 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
     }
     Walk ahead_walk = next;  // the copies' walk, up to ST - 1 chunks ahead of the arithmetic
 
-    // ---- copies: a chunk's codes and scales of K and V by 16 bytes a lane
+    // ---- copies: a chunk's codes and scales of K and V by 16 bytes a lane.  A lane's places in
+    // its tokens' blocks are the same in every chunk, so an address is one multiplication of
+    // the block's number.
     const uint32_t ring = smem_addr(sm.ring[warp][0]);
-    const int bs1 = (1 << P.shift) - 1;
     constexpr uint32_t row_bytes = D / 2;
-    const uint32_t block_rows = (uint32_t)a.num_kv_heads << P.shift;  // the pool's row numbers have 32 bits
-    constexpr int N = kChunk / SPAN;  // lanes that copy the scales of K, and again of V
-    const uint8_t *k_from = static_cast<const uint8_t *>(a.k_codes) + lane % PARTS * 16,
-                  *v_from = static_cast<const uint8_t *>(a.v_codes) + lane % PARTS * 16,
-                  *s_from = static_cast<const uint8_t *>(lane < N ? a.k_scales : a.v_scales);
+    constexpr int N = kChunk / SPAN;          // lanes that copy the scales of K, and again of V
+    constexpr int TOKENS = 32 / PARTS;        // of a copy of all lanes
+    const int bs1 = (1 << P.shift) - 1;
+    const uint32_t block_rows = (uint32_t)a.num_kv_heads << P.shift;  // of all heads
+    const int part = lane % PARTS, tau0 = lane / PARTS, tau_s = lane % N * SPAN;
+    // eight rows of one part are eight different banks of 16 bytes
+    const uint32_t place = tau0 * row_bytes + (D == 64 ? part ^ ((tau0 >> 2) & 1) : part ^ ((tau0 >> 1) & 3)) * 16;
+    const uint32_t lane_at = (tau0 & bs1) * row_bytes + part * 16, lane_at_s = (tau_s & bs1) * (2 * R);
+    // blocks of 32: the second 16 tokens are further on in the same block (head_dim 64)
+    const uint32_t hop = D == 64 && P.shift == 5 ? 16 * row_bytes : 0u;
     Piece ip;
     ip.c = ip.c1 = 0;
     ip.s = ip.h = ip.L = 0;
-    int entry = -1;           // the block of this lane's token in the next chunk to copy
-    uint32_t head_row = 0u;   // first row of the piece's kv head in a block
+    int entry = -1;  // the block of this lane's token in the next chunk to copy
+    const uint8_t *k_from = nullptr, *v_from = nullptr, *s_from = nullptr;  // of the piece's head in block 0
     const int32_t *row_of = nullptr;  // its sequence's table row
-    uint32_t to = ring;
-    int issued = 0;           // chunks, modulo ST
+    uint32_t to = ring, in_flight[ST - 1] = {};  // tokens that count of the chunks on their way
     auto look_up = [&]() {  // the next chunk's blocks, whose piece may be another one
         if (ip.c == ip.c1) {
             while (ip.c == ip.c1 && ahead_walk.left > 0)
                 ip = next_piece(P, ahead_walk);
             if (ip.c < ip.c1) {
                 const int kv = P.subs == 1 ? ip.h : ip.h / P.subs;
-                head_row = (uint32_t)kv << P.shift;
+                const uint32_t head = (uint32_t)kv << P.shift;
+                k_from = static_cast<const uint8_t *>(a.k_codes) + (head * row_bytes + lane_at);
+                v_from = static_cast<const uint8_t *>(a.v_codes) + (head * row_bytes + lane_at);
+                s_from = static_cast<const uint8_t *>(lane < N ? a.k_scales : a.v_scales) + (head * (2 * R) + lane_at_s);
                 row_of = a.block_tables + (long long)ip.s * a.max_blocks_per_seq;
             }
         }
@@ -449,42 +456,37 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
             entry = row_of[tok >> P.shift];
     };
     auto issue = [&]() {
-        if (ip.c < ip.c1) {
-            const bool ok = entry >= 0 && entry < a.num_blocks;
-            if (!ok && ip.c * kChunk + lane < ip.L)
-                raise_status(a.status, NS_DEV_BAD_BLOCK_ID);
-            const uint32_t live = __ballot_sync(0xffffffffu, ok);
-            if (lane == 0)
-                sm.live[warp][issued] = live;
-            const int block = ok ? entry : -1;
 #pragma unroll
-            for (int i = 0; i < COPIES; ++i) {
-                const int tau = lane / PARTS + i * (32 / PARTS), part = lane % PARTS;
-                const int id = __shfl_sync(0xffffffffu, block, tau);
-                // eight rows of one part are eight different banks of 16 bytes
-                const int turned = D == 64 ? part ^ ((tau >> 2) & 1) : part ^ ((tau >> 1) & 3);
-                const uint32_t dst = to + tau * row_bytes + turned * 16;
+        for (int i = 0; i < ST - 2; ++i)
+            in_flight[i] = in_flight[i + 1];
+        if (ip.c < ip.c1) {
+            const bool ok = (uint32_t)entry < P.blocks;
+            const int block = ok ? entry : -1;
+            const uint32_t live = __ballot_sync(0xffffffffu, ok);
+            in_flight[ST - 2] = live;
+            if (live != 0xffffffffu && !ok && ip.c * kChunk + lane < ip.L)
+                raise_status(a.status, NS_DEV_BAD_BLOCK_ID);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // 16 tokens each
+                const int id = __shfl_sync(0xffffffffu, block, tau0 + 16 * i);
                 if (id >= 0) {
-                    const uint32_t row = (uint32_t)id * block_rows + (head_row + (tau & bs1));
-                    copy16(dst, k_from + (unsigned long long)row * row_bytes);
-                    copy16(dst + GG::CODES, v_from + (unsigned long long)row * row_bytes);
+                    const unsigned long long at = (unsigned long long)((uint32_t)id) * (block_rows * row_bytes) + i * hop;
+                    const uint8_t *k = k_from + at, *v = v_from + at;
+                    const uint32_t dst = to + place + i * 16 * row_bytes;
+#pragma unroll
+                    for (int x = 0; x < 16 / TOKENS; ++x) {
+                        copy16(dst + x * TOKENS * row_bytes, k + x * TOKENS * row_bytes);
+                        copy16(dst + x * TOKENS * row_bytes + GG::CODES, v + x * TOKENS * row_bytes);
+                    }
                 }
             }
             {
-                const int tau = (lane % N) * SPAN;
-                const int id = __shfl_sync(0xffffffffu, block, tau);
-                if (id >= 0 && lane < 2 * N) {
-                    const uint32_t row = (uint32_t)id * block_rows + (head_row + (tau & bs1));
-                    copy16(to + 2 * GG::CODES + lane * 16, s_from + (unsigned long long)row * (2 * R));
-                }
+                const int id = __shfl_sync(0xffffffffu, block, tau_s);
+                if (id >= 0 && lane < 2 * N)
+                    copy16(to + 2 * GG::CODES + lane * 16, s_from + (unsigned long long)((uint32_t)id) * (block_rows * (2 * R)));
             }
             ++ip.c;
-            ++issued;
-            to += GG::STAGE;
-            if (issued == ST) {
-                issued = 0;
-                to = ring;
-            }
+            to = to == ring + (ST - 1) * GG::STAGE ? ring : to + GG::STAGE;
             look_up();
         }
         copies_commit();
@@ -582,10 +584,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
         for (int c = p.c; c < p.c1; ++c) {
             copies_wait<ST - 2>();
             __syncwarp();
+            const uint32_t live = in_flight[0];
             issue();  // into the stage that the last turn has read
             const uint32_t from = read_behind(ring + used * GG::STAGE);
             const uint8_t *stage = sm.ring[warp][used];
-            const uint32_t live = sm.live[warp][used];
             used = used + 1 == ST ? 0 : used + 1;
 
             // ---- scores: 16 tokens at a time, by group
@@ -968,6 +970,7 @@ cudaError_t launch_decode_q4(const Q4DecodeArgs &a, cudaStream_t stream)
     P.heads = a.num_kv_heads * P.subs;
     P.shift = a.block_size == 4 ? 2 : a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
     // a unit of the products has to be positive: q takes the scale's sign
+    P.blocks = (uint32_t)std::min<long long>(a.num_blocks, 0x80000000LL);
     P.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
     P.sign = a.scale < 0.f ? -1.f : 1.f;
     P.counters = a.counters;

@@ -828,7 +828,7 @@ ns_status ns_paged_attn_decode_q4_0(const void *q, const void *k_codes, const vo
         return NS_ERR_INVALID_ARG;
     const int subs = (num_q_heads / num_kv_heads + ns::kMaxGroup - 1) / ns::kMaxGroup;  // 8 query heads at a time
     if ((long long)max_blocks_per_seq * block_size > 0x7fffffffLL - 1024 ||  // positions are 32-bit
-        num_blocks > 0x100000000LL / ((long long)num_kv_heads * block_size) ||  // as are the pool's rows (2^32 are 309 GB)
+        (long long)num_kv_heads * block_size * (head_dim / 2) > 0xffffffffLL ||  // as are the bytes of a block
         !ns::q4_decode_fits(num_seqs, (long long)num_kv_heads * subs, max_blocks_per_seq, block_size))
         return NS_ERR_UNSUPPORTED;
     if (num_seqs == 0)

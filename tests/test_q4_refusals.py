@@ -85,7 +85,7 @@ def decode(lib, q=A, kc=A, ks=A, vc=A, vs=A, bt=A, cl=A, S=2, hq=14, hkv=2, d=64
     (dict(hq=65, hkv=1), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(d=128, bs=32), UNSUPPORTED),
     (dict(bs=64), UNSUPPORTED), (dict(dtype=2), UNSUPPORTED), (dict(width=0), INVALID), (dict(nb=0), INVALID),
     (dict(width=1 << 30), UNSUPPORTED), (dict(S=1 << 20, width=1 << 20, bs=32), UNSUPPORTED),
-    (dict(nb=1 << 40), UNSUPPORTED), (dict(nb=(1 << 27) + 1), UNSUPPORTED),
+    (dict(hq=1 << 27, hkv=1 << 27), UNSUPPORTED),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(q=None), INVALID),
     (dict(ks=None), INVALID), (dict(bt=None), INVALID), (dict(cl=None), INVALID), (dict(out=None), INVALID),
     (dict(ws=None), INVALID), (dict(vc=A + 8), INVALID), (dict(out=A + 2), INVALID), (dict(wsb=100), INVALID),
