@@ -160,6 +160,39 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+def _current() -> int:
+    """The current device, or -2 where there is none (then the tensors are refused)."""
+    try:
+        return _raw_device()
+    except RuntimeError:
+        return -2
+
+
+def _on_current(t: torch.Tensor, name: str, device: int):
+    if t.get_device() != device:
+        raise ValueError(f"{name} must live on the current CUDA device")
+
+
+def _here(t: torch.Tensor, name: str, dtype, device: int) -> int:
+    """_dev of a tensor that has to be on the current device."""
+    if t.get_device() == device and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    at = _dev(t, name, dtype)
+    _on_current(t, name, device)
+    return at
+
+
+def _rows_here(t: torch.Tensor, name: str, dtype, shape, device: int):
+    """_rows of a tensor that has to be on the current device."""
+    if t.get_device() == device and t.dtype is dtype:
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and s1 == shape[2] and shape[0] > 1:
+            return t.data_ptr(), s0
+    at = _rows(t, name, dtype, shape)
+    _on_current(t, name, device)
+    return at
+
+
 def _stream(stream) -> int:
     if _capture.on:
         return _STREAM_SLOT
@@ -422,10 +455,6 @@ def ns_kv_append_paged_attn_decode_q8_0(q, k_new, v_new, slot_mapping, k_codes, 
 def _rows(t: torch.Tensor, name: str, dtype, shape):
     """Pointer of [T, H, D] rows that are dense themselves, and elements from one to the next
     (with no next row, the row's own width)."""
-    if t.is_cuda and t.dtype is dtype:
-        s0, s1, s2 = t.stride()
-        if s2 == 1 and s1 == shape[2] and shape[0] > 1:
-            return t.data_ptr(), s0
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
     if t.dtype is not dtype:
@@ -529,51 +558,56 @@ def ns_kv_gather_q8_0(k_codes, k_scales, v_codes, v_scales, block_tables, start_
     _check(st, "ns_kv_gather_q8_0")
 
 
-def _q4_pools(k_codes, k_scales, v_codes, v_scales):
+def _q4_pools(k_codes, k_scales, v_codes, v_scales, here):
     codes = k_codes.shape
     nb, hkv, bs, half = codes
     if v_codes.shape != codes or k_scales.shape != (nb, hkv, bs, half // 16) or v_scales.shape != k_scales.shape:
         raise ValueError("q4_0 pools: codes [NB, Hkv, bs, D/2] uint8, scales [NB, Hkv, bs, D/32] fp16")
-    return (nb, hkv, bs, 2 * half, _dev(k_codes, "k_codes", torch.uint8), _dev(k_scales, "k_scales", torch.float16),
-            _dev(v_codes, "v_codes", torch.uint8), _dev(v_scales, "v_scales", torch.float16))
+    return (nb, hkv, bs, 2 * half, _here(k_codes, "k_codes", torch.uint8, here),
+            _here(k_scales, "k_scales", torch.float16, here), _here(v_codes, "v_codes", torch.uint8, here),
+            _here(v_scales, "v_scales", torch.float16, here))
 
 
 def ns_kv_append_q4_0(k, v, slot_mapping, k_codes, k_scales, v_codes, v_scales, stream=None):
     """Quantise k/v [T, Hkv, D] to q4_0 and write codes and scales at slot_mapping [T] (int64)."""
+    here = _current()
     T, hkv, d = k.shape
-    nb, hkv2, bs, d2, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    nb, hkv2, bs, d2, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales, here)
     if v.shape != k.shape or hkv2 != hkv or d2 != d or slot_mapping.shape != (T,):
         raise ValueError("shape mismatch")
-    st = _invoke("ns_kv_append_q4_0", _dev(k, "k"), _dev(v, "v", k.dtype),
-                 _dev(slot_mapping, "slot_mapping", torch.int64), kc, ks, vc, vs, T, hkv, d,
+    st = _invoke("ns_kv_append_q4_0", _here(k, "k", k.dtype, here), _here(v, "v", k.dtype, here),
+                 _here(slot_mapping, "slot_mapping", torch.int64, here), kc, ks, vc, vs, T, hkv, d,
                  bs, nb, _dtype_code(k), _stream(stream))
     _check(st, "ns_kv_append_q4_0")
 
 
 def ns_kv_gather_q4_0(k_codes, k_scales, v_codes, v_scales, block_tables, start_loc, k_out, v_out, stream=None):
     """ns_kv_gather from a q4_0 pool: the dequantised rows, rounded to k_out's type."""
-    nb, hkv, bs, d, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    here = _current()
+    nb, hkv, bs, d, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales, here)
     S, width, T, _ = _gather_shapes(hkv, d, block_tables, start_loc, k_out, v_out)
-    st = _invoke("ns_kv_gather_q4_0", kc, ks, vc, vs, _dev(block_tables, "block_tables", torch.int32),
-                 _dev(start_loc, "start_loc", torch.int32), S, T, hkv, d, bs, _dev(k_out, "k_out"),
-                 _dev(v_out, "v_out"), _stream(stream), width, nb, _dtype_code(k_out))
+    st = _invoke("ns_kv_gather_q4_0", kc, ks, vc, vs, _here(block_tables, "block_tables", torch.int32, here),
+                 _here(start_loc, "start_loc", torch.int32, here), S, T, hkv, d, bs,
+                 _here(k_out, "k_out", k_out.dtype, here), _here(v_out, "v_out", k_out.dtype, here), _stream(stream),
+                 width, nb, _dtype_code(k_out))
     _check(st, "ns_kv_gather_q4_0")
 
 
 def ns_paged_attn_decode_q4_0(q, k_codes, k_scales, v_codes, v_scales, block_tables, context_lens, scale, out,
                               workspace, stream=None):
     """Decode attention of q [S, Hq, D] over a q4_0 pool; the workspace is alloc_workspace's."""
+    here = _current()
     rows, tables = q.shape, block_tables.shape
     S, hq, d = rows
-    nb, hkv, bs, d2, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    nb, hkv, bs, d2, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales, here)
     if d2 != d or out.shape != rows or context_lens.shape != (S,) or len(tables) != 2 or tables[0] != S:
         raise ValueError("shape mismatch")
     dtype = q.dtype
     st = _invoke("ns_paged_attn_decode_q4_0",
-                 _dev(q, "q"), kc, ks, vc, vs, _dev(block_tables, "block_tables", torch.int32),
-                 _dev(context_lens, "context_lens", torch.int32), S, hq, hkv, d, bs, float(scale),
-                 _dev(out, "out", dtype), _stream(stream), tables[1], nb, _dtype_code(q),
-                 _dev(workspace, "workspace", torch.uint8), workspace.numel())
+                 _here(q, "q", q.dtype, here), kc, ks, vc, vs, _here(block_tables, "block_tables", torch.int32, here),
+                 _here(context_lens, "context_lens", torch.int32, here), S, hq, hkv, d, bs, float(scale),
+                 _here(out, "out", dtype, here), _stream(stream), tables[1], nb, _dtype_code(q),
+                 _here(workspace, "workspace", torch.uint8, here), workspace.numel())
     _check(st, "ns_paged_attn_decode_q4_0")
 
 
@@ -581,22 +615,23 @@ def ns_paged_attn_prefill_q4_0(q, query_start_loc, k_codes, k_scales, v_codes, v
                                context_lens, scale, out, workspace, stream=None):
     """Attention of the query spans ``query_start_loc`` over a q4_0 pool (head_dim 64, block size 16); the
     workspace is alloc_span_workspace's."""
+    here = _current()
     rows, tables = q.shape, block_tables.shape
     T, hq, d = rows
-    nb, hkv, bs, d2, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    nb, hkv, bs, d2, kc, ks, vc, vs = _q4_pools(k_codes, k_scales, v_codes, v_scales, here)
     S = context_lens.shape[0]
     if d2 != d or out.shape != rows or query_start_loc.shape != (S + 1,) or len(tables) != 2 or tables[0] != S:
         raise ValueError("shape mismatch")
     st = _invoke("ns_paged_attn_prefill_q4_0",
-                 _dev(q, "q"), _dev(query_start_loc, "query_start_loc", torch.int32), kc, ks, vc, vs,
-                 _dev(block_tables, "block_tables", torch.int32), _dev(context_lens, "context_lens", torch.int32),
-                 S, T, hq, hkv, d, bs, float(scale), _dev(out, "out", q.dtype), _stream(stream), tables[1], nb,
-                 _dtype_code(q), _dev(workspace, "workspace", torch.uint8), workspace.numel())
+                 _here(q, "q", q.dtype, here), _here(query_start_loc, "query_start_loc", torch.int32, here), kc, ks, vc, vs,
+                 _here(block_tables, "block_tables", torch.int32, here), _here(context_lens, "context_lens", torch.int32, here),
+                 S, T, hq, hkv, d, bs, float(scale), _here(out, "out", q.dtype, here), _stream(stream), tables[1], nb,
+                 _dtype_code(q), _here(workspace, "workspace", torch.uint8, here), workspace.numel())
     _check(st, "ns_paged_attn_prefill_q4_0")
 
 
 def _rope_append(name, q, k, v, positions, cos_sin, slot_mapping, q_out, pools, nb, hkv, bs, d, k_out, interleaved,
-                 stream):
+                 stream, here):
     rows, keys, table = q.shape, k.shape, cos_sin.shape
     if len(rows) != 3 or rows[2] != d or keys != (rows[0], hkv, d) or v.shape != keys:
         raise ValueError("q must be [T, Hq, D], k and v [T, Hkv, D], with the pools' heads and head_dim")
@@ -608,11 +643,14 @@ def _rope_append(name, q, k, v, positions, cos_sin, slot_mapping, q_out, pools, 
         raise ValueError("positions and slot_mapping must be [T], cos_sin [max_positions, rotary_dim]")
     dtype = q.dtype
     dt = _dtype_code(q)
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", dtype, rows), _rows(k, "k", dtype, keys), _rows(v, "v", dtype, keys)
-    qo, qos = _rows(q_out, "q_out", dtype, rows)
-    ko, kos = (None, 0) if k_out is None else _rows(k_out, "k_out", dtype, keys)
-    st = _invoke(name, qp, kp, vp, _dev(positions, "positions", torch.int32), _dev(cos_sin, "cos_sin", torch.float32),
-                 _dev(slot_mapping, "slot_mapping", torch.int64), qo, ko, *pools, T, hq, hkv, d, table[1],
+    qp, qs = _rows_here(q, "q", dtype, rows, here)
+    kp, ks = _rows_here(k, "k", dtype, keys, here)
+    vp, vs = _rows_here(v, "v", dtype, keys, here)
+    qo, qos = _rows_here(q_out, "q_out", dtype, rows, here)
+    ko, kos = (None, 0) if k_out is None else _rows_here(k_out, "k_out", dtype, keys, here)
+    st = _invoke(name, qp, kp, vp, _here(positions, "positions", torch.int32, here),
+                 _here(cos_sin, "cos_sin", torch.float32, here),
+                 _here(slot_mapping, "slot_mapping", torch.int64, here), qo, ko, *pools, T, hq, hkv, d, table[1],
                  1 if interleaved else 0, table[0], qs, ks, vs, qos, kos, bs, nb, dt, _stream(stream))
     _check(st, name)
 
@@ -629,25 +667,30 @@ def ns_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, q_out, k_pool, 
     if len(pool) != 4 or v_pool.shape != pool:
         raise ValueError("k_pool and v_pool must be [NB, Hkv, bs, D]")
     nb, hkv, bs, d = pool
-    pools = (_dev(k_pool, "k_pool", q.dtype), _dev(v_pool, "v_pool", q.dtype))
+    here = _current()
+    pools = (_here(k_pool, "k_pool", q.dtype, here), _here(v_pool, "v_pool", q.dtype, here))
     _rope_append("ns_rope_kv_append", q, k, v, positions, cos_sin, slot_mapping, q_out, pools, nb, hkv, bs, d, k_out,
-                 interleaved, stream)
+                 interleaved, stream, here)
 
 
 def ns_rope_kv_append_q8_0(q, k, v, positions, cos_sin, slot_mapping, q_out, k_codes, k_scales, v_codes, v_scales,
                            k_out=None, interleaved=False, stream=None):
     """ns_rope_kv_append into a q8_0 pool."""
     nb, hkv, bs, d, *pools = _q8_pools(k_codes, k_scales, v_codes, v_scales)
+    here = _current()
+    for t, what in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales")):
+        _on_current(t, what, here)
     _rope_append("ns_rope_kv_append_q8_0", q, k, v, positions, cos_sin, slot_mapping, q_out, pools, nb, hkv, bs, d,
-                 k_out, interleaved, stream)
+                 k_out, interleaved, stream, here)
 
 
 def ns_rope_kv_append_q4_0(q, k, v, positions, cos_sin, slot_mapping, q_out, k_codes, k_scales, v_codes, v_scales,
                            k_out=None, interleaved=False, stream=None):
     """ns_rope_kv_append into a q4_0 pool."""
-    nb, hkv, bs, d, *pools = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    here = _current()
+    nb, hkv, bs, d, *pools = _q4_pools(k_codes, k_scales, v_codes, v_scales, here)
     _rope_append("ns_rope_kv_append_q4_0", q, k, v, positions, cos_sin, slot_mapping, q_out, pools, nb, hkv, bs, d,
-                 k_out, interleaved, stream)
+                 k_out, interleaved, stream, here)
 
 
 def _prob_rows(t, name, shape):

@@ -26,17 +26,15 @@ constexpr int kThreads = 128;
 // key and value rows.
 template <int D>
 constexpr int step_rows() { return 32 / (D / 8); }
-// Query steps in flight: 18 rows of 64 elements are one batch and a step (13400 tokens 15.8 us, 16.8 by
-// three); wider rows fill the GPU sooner by smaller ones (256 tokens of 32 / 8 heads 3.1 us, 3.5 by four).
-template <int D>
-constexpr int batch_steps() { return D == 64 ? 4 : 3; }
+constexpr int kBatch = 4;  // query steps in flight
+constexpr int kLeast = 2;  // steps of a warp, at least
 
 template <typename T, int D, int POOL, bool ROPE>
-__global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const RopeAppendArgs a, int parts, int part_steps)
+__global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(const RopeAppendArgs a, int parts, int part_steps)
 {
     grid_dependency_wait();
     grid_launch_dependents();
-    constexpr int C = D / 8, ROWS = step_rows<D>(), kBatch = batch_steps<D>();  // lanes of a row, rows of a step
+    constexpr int C = D / 8, ROWS = step_rows<D>();  // lanes of a row, rows of a step
     const int lane = threadIdx.x & 31, c = lane % C, sub = lane / C;
     const long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const long long t = item / parts;
@@ -215,15 +213,14 @@ cudaError_t launch_rope_append(const RopeAppendArgs &in, int pool, cudaStream_t 
     const cudaError_t e = current_sms(&sms);
     if (e != cudaSuccess)
         return e;
-    // A batch of steps is the least a warp takes; a token's batches are shared by as many
-    // warps as the GPU has room for (32 an SM), so that few tokens spread over it.
+    // A token's steps are shared by as many warps as the GPU has room for (32 an SM), so that few
+    // tokens spread over it.
     const int rows = a.head_dim == 64 ? step_rows<64>() : step_rows<128>();
-    const int batch = a.head_dim == 64 ? batch_steps<64>() : batch_steps<128>();
     const int steps = ((rope ? a.num_q_heads : 0) + rows - 1) / rows + (2 * a.num_kv_heads + rows - 1) / rows;
-    const long long batches = (steps + batch - 1) / batch;
+    const long long shares = (steps + kLeast - 1) / kLeast;
     const long long room = std::max<long long>(1, (long long)sms * 32 / a.num_tokens);
-    const int per = (int)((batches + std::min(batches, room) - 1) / std::min(batches, room));
-    int part_steps = per * batch, parts = (steps + part_steps - 1) / part_steps;
+    const int per = (int)((shares + std::min(shares, room) - 1) / std::min(shares, room));
+    int part_steps = per * kLeast, parts = (steps + part_steps - 1) / part_steps;
     const long long warps = (long long)a.num_tokens * parts, grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (grid > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;

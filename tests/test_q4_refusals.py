@@ -140,6 +140,32 @@ def test_binding_refuses_shapes_that_do_not_match():
         binding.ns_kv_append_q4_0(k, k, slots, codes, steps, cpu(4, 2, 16, 64, dtype=torch.uint8), steps)
 
 
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on GPU 7."""
+    is_cuda = True
+
+    def get_device(self):
+        return 7
+
+
+def test_binding_refuses_tensors_of_another_device(monkeypatch):
+    monkeypatch.setattr(binding, "_raw_device", lambda: 0)
+    monkeypatch.setattr(binding, "_invoke", lambda *a: pytest.fail("called"))
+    def there(*shape, dtype=torch.float16):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(Elsewhere)
+    codes, steps = there(4, 2, 16, 32, dtype=torch.uint8), there(4, 2, 16, 2)
+    q, k, slots = there(3, 14, 64), there(3, 2, 64), there(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        binding.ns_kv_append_q4_0(k, k, slots, codes, steps, codes, steps)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        binding.ns_rope_kv_append(q, k, k, there(3, dtype=torch.int32), there(9, 64, dtype=torch.float32), slots, q,
+                                  there(4, 2, 16, 64), there(4, 2, 16, 64))
+    codes8 = there(4, 2, 16, 64, dtype=torch.int8)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        binding.ns_rope_kv_append_q8_0(q, k, k, there(3, dtype=torch.int32), there(9, 64, dtype=torch.float32), slots, q,
+                                       codes8, steps, codes8, steps)
+
+
 # ---------------------------------------------------------------- order on the stream
 @pytest.mark.parametrize("name,kernel", [("rope_append.cu", "rope_append_kernel"), ("decode_q4.cu", "decode_q4_kernel"),
                                          ("kv_gather.cu", "kv_gather_kernel")])
