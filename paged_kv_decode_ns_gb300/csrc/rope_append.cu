@@ -30,15 +30,14 @@ constexpr int kBatch = 4;  // query steps in flight
 constexpr int kLeast = 2;  // steps of a warp, at least
 
 template <typename T, int D, int POOL, bool ROPE>
-__global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(const RopeAppendArgs a, int parts, int part_steps)
+__global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(const RopeAppendArgs a, int part_steps)
 {
     grid_dependency_wait();
     grid_launch_dependents();
     constexpr int C = D / 8, ROWS = step_rows<D>();  // lanes of a row, rows of a step
     const int lane = threadIdx.x & 31, c = lane % C, sub = lane / C;
-    const long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const long long t = item / parts;
-    const int part = (int)(item - t * parts);
+    const long long t = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int part = blockIdx.y;
     if (t >= a.num_tokens)
         return;
     const int hq = ROPE ? a.num_q_heads : 0, hkv = a.num_kv_heads;
@@ -119,10 +118,10 @@ __global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(const RopeAppe
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[i] = unpack2<T>(mine[i]);
-            if (turn) {  // (the packed products and sum of fp32 pairs come out contracted)
-                const float2 y = unpack2<T>(others[i]);
-                x[i].x = __fadd_rn(__fmul_rn(x[i].x, co[i].x), __fmul_rn(y.x, si[i].x));
-                x[i].y = __fadd_rn(__fmul_rn(x[i].y, co[i].y), __fmul_rn(y.y, si[i].y));
+            if (turn) {  // (with the sum of pairs too they come out contracted)
+                const float2 y = fmul2(unpack2<T>(others[i]), si[i]);
+                x[i] = fmul2(x[i], co[i]);
+                x[i] = make_float2(__fadd_rn(x[i].x, y.x), __fadd_rn(x[i].y, y.y));
             }
         }
     };
@@ -220,12 +219,12 @@ cudaError_t launch_rope_append(const RopeAppendArgs &in, int pool, cudaStream_t 
     const long long shares = (steps + kLeast - 1) / kLeast;
     const long long room = std::max<long long>(1, (long long)sms * 32 / a.num_tokens);
     const int per = (int)((shares + std::min(shares, room) - 1) / std::min(shares, room));
-    int part_steps = per * kLeast, parts = (steps + part_steps - 1) / part_steps;
-    const long long warps = (long long)a.num_tokens * parts, grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    if (grid > 0x7fffffffLL)
+    int part_steps = per * kLeast;
+    const int parts = (steps + part_steps - 1) / part_steps;
+    if (parts > 65535)
         return cudaErrorInvalidConfiguration;
-    void *args[] = {&a, &parts, &part_steps};
-    return launch_early(kern, dim3((unsigned)grid), kThreads, 0, stream, args);
+    void *args[] = {&a, &part_steps};
+    return launch_early(kern, dim3((unsigned)((a.num_tokens - 1) / (kThreads / 32) + 1), (unsigned)parts), kThreads, 0, stream, args);
 }
 
 }  // namespace ns
