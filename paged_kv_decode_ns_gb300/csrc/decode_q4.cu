@@ -18,7 +18,7 @@
 // of the largest weight times the largest step so far).
 //
 // Work.  The pairs (sequence, kv head, 8 query heads) lie end to end on a line, in chunks of
-// 32 tokens and one more for a pair's own cost, and each warp of a persistent grid takes an
+// 32 tokens and two more for a pair's own cost, and each warp of a persistent grid takes an
 // equal run of it.  A pair cut by warps of one CTA is joined in shared memory, one cut by
 // CTAs through records in the workspace, by the CTA that arrives last; in the order of the
 // keys, so results do not depend on timing.
@@ -34,8 +34,8 @@ namespace ns {
 namespace {
 
 constexpr int kChunk = 32;     // tokens of a step: one a lane
-constexpr int kPairCost = 1;   // chunks that a pair counts besides its own
-constexpr int kWarpJoin = 8;   // CTAs' records that a warp joins by itself
+constexpr int kPairCost = 2;   // chunks that a pair counts besides its own (batch 256 21.9 us; 0: 23.7, 1 and 3: 22.4)
+constexpr int kWarpJoin = 2;   // CTAs' records that a warp joins by itself (16: 8 x 4096 tokens 10.7 us, 8.9)
 constexpr float kNone = -3.402823466e38f;
 // m is set so that the largest w dv is just below 2^kLift, and moves when one would pass
 // that by 2^kSlack: fp16 has room up to 2^16 and steps of 2^-24.
@@ -374,9 +374,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
     }
     total *= P.heads;
     // Runs: the first `rest` of `runs` warps take share + 1 chunks, the others share.  What one CTA
-    // can do with two chunks a warp stays in one (four short sequences 6.4 us, 7.6 by single chunks
-    // in two CTAs; 8 x 4096 tokens the other way round 10.0 and 9.2).
-    const int runs = min((int)gridDim.x * W, total <= 2 * W ? (total + 1) / 2 : total);
+    // can do with three chunks a warp stays in one (four short sequences 6.4 us, 7.2 by single chunks
+    // in three CTAs; 8 x 4096 tokens by two chunks 10.0, by one 9.0).
+    const int runs = min((int)gridDim.x * W, total <= 3 * W ? min(W, (total + 1) / 2) : total);
     const int share = quotient(total, runs), rest = total - share * runs;
     const int me = blockIdx.x * W + warp;
     if ((int)blockIdx.x * W >= runs)
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
     };
 
     look_up();
-#pragma unroll
+#pragma unroll 1  // (less code to fetch: batch 256 22.6 -> 22.3 us)
     for (int i = 0; i < ST - 1; ++i)
         issue();
 
