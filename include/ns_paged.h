@@ -697,7 +697,7 @@ ns_status ns_paged_attn_prefill_q4_0(const void *q, const int32_t *query_start_l
  * fp32 each, then
  *   q_out[t], k_out[t] and the 16-bit pool's row: once to dtype
  *   q8_0, q4_0 pools: codes and scales of the fp32 values, bit for bit
- * A negative slot marks a padding token: nothing of it is read or written.  A
+ * A negative slot marks a padding token: nothing is written for it.  A
  * token whose slot lies outside the pool (NS_DEV_BAD_SLOT) or whose position lies
  * outside [0, max_positions) (NS_DEV_BAD_POSITION) is skipped in the same way.  Two
  * tokens with the same slot race (one of them wins, row by row).

@@ -35,7 +35,6 @@ namespace {
 
 constexpr int kChunk = 32;     // tokens of a step: one a lane
 constexpr int kPairCost = 2;   // chunks that a pair counts besides its own (batch 256 21.9 us; 0: 23.7, 1 and 3: 22.4)
-constexpr int kWarpJoin = 2;   // CTAs' records that a warp joins by itself (16: 8 x 4096 tokens 10.7 us, 8.9)
 constexpr float kNone = -3.402823466e38f;
 // m is set so that the largest w dv is just below 2^kLift, and moves when one would pass
 // that by 2^kSlack: fp16 has room up to 2^16 and steps of 2^-24.
@@ -96,25 +95,20 @@ __device__ __forceinline__ void copies_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Four 8 x 8 matrices of 16-bit elements.  Without a memory clobber, so that the compiler is free
-// to place them among the arithmetic; their addresses come from read_behind, so not above it.
+// Four 8 x 8 matrices of 16-bit elements.
 __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr)
 {
-    asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-        : "r"(addr));
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
 __device__ __forceinline__ void load_matrices_turned(uint32_t (&r)[4], uint32_t addr)
 {
-    asm("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-        : "r"(addr));
-}
-// What is read through this address is read behind this point.
-__device__ __forceinline__ uint32_t read_behind(uint32_t addr)
-{
-    asm volatile("" : "+r"(addr)::"memory");
-    return addr;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t turn_matrix(uint32_t x)
 {
@@ -216,102 +210,97 @@ __device__ __forceinline__ Piece next_piece(const Params &P, Walk &w)
 }
 
 // ---------------------------------------------------------------------------
-// Records of a pair's parts, joined by a warp: lane i has float4s i, i + 32, .. of O, and the
-// reference and the sum of head i % 8.
+// A pair's parts, joined by a warp: lane i has float4s i, i + 32, .. of O, with the reference and
+// the sum of their heads.  Loops of little code, since every warp runs them once and has to
+// fetch it (batch 256 21.4 us; unrolled over all 16 records 21.8, not at all 21.8).
 template <int D>
 struct Joined {
-    static constexpr int F = D / 16;
+    static constexpr int F = D / 16, PER = D / 4;  // float4s of a lane, of a head
     float4 acc[F];
-    float top, sum;
+    float top[F], sum[F];
 
-    // n <= MOST records in the order of the keys; GLOBAL: they were written by other CTAs
-    template <int MOST, bool GLOBAL, typename Record>
+    // n records of this CTA, in the order of the keys
+    template <typename Record>
     __device__ __forceinline__ void join(int n, int lane, const Record &record)
     {
-        constexpr int K = (MOST + 3) / 4, B = GLOBAL ? 16 / F : 4;  // records whose loads fly together
-        const int x = lane >> 3, h = lane & 7;
-        float m[K], l[K];
-        top = kNone;
-        sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const bool on = 4 * k + x < n;
-            const float *r = record(on ? 4 * k + x : 0);
-            m[k] = on ? (GLOBAL ? __ldcg(r + h) : r[h]) : kNone;
-            l[k] = on ? (GLOBAL ? __ldcg(r + 8 + h) : r[8 + h]) : 0.f;
-        }
-        float4 y[B][F];
-        auto load = [&](int i0) {
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const float4 *r = reinterpret_cast<const float4 *>(record(min(i0 + b, n - 1)) + 16) + lane;
-#pragma unroll
-                for (int f = 0; f < F; ++f)
-                    y[b][f] = GLOBAL ? __ldcg(r + 32 * f) : r[32 * f];
-            }
-        };
-        load(0);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            top = fmaxf(top, m[k]);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            m[k] = 4 * k + x < n ? fast_exp2(m[k] - top) : 0.f;
-            sum = fmaf(m[k], l[k], sum);
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-#pragma unroll
-        for (int f = 0; f < F; ++f)
+        for (int f = 0; f < F; ++f) {
             acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+            top[f] = kNone;
+            sum[f] = 0.f;
+        }
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float *r = record(i);
 #pragma unroll
-        for (int i0 = 0; i0 < MOST; i0 += B) {
-            if (i0 > 0) {
-                if (i0 >= n)
-                    break;
-                load(i0);
+            for (int f = 0; f < F; ++f)
+                top[f] = fmaxf(top[f], r[(32 * f + lane) / PER]);
+        }
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float *r = record(i);
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const int at = 32 * f + lane, h = at / PER;
+                const float c = fast_exp2(r[h] - top[f]);
+                const float4 y = reinterpret_cast<const float4 *>(r + 16)[at];
+                sum[f] = fmaf(c, r[8 + h], sum[f]);
+                acc[f].x = fmaf(c, y.x, acc[f].x), acc[f].y = fmaf(c, y.y, acc[f].y);
+                acc[f].z = fmaf(c, y.z, acc[f].z), acc[f].w = fmaf(c, y.w, acc[f].w);
             }
+        }
+    }
+
+    // A record of another CTA.
+    __device__ __forceinline__ void load(const float *rec, int lane)
+    {
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int i = i0 + b;
-                if (i >= MOST || i >= n)
-                    break;
+        for (int f = 0; f < F; ++f) {
+            const int at = 32 * f + lane;
+            top[f] = __ldcg(rec + at / PER);
+            sum[f] = __ldcg(rec + 8 + at / PER);
+            acc[f] = __ldcg(reinterpret_cast<const float4 *>(rec + 16) + at);
+        }
+    }
+
+    // The part behind this one in the order of the keys.
+    __device__ __forceinline__ void add(const Joined &next)
+    {
 #pragma unroll
-                for (int f = 0; f < F; ++f) {
-                    const float c = __shfl_sync(0xffffffffu, m[i / 4], 8 * (i % 4) + (32 * f + lane) / (D / 4));
-                    acc[f].x = fmaf(c, y[b][f].x, acc[f].x), acc[f].y = fmaf(c, y[b][f].y, acc[f].y);
-                    acc[f].z = fmaf(c, y[b][f].z, acc[f].z), acc[f].w = fmaf(c, y[b][f].w, acc[f].w);
-                }
-            }
+        for (int f = 0; f < F; ++f) {
+            const float higher = fmaxf(top[f], next.top[f]);
+            const float a = fast_exp2(top[f] - higher), b = fast_exp2(next.top[f] - higher);
+            top[f] = higher;
+            sum[f] = fmaf(b, next.sum[f], a * sum[f]);
+            acc[f].x = fmaf(b, next.acc[f].x, a * acc[f].x), acc[f].y = fmaf(b, next.acc[f].y, a * acc[f].y);
+            acc[f].z = fmaf(b, next.acc[f].z, a * acc[f].z), acc[f].w = fmaf(b, next.acc[f].w, a * acc[f].w);
         }
     }
 
     __device__ __forceinline__ void keep(float *rec, int lane) const
     {
-        if (lane < 8) {
-            rec[lane] = top;
-            rec[8 + lane] = sum;
-        }
 #pragma unroll
-        for (int f = 0; f < F; ++f)
-            reinterpret_cast<float4 *>(rec + 16)[32 * f + lane] = acc[f];
+        for (int f = 0; f < F; ++f) {
+            const int at = 32 * f + lane;
+            if (at % PER == 0) {
+                rec[at / PER] = top[f];
+                rec[8 + at / PER] = sum[f];
+            }
+            reinterpret_cast<float4 *>(rec + 16)[at] = acc[f];
+        }
     }
 
     template <typename T>
     __device__ __forceinline__ void put(const Params &P, int pair, int lane) const
     {
         const int s = pair / P.heads, ph = pair - s * P.heads, kv = ph / P.subs, sub = ph - kv * P.subs;
-        const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+        uint8_t *row = static_cast<uint8_t *>(P.a.out) + ((long long)s * P.a.num_q_heads + kv * P.group + sub * 8) * (D * 2);
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-            const int h = (32 * f + lane) / (D / 4);
-            const float c = __shfl_sync(0xffffffffu, inv, h);
-            if (h < P.group - sub * 8)
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(P.a.out) +
-                                           (((long long)s * P.a.num_q_heads + kv * P.group + sub * 8 + h) * D + lane % (D / 4) * 4) * 2) =
-                    make_uint2(pack2<T>(acc[f].x * c, acc[f].y * c), pack2<T>(acc[f].z * c, acc[f].w * c));
+            const int at = 32 * f + lane;
+            const float c = sum[f] == 0.f ? 0.f : __fdividef(1.f, sum[f]);
+            if (at / PER < P.group - sub * 8)
+                reinterpret_cast<uint2 *>(row)[at] = make_uint2(pack2<T>(acc[f].x * c, acc[f].y * c), pack2<T>(acc[f].z * c, acc[f].w * c));
         }
     }
 };
@@ -586,7 +575,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
             __syncwarp();
             const uint32_t live = in_flight[0];
             issue();  // into the stage that the last turn has read
-            const uint32_t from = read_behind(ring + used * GG::STAGE);
+            const uint32_t from = ring + used * GG::STAGE;
             const uint8_t *stage = sm.ring[warp][used];
             used = used + 1 == ST ? 0 : used + 1;
 
@@ -791,32 +780,35 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
     const bool goes_on = opener >= 0 && (enders >> (opener + 1)) == 0u;
     const uint32_t chains = open << 1 | (from_before ? 1u : 0u);  // bit w + 1: chain w
     const int chain = warp - 1;
-    // the pair's CTAs have each counted themselves when the last of them does
-    auto arrive_last = [&](int slot, int pair) {
-        __threadfence();
+    auto of_cta = [&](int slot, int i) {  // record i of a pair of several CTAs
+        const int c0 = sm.first_cta[slot];
+        return P.record(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i), GG::RECORD);
+    };
+    // This CTA's record of the pair is written.  Each CTA counts itself, and the last to do so joins
+    // them: a warp two of them, more the whole CTA.
+    auto finish = [&](int slot, int pair) {
+        const int n = sm.pieces[slot];
         __syncwarp();
         int last = 0;
-        if (lane == 0) {
-            last = atomicAdd(P.counters + pair, 1) == sm.pieces[slot] - 1;
+        if (lane == 0) {  // what the warp wrote is out before its count, what others wrote is read behind theirs
+            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(last) : "l"(P.counters + pair) : "memory");
+            last = last == n - 1;
             if (last)
                 P.counters[pair] = 0;
-            __threadfence();
         }
         last = __shfl_sync(0xffffffffu, last, 0);
         __syncwarp();
-        return last != 0;
-    };
-    auto finish = [&](int slot, int pair) {  // this CTA's record of the pair is written
-        if (!arrive_last(slot, pair))
+        if (!last)
             return;
-        const int n = sm.pieces[slot], c0 = sm.first_cta[slot];
-        if (n > kWarpJoin) {
+        if (n > 2) {
             if (lane == 0)
                 sm.to_join[slot] = pair;
             return;
         }
-        Joined<D> r;
-        r.template join<kWarpJoin, true>(n, lane, [&](int i) { return P.record(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i), GG::RECORD); });
+        Joined<D> r, behind;
+        r.load(of_cta(slot, 0), lane);
+        behind.load(of_cta(slot, 1), lane);
+        r.add(behind);
         r.template put<T>(P, pair, lane);
     };
     if ((chains >> warp) & 1u) {
@@ -825,7 +817,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
         const bool ends = behind != 0u;
         const int n = (ends ? __ffs(behind) - 1 : W - 1) - chain + (chain < 0 ? 0 : 1);
         Joined<D> r;
-        r.template join<W, false>(n, lane, [&](int i) -> const float * {
+        r.join(n, lane, [&](int i) -> const float * {
             return chain < 0 ? sm.first[i] : i == 0 ? reinterpret_cast<const float *>(sm.ring[chain][0]) : sm.first[chain + i];
         });
         if (chain >= 0 && ends) {
@@ -840,7 +832,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
     const uint32_t idle = ~chains & ((1u << W) - 1u);
     if (opener == W - 1 && warp == (idle != 0u ? __ffs(idle) - 1 : W - 1))
         finish(1, sm.last_pair[W - 1]);
-    if (!(from_before && sm.pieces[0] > kWarpJoin) && !(goes_on && sm.pieces[1] > kWarpJoin))
+    if (!(from_before && sm.pieces[0] > 2) && !(goes_on && sm.pieces[1] > 2))
         return;
 
     // ---- pairs of more CTAs: the whole CTA joins them
