@@ -29,11 +29,13 @@ constexpr int step_rows() { return 32 / (D / 8); }
 constexpr int kBatch = 4;  // query steps in flight
 constexpr int kLeast = 2;  // steps of a warp, at least
 
-template <typename T, int D, int POOL, bool ROPE>
+// TURN: 0 no rotation, 1 pairs of halves, 2 neighbours.
+template <typename T, int D, int POOL, int TURN>
 __global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(const RopeAppendArgs a, int part_steps)
 {
     grid_dependency_wait();
     grid_launch_dependents();
+    constexpr bool ROPE = TURN != 0, pairs = TURN == 2;
     constexpr int C = D / 8, ROWS = step_rows<D>();  // lanes of a row, rows of a step
     const int lane = threadIdx.x & 31, c = lane % C, sub = lane / C;
     const long long t = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -81,7 +83,6 @@ __global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(const RopeAppe
     float2 co[4], si[4];
     const int half = a.rotary_dim / 2, hc = half / 8;  // elements, lanes (halves)
     const bool turned = ROPE && c < 2 * hc;
-    const bool pairs = ROPE && a.interleaved;
     int other = lane;
     if (turned) {
         const float *row = a.cos_sin + (long long)pos * a.rotary_dim;
@@ -190,14 +191,21 @@ __global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(const RopeAppe
     }
 }
 
-template <typename T, int D>
-const void *kernel_of(int pool, bool rope)
+template <typename T, int D, int TURN>
+const void *kernel_of(int pool)
 {
-    if (pool == 16)
-        return (const void *)rope_append_kernel<T, D, 16, true>;
-    if (pool == 4)
-        return rope ? (const void *)rope_append_kernel<T, D, 4, true> : (const void *)rope_append_kernel<T, D, 4, false>;
-    return D == 64 ? (const void *)rope_append_kernel<T, 64, 8, true> : nullptr;
+    if constexpr (TURN == 0)
+        return (const void *)rope_append_kernel<T, D, 4, 0>;
+    else if (pool == 8)
+        return D == 64 ? (const void *)rope_append_kernel<T, 64, 8, TURN> : nullptr;
+    else
+        return pool == 16 ? (const void *)rope_append_kernel<T, D, 16, TURN> : (const void *)rope_append_kernel<T, D, 4, TURN>;
+}
+
+template <typename T, int D>
+const void *kernel_of(int pool, int turn)
+{
+    return turn == 0 ? kernel_of<T, D, 0>(pool) : turn == 1 ? kernel_of<T, D, 1>(pool) : kernel_of<T, D, 2>(pool);
 }
 
 }  // namespace
@@ -206,8 +214,9 @@ cudaError_t launch_rope_append(const RopeAppendArgs &in, int pool, cudaStream_t 
 {
     RopeAppendArgs a = in;
     const bool rope = a.positions != nullptr;
-    const void *kern = a.dtype == NS_BF16 ? (a.head_dim == 64 ? kernel_of<BF16, 64>(pool, rope) : kernel_of<BF16, 128>(pool, rope))
-                                          : (a.head_dim == 64 ? kernel_of<F16, 64>(pool, rope) : kernel_of<F16, 128>(pool, rope));
+    const int turn = !rope ? 0 : a.interleaved ? 2 : 1;
+    const void *kern = a.dtype == NS_BF16 ? (a.head_dim == 64 ? kernel_of<BF16, 64>(pool, turn) : kernel_of<BF16, 128>(pool, turn))
+                                          : (a.head_dim == 64 ? kernel_of<F16, 64>(pool, turn) : kernel_of<F16, 128>(pool, turn));
     int sms = 0;
     const cudaError_t e = current_sms(&sms);
     if (e != cudaSuccess)
