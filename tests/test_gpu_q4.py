@@ -1,4 +1,8 @@
 """The q4_0 cache on the GPU: append bit for bit, read-back, decode and span attention against fp64."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -140,6 +144,11 @@ def test_decode_splits_and_batches(lens):
 @pytest.mark.parametrize("lens", [[12000], [3000, 2500, 10, 4000], [130] * 400])
 def test_decode_splits_head_dim_128(lens):
     check_decode(4, lens, 8, 2, 128, wl.BF16)
+
+
+@pytest.mark.parametrize("d,hq,hkv,length", [(64, 2, 1, 300001), (128, 9, 1, 100003)])
+def test_decode_one_pair_across_every_cta(d, hq, hkv, length):
+    check_decode(6, [length], hq, hkv, d, wl.F16)
 
 
 @pytest.mark.parametrize("amp", [1e-4, 30.0, 3000.0])
@@ -285,6 +294,37 @@ def test_decode_captured_replayed_and_on_another_stream():
     call(stream=side)
     side.synchronize()
     assert _q4.same_bits(out, want) and _q4.status() == 0
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [%r, %r]
+import numpy as np, torch
+import _gpu, _q4
+from paged_kv_decode_ns_gb300 import binding as nb
+rng = np.random.default_rng(1)
+cache = _q4.Cache(rng, [300, 5], 2, 16, 128)
+q = _q4.to16(rng.standard_normal((2, 14, 128)).astype(np.float32), _q4.wl.F16)
+kc, ks, vc, vs, bt = cache.dev()
+qd, cl, ws = q.cuda(), _gpu.dev_ints([300, 5], np.int32), nb.alloc_workspace(2, 14, 2, 128)
+out, rows = torch.zeros_like(qd), [torch.zeros(305, 2, 128, dtype=qd.dtype, device="cuda") for _ in range(2)]
+start = _gpu.dev_ints([0, 300, 305], np.int32)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    nb.ns_paged_attn_decode_q4_0(qd, kc, ks, vc, vs, bt, cl, 0.1, out, ws)
+    nb.ns_kv_gather_q4_0(kc, ks, vc, vs, bt, start, *rows)
+graph.replay()
+torch.cuda.synchronize()
+_q4.compare(out, _q4.attend_all(q, [(1, 300), (1, 5)], cache, 0.1).numpy(), _q4.wl.F16)
+assert np.array_equal(_gpu.to_f64(rows[0]), torch.cat(cache.k).numpy().astype(np.float16).astype(np.float64))
+print("captured")
+"""
+
+
+def test_the_first_calls_of_a_process_are_captured():
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL % (here, os.path.dirname(here))], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------- spans
