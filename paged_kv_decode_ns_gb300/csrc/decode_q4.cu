@@ -522,24 +522,17 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // the row's largest goes to [2^14, 2^15); the factor stays a normal number
             const int e = top > 0.f && top < INFINITY ? min(max(141 - (int)(__float_as_uint(top) >> 23), -113), 113) : 0;
-            const float f = __uint_as_float((uint32_t)(127 + e) << 23);
+            const float f = P.sign * __uint_as_float((uint32_t)(127 + e) << 23), f_high = f * 0.0625f;
             q_unit = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const uint32_t x[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 y = unpack2<T>(x[i]);
-                    v[2 * i] = y.x * (f * P.sign);
-                    v[2 * i + 1] = y.y * (f * P.sign);
-                }
                 // elements i and i + 4, less four binary places where the code is that much higher
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float less = i & 1 ? 0.0625f : 1.f;
-                    q[r][i] = pack2<F16>(v[i] * less, v[i + 4] * less);
+                    const float2 a0 = unpack2<T>(x[i >> 1]), a1 = unpack2<T>(x[(i >> 1) + 2]);
+                    q[r][i] = i & 1 ? pack2<F16>(a0.y * f_high, a1.y * f_high) : pack2<F16>(a0.x * f, a1.x * f);
                     const float2 y = halves(q[r][i]);
                     sum = fmaf(y.x + y.y, i & 1 ? 16.f : 1.f, sum);
                 }
