@@ -669,9 +669,8 @@ ns_status ns_paged_attn_decode_q4_0(const void *q, const void *k_codes, const vo
 
 /*
  * ns_paged_attn_prefill_q4_0 -- ns_paged_attn_prefill_q8_0 over a q4_0 pool, with
- * the same shapes (head_dim 64, block_size 16), checks and workspace.  (At head_dim
- * 128 the cached rows come back through ns_kv_gather_q4_0, and ns_prompt_attn
- * takes them as the prefix.)  Scales far below the largest of the sequence and kv
+ * the same block size (16), checks and workspace (ns_span_attn_workspace_bytes of
+ * the head_dim), at head_dim 64 and 128.  Scales far below the largest of the sequence and kv
  * head lose bits as there (their values are off by up to 2^-32 of the largest value).
  */
 ns_status ns_paged_attn_prefill_q4_0(const void *q, const int32_t *query_start_loc, const void *k_codes,

@@ -613,8 +613,8 @@ def ns_paged_attn_decode_q4_0(q, k_codes, k_scales, v_codes, v_scales, block_tab
 
 def ns_paged_attn_prefill_q4_0(q, query_start_loc, k_codes, k_scales, v_codes, v_scales, block_tables,
                                context_lens, scale, out, workspace, stream=None):
-    """Attention of the query spans ``query_start_loc`` over a q4_0 pool (head_dim 64, block size 16); the
-    workspace is alloc_span_workspace's."""
+    """Attention of the query spans ``query_start_loc`` over a q4_0 pool (head_dim 64 or 128, block size 16);
+    the workspace is alloc_span_workspace's for that head_dim."""
     here = _current()
     rows, tables = q.shape, block_tables.shape
     T, hq, d = rows

@@ -76,7 +76,7 @@ ns_status prefill_paged(const void *q, const int32_t *query_start_loc, const voi
     const ns_status s = check_heads(num_q_heads, num_kv_heads, dtype);
     if (s != NS_OK)
         return s;
-    if (block_size != 16 || head_dim != 64)
+    if (block_size != 16 || (head_dim != 64 && (pool != 4 || head_dim != 128)))
         return NS_ERR_UNSUPPORTED;
     if (max_blocks_per_seq < 1 || num_blocks < 1 || !std::isfinite(scale))
         return NS_ERR_INVALID_ARG;

@@ -44,7 +44,7 @@ cudaError_t launch_span_attn(const SpanAttnArgs &a, int pool, cudaStream_t strea
     P.headers = static_cast<span::Header *>(a.workspace);
     P.records = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + span::header_bytes());
     span::Maps tm = {};
-    if (span::q_by_tma(a.head_dim, a.dtype == NS_BF16)) {
+    if (span::q_by_tma(a.head_dim, a.dtype == NS_BF16, pool != 0)) {
         // Q: [token][head][element], boxes of a group's heads of a query tile's tokens
         const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.total_q_tokens};
         const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)a.q_row_stride * 2};
@@ -69,8 +69,10 @@ cudaError_t launch_span_attn(const SpanAttnArgs &a, int pool, cudaStream_t strea
     }
     const int ctas = std::min(sms, span::kMaxCtas);
     const bool bf16 = a.dtype == NS_BF16;
-    if (pool != 0)
-        return pool == 4 ? launch_span_q4(bf16, tm, P, ctas, stream) : launch_span_q8(bf16, tm, P, ctas, stream);
+    if (pool == 8)
+        return launch_span_q8(bf16, tm, P, ctas, stream);
+    if (pool == 4)
+        return a.head_dim == 64 ? launch_span_q4(bf16, tm, P, ctas, stream) : launch_span_q4_d128(bf16, tm, P, ctas, stream);
     return a.head_dim == 64 ? launch_span_d64(bf16, tm, P, ctas, stream)
                             : launch_span_d128(bf16, tm, P, ctas, stream);
 }

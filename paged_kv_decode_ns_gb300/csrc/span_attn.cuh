@@ -21,7 +21,7 @@
 //   8-11      conversion: K and V tiles into the form that the products take;
 //   12        producer: TMA copies of K and V tiles;
 //   13, 14    issue S = Q K^T and O += P V of query tile 0 and 1;
-//   15        walks the CTA's run of units, and copies their Q (fp16, or head_dim 128).
+//   15        walks the CTA's run of units, and copies their Q (fp16, or head_dim 128 over packed rows).
 // The two tiles' softmax and products alternate by themselves: while one tile's
 // scores are exponentiated, the other's products run.
 //
@@ -89,9 +89,10 @@ constexpr int kLeast = 54; // and not below this field: a sum times 2^84 stays i
 template <int D, int POOL>
 struct Geo {
     static constexpr bool PAGED = POOL != 0;
-    static constexpr int CODES = POOL == 4 ? 32 : 64;  // bytes of a key's codes (head_dim 64)
+    static constexpr int CODES = POOL == 4 ? 32 : 64;  // bytes of a key's codes, of 64 elements
     static constexpr int KT = D == 64 ? 128 : 64;  // keys of a tile
     static constexpr int REG = D / 64;             // panels of a row
+    static constexpr int ROW = REG * CODES, STEPS = REG * 4;  // bytes of a key's codes, of its scales
     static constexpr int TILE = REG * KT * kPanel; // bytes of a K or V tile
     static constexpr int GROUP = KT / 4;           // keys of a conversion warp
     static constexpr int STAGES = PAGED ? 3 : 4;
@@ -115,7 +116,8 @@ struct Geo {
 // 134.8 against 134.2; bf16 at 64, packed 81.0 against 77.0, four short ones 10.7 against
 // 10.4, 8192 tokens 146.7 against 149.1: many units gain there from the threads, since the
 // two query tiles' softmax bounds the call and the later Q of one keeps them out of step.
-constexpr bool q_by_tma(int D, bool bf16) { return D == 128 || !bf16; }
+// (bf16 queries over 8- or 4-bit keys become fp16 on the way.)
+constexpr bool q_by_tma(int D, bool bf16, bool paged) { return paged ? !bf16 : D == 128 || !bf16; }
 
 // A CTA's part of a unit: key tiles [t0, t1).
 struct Unit {
@@ -156,7 +158,7 @@ struct alignas(1024) Smem {
     uint8_t q[2][GG::REG * kRows * kPanel];
     uint8_t k[GG::STAGES][GG::TILE];
     uint8_t v[GG::STAGES][GG::TILE];
-    uint8_t raw[GG::RAW][GG::PAGED ? 2 * GG::KT * GG::CODES + 2 * GG::KT * 4 : 16];  // codes of K, of V, scales of K, of V
+    uint8_t raw[GG::RAW][GG::PAGED ? 2 * GG::KT * (GG::ROW + GG::STEPS) : 16];  // codes of K, of V, scales of K, of V
     uint64_t raw_full[GG::RAW], raw_empty[GG::RAW];
     uint64_t v_full[GG::STAGES];
     uint64_t k_ready[GG::STAGES], v_ready[GG::STAGES], k_empty[GG::STAGES], v_empty[GG::STAGES];
@@ -394,15 +396,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using GG = Geo<D, POOL>;
     constexpr bool PAGED = GG::PAGED;
-    constexpr int KT = GG::KT, REG = GG::REG, ST = GG::STAGES, CODES = GG::CODES;
+    constexpr int KT = GG::KT, REG = GG::REG, ST = GG::STAGES, CODES = GG::CODES, ROW = GG::ROW, STEPS = GG::STEPS;
     constexpr bool BF = T::code == NS_BF16;
     constexpr bool SCALED = PAGED || BF;  // V tiles carry an exponent
     // The softmax reads that exponent with the scores, which then wait for the tile's V, or
     // only before it touches O.  The second is faster at head_dim 128, where the conversion
     // is behind (8192 bf16 tokens 480 us against 488, packed prompts 209 against 214), the
     // first at 64 (149 against 150, packed 76.9 against 77.1; drafts over q8_0 18.5 against 19.2).
-    constexpr bool LATE = BF && D == 128;
-    constexpr bool Q_TMA = q_by_tma(D, BF);
+    constexpr bool LATE = BF && D == 128 && !PAGED;
+    constexpr bool Q_TMA = q_by_tma(D, BF, PAGED);
     extern __shared__ unsigned char smem_raw[];
     Smem<D, POOL> &sm = *reinterpret_cast<Smem<D, POOL> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -644,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < KT; ++c)
                         sv[c] = c <= lim ? sv[c] : -INFINITY;
                 }
-                if (PAGED && (loaded & 0xffu) != 0xffu) {  // blocks that are not in the pool count for nothing
+                constexpr uint32_t all_blocks = (1u << (KT / 16)) - 1u;
+                if (PAGED && (loaded & all_blocks) != all_blocks) {  // blocks that are not in the pool count for nothing
 #pragma unroll
                     for (int c = 0; c < KT; ++c)
                         sv[c] = (loaded >> (c / 16)) & 1u ? sv[c] : -INFINITY;
@@ -844,12 +847,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint8_t *raw = sm.raw[rs];
                     const uint32_t loaded = sm.raw_loaded[rs];
                     const bool have = live && ((loaded >> (key / 16)) & 1u);
-                    const uint32_t *scales = reinterpret_cast<const uint32_t *>(raw + 2 * KT * CODES);
-                    const uint32_t d[2] = {have ? scales[key] : 0u, have ? scales[KT + key] : 0u};
-                    // the tile's largest scale of V, four keys a lane (those that are there)
-                    const int key4 = 4 * lane;
-                    const int there = (loaded >> (key4 / 16)) & 1u ? u.L - j * KT - key4 : 0;
-                    uint4 w4 = lds128(scales + KT + key4);
+                    const uint32_t *scales = reinterpret_cast<const uint32_t *>(raw + 2 * KT * ROW);  // pairs, of a panel
+                    const int pair = key * REG + pan;
+                    const uint32_t d[2] = {have ? scales[pair] : 0u, have ? scales[KT * REG + pair] : 0u};
+                    // the tile's largest scale of V, four pairs a lane (those that are there)
+                    const int pair4 = 4 * lane;
+                    const int there = (loaded >> (pair4 / REG / 16)) & 1u ? (u.L - j * KT) * REG - pair4 : 0;
+                    uint4 w4 = lds128(scales + KT * REG + pair4);
                     if (there < 4) {
                         w4.w = 0u;
                         w4.z = there > 2 ? w4.z : 0u;
@@ -867,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int c = 0; c < CHUNKS; ++c)
-                            code[x][c] = lds128(raw + x * KT * CODES + key * CODES + ((c ^ first) << 4));
+                            code[x][c] = lds128(raw + x * KT * ROW + pair * CODES + ((c ^ first) << 4));
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         // the largest scale of these keys' K goes just below 2^8 (4 bits: 2^12), its
@@ -947,9 +951,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                     } else {
-                        // lane i: block i / 4 of the tile, its codes of K, of V, scales of K, of V
+                        // lane i: block i / 4 of the tile (if it has as many), its codes of K, of V, scales of K, of V
                         const int rs = tile % GG::RAW;
-                        const int b = lane >> 2, what = lane & 3, blk = j * (KT / 16) + b;
+                        const int b = lane >> 2, what = lane & 3, blk = b < KT / 16 ? j * (KT / 16) + b : blocks;
                         int phys = -1;
                         if (blk < blocks) {
                             phys = a.block_tables[(long long)u.s * a.max_blocks_per_seq + blk];
@@ -969,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     mask |= ((fine >> (4 * i)) & 1u) << i;
                                 sm.raw_loaded[rs] = mask;
                                 mbar_arrive_expect_tx(&sm.raw_full[rs],
-                                                      (uint32_t)(__popc(have) / 4) * 2u * (16u * CODES + 16u * 4u));
+                                                      (uint32_t)(__popc(have) / 4) * 2u * 16u * (ROW + STEPS));
                             }
                         }
                         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -977,13 +981,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const long long row = ((long long)phys * a.num_kv_heads + u.h) * 16;
                             uint8_t *raw = sm.raw[rs];
                             if (what < 2)
-                                bulk_load(raw + what * KT * CODES + b * 16 * CODES,
-                                          static_cast<const uint8_t *>(what == 0 ? a.k_codes : a.v_codes) + row * CODES,
-                                          16u * CODES, &sm.raw_full[rs]);
+                                bulk_load(raw + what * KT * ROW + b * 16 * ROW,
+                                          static_cast<const uint8_t *>(what == 0 ? a.k_codes : a.v_codes) + row * ROW,
+                                          16u * ROW, &sm.raw_full[rs]);
                             else
-                                bulk_load(raw + 2 * KT * CODES + (what - 2) * KT * 4 + b * 64,
-                                          static_cast<const uint8_t *>(what == 2 ? a.k_scales : a.v_scales) + row * 4, 64u,
-                                          &sm.raw_full[rs]);
+                                bulk_load(raw + 2 * KT * ROW + (what - 2) * KT * STEPS + b * 16 * STEPS,
+                                          static_cast<const uint8_t *>(what == 2 ? a.k_scales : a.v_scales) + row * STEPS,
+                                          16u * STEPS, &sm.raw_full[rs]);
                         }
                     }
                 }
@@ -1355,6 +1359,7 @@ cudaError_t launch(const Maps &tm, const Params &P, int ctas, cudaStream_t strea
 
 cudaError_t launch_span_d64(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
 cudaError_t launch_span_d128(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
+cudaError_t launch_span_q4_d128(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
 cudaError_t launch_span_q4(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
 cudaError_t launch_span_q8(bool bf16, const span::Maps &tm, const span::Params &P, int ctas, cudaStream_t stream);
 

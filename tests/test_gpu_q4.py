@@ -328,19 +328,20 @@ def test_the_first_calls_of_a_process_are_captured():
 
 
 # ---------------------------------------------------------------- spans
-def check_spans(seed, spans, hq, hkv, dtype, amp=1.0):
+def check_spans(seed, spans, hq, hkv, dtype, amp=1.0, d=64):
+    scale = d ** -0.5  # scores of the same spread at either width, and so the same errors of the weights
     rng = np.random.default_rng(seed)
-    cache = _q4.Cache(rng, [L for _, L in spans], hkv, 16, 64, amp)
+    cache = _q4.Cache(rng, [L for _, L in spans], hkv, 16, d, amp)
     T = sum(n for n, _ in spans)
-    q = rows(rng, T, hq, 64, dtype)
+    q = rows(rng, T, hq, d, dtype)
     kc, ks, vc, vs, bt = cache.dev()
-    out = torch.full((T + 3, hq, 64), 5.0, dtype=q.dtype, device="cuda")
+    out = torch.full((T + 3, hq, d), 5.0, dtype=q.dtype, device="cuda")
     start = torch.from_numpy(_span.starts([n for n, _ in spans])).cuda()
     cl = torch.tensor([L for _, L in spans], dtype=torch.int32, device="cuda")
-    padded = torch.cat((q, torch.full((3, hq, 64), float("nan"), dtype=q.dtype))).cuda()
-    nb.ns_paged_attn_prefill_q4_0(padded, start, kc, ks, vc, vs, bt, cl, 0.125, out, nb.alloc_span_workspace(64))
+    padded = torch.cat((q, torch.full((3, hq, d), float("nan"), dtype=q.dtype))).cuda()
+    nb.ns_paged_attn_prefill_q4_0(padded, start, kc, ks, vc, vs, bt, cl, scale, out, nb.alloc_span_workspace(d))
     assert (out[T:] == 5.0).all()  # rows behind the last sequence
-    _span.compare(out[:T], _q4.attend_all(q, spans, cache, 0.125), dtype, str(spans[:4]), q8=True)
+    _span.compare(out[:T], _q4.attend_all(q, spans, cache, scale), dtype, str(spans[:4]), q8=True)
     assert _q4.status() == 0
 
 
@@ -361,6 +362,44 @@ def test_span_groups(hq, hkv):
 
 def test_span_values_of_other_sizes():
     check_spans(5, [(20, 200), (3, 600)], 14, 2, wl.BF16, amp=0.01)
+
+
+@pytest.mark.parametrize("dtype", [wl.F16, wl.BF16])
+@pytest.mark.parametrize("spans", SPANS + [[(1, n) for n in (15, 16, 17, 63, 64, 65, 127, 128, 129)]])
+def test_spans_head_dim_128(dtype, spans):
+    check_spans(len(spans) + 50, spans, 32, 8, dtype, d=128)
+
+
+@pytest.mark.parametrize("dtype", [wl.F16, wl.BF16])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 8), (9, 1), (64, 1)])
+def test_span_groups_head_dim_128(hq, hkv, dtype):
+    check_spans(hq + 50, [(9, 100), (40, 333)], hq, hkv, dtype, d=128)
+
+
+def test_span_values_of_other_sizes_head_dim_128():
+    check_spans(6, [(20, 200), (3, 600)], 14, 2, wl.BF16, amp=0.01, d=128)
+    check_spans(7, [(20, 200), (3, 600)], 14, 2, wl.F16, amp=0.01, d=128)
+
+
+def test_spans_bad_blocks_head_dim_128():
+    # pages left out in the first key tile, in the middle and at the end of one behind it, and all of one sequence's
+    rng = np.random.default_rng(71)
+    cache = _q4.Cache(rng, [230, 60, 20], 2, 16, 128)
+    q = rows(rng, 15, 14, 128, wl.F16)
+    kc, ks, vc, vs, bt = cache.dev()
+    bad = {0: [1, 5, 7], 1: [], 2: [0, 1]}
+    for s, blocks in bad.items():
+        for i, b in enumerate(blocks):
+            bt[s, b] = (-1, kc.shape[0], 2 ** 31 - 1)[i]
+    out = torch.zeros(15, 14, 128, dtype=q.dtype, device="cuda")
+    nb.ns_paged_attn_prefill_q4_0(q.cuda(), torch.tensor([0, 7, 12, 15], dtype=torch.int32, device="cuda"), kc, ks, vc, vs, bt,
+                                  torch.tensor([230, 60, 20], dtype=torch.int32, device="cuda"), 128 ** -0.5, out,
+                                  nb.alloc_span_workspace(128))
+    assert _q4.status() == 0x1
+    keep = np.setdiff1d(np.arange(230), np.r_[16:32, 80:96, 112:128])
+    _span.compare(out[:7], _span.attend(q[:7], cache.k[0][keep], cache.v[0][keep], 128 ** -0.5), wl.F16, q8=True)
+    _span.compare(out[7:12], _span.attend(q[7:12], cache.k[1], cache.v[1], 128 ** -0.5), wl.F16, q8=True)
+    assert (out[12:] == 0).all()
 
 
 def test_spans_what_no_token_fills_and_bad_blocks():

@@ -108,10 +108,10 @@ def prefill(lib, q=A, qsl=A, kc=A, ks=A, vc=A, vs=A, bt=A, cl=A, S=2, T=8, hq=14
 
 
 @pytest.mark.parametrize("change,want", [
-    (dict(d=128), UNSUPPORTED), (dict(bs=32), UNSUPPORTED), (dict(hq=15), UNSUPPORTED), (dict(hq=65, hkv=1), UNSUPPORTED),
+    (dict(d=96), UNSUPPORTED), (dict(bs=32), UNSUPPORTED), (dict(d=128, bs=8), UNSUPPORTED), (dict(hq=15), UNSUPPORTED), (dict(hq=65, hkv=1), UNSUPPORTED),
     (dict(dtype=9), UNSUPPORTED), (dict(width=1 << 30), UNSUPPORTED), (dict(width=0), INVALID), (dict(S=-1), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(q=None), INVALID), (dict(vs=None), INVALID), (dict(ks=A + 2), INVALID),
-    (dict(wsb=0), INVALID), (dict(T=0), OK), (dict(S=0), OK)])
+    (dict(wsb=0), INVALID), (dict(d=128, wsb=0), INVALID), (dict(d=128, T=0), OK), (dict(T=0), OK), (dict(S=0), OK)])
 def test_prefill_checks(lib, change, want):
     assert prefill(lib, **change) == want
 
