@@ -95,13 +95,14 @@ struct Geo {
     static constexpr int ROW = REG * CODES, STEPS = REG * 4;  // bytes of a key's codes, of its scales
     static constexpr int TILE = REG * KT * kPanel; // bytes of a K or V tile
     static constexpr int GROUP = KT / 4;           // keys of a conversion warp
-    static constexpr int STAGES = PAGED ? 3 : 4;
+    static constexpr int STAGES = PAGED ? 3 : 4;  // (4 for a 4-bit pool at 128: long chunks 444 us, 438 with 3)
     static constexpr int RAW = PAGED ? 3 : 1;         // q8_0 tiles in flight (4 measured 2 to 4 % slower)
     // TMEM columns: S of tile t at KT t, O at 2 KT + D t, P at 2 KT + 2 D + KT / 2 t
     static constexpr int O = 2 * KT, P = 2 * KT + 2 * D;
     static_assert(P + KT <= 512, "tensor memory");
     // cost of a unit besides its keys (laying out Q, filling the pipe, the epilogue)
-    // and the least cost that a CTA is given, in keys
+    // and the least cost that a CTA is given, in keys (drafts over a 4-bit pool at 128: 41.5 us,
+    // 4 KT 42.9, 8 KT 45.0)
     static constexpr int OVERHEAD = D == 128 ? 11 * KT / 2 : PAGED ? 5 * KT / 2 : 3 * KT;
     static constexpr int SHARE = OVERHEAD;  // at most one short unit a CTA while there are CTAs
     static constexpr int WHOLE = 4;  // units of so few key tiles are not cut
@@ -402,7 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The softmax reads that exponent with the scores, which then wait for the tile's V, or
     // only before it touches O.  The second is faster at head_dim 128, where the conversion
     // is behind (8192 bf16 tokens 480 us against 488, packed prompts 209 against 214), the
-    // first at 64 (149 against 150, packed 76.9 against 77.1; drafts over q8_0 18.5 against 19.2).
+    // first at 64 (149 against 150, packed 76.9 against 77.1; drafts over q8_0 18.5 against 19.2)
+    // and over 4-bit pools (head_dim 128, four chunks of 1024 over 5 to 7 K: fp16 438 against 444,
+    // bf16 449 against 451).
     constexpr bool LATE = BF && D == 128 && !PAGED;
     constexpr bool Q_TMA = q_by_tma(D, BF, PAGED);
     extern __shared__ unsigned char smem_raw[];
