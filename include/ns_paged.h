@@ -628,6 +628,7 @@ ns_status ns_verify_drafts(const float *target_probs, const float *draft_probs, 
  * rows (fp16 or bf16, [num_tokens][num_kv_heads][head_dim]) are quantised as
  * above and written at slot_mapping (negative: skipped; outside the pool:
  * skipped, NS_DEV_BAD_SLOT).  Codes and steps match the definition bit for bit.
+ * A token's keys are at most 2^30 elements.
  */
 ns_status ns_kv_append_q4_0(const void *k, const void *v, const int64_t *slot_mapping, void *k_codes,
                             void *k_scales, void *v_codes, void *v_scales, int num_tokens, int num_kv_heads,
@@ -714,7 +715,8 @@ ns_status ns_paged_attn_prefill_q4_0(const void *q, const int32_t *query_start_l
  *               (written)
  * Strides are multiples of 8 and at least the heads' width.  rotary_dim is a
  * multiple of 16, 16 .. head_dim.  num_q_heads need not be a multiple of
- * num_kv_heads.  head_dim is 64, or 128 with block_size 16 (q8_0 pools: 64).
+ * num_kv_heads; a token's queries and its keys are at most 2^30 elements each.
+ * head_dim is 64, or 128 with block_size 16 (q8_0 pools: 64).
  */
 ns_status ns_rope_kv_append(const void *q, const void *k, const void *v, const int32_t *positions,
                             const float *cos_sin, const int64_t *slot_mapping, void *q_out, void *k_out,

@@ -117,6 +117,8 @@ ns_status prefill_paged(const void *q, const int32_t *query_start_loc, const voi
     return done(ns::launch_span_attn(a, pool, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+constexpr int64_t kMaxRow = int64_t(1) << 30;  // elements of a token's row: offsets within it are 32-bit
+
 // What every append of this file asks of its arguments; NS_OK with no tokens too, then
 // without a look at the pointers.
 ns_status check_append(const ns::RopeAppendArgs &a, int pool)
@@ -128,6 +130,8 @@ ns_status check_append(const ns::RopeAppendArgs &a, int pool)
     if ((a.head_dim != 64 && a.head_dim != 128) || !block_size_ok(a.block_size))
         return NS_ERR_UNSUPPORTED;
     if (a.head_dim == 128 && (pool == 8 || a.block_size != 16))
+        return NS_ERR_UNSUPPORTED;
+    if ((int64_t)a.num_kv_heads * a.head_dim > kMaxRow || (int64_t)a.num_q_heads * a.head_dim > kMaxRow)
         return NS_ERR_UNSUPPORTED;
     if (a.num_tokens == 0)
         return NS_OK;

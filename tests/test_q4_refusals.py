@@ -44,6 +44,12 @@ def test_rope_append_checks(lib, pool, change, want):
     assert rope(lib, pool, **change) == want
 
 
+def test_rows_whose_offsets_pass_32_bits_are_refused(lib):
+    assert rope(lib, hq=(1 << 24) + 1) == UNSUPPORTED and rope(lib, hkv=(1 << 24) + 1) == UNSUPPORTED
+    assert rope(lib, "q4_0", hq=(1 << 31) - 1) == UNSUPPORTED and append(lib, hkv=(1 << 31) - 1) == UNSUPPORTED
+    assert rope(lib, hq=1 << 24, T=0) == OK and append(lib, hkv=1 << 24, T=0) == OK
+
+
 def test_rope_append_pools_of_their_own(lib):
     assert rope(lib, "q8_0", d=128, r=64) == UNSUPPORTED
     for pool in ("q8_0", "q4_0"):
