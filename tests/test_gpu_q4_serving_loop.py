@@ -89,18 +89,18 @@ def test_prompts_steps_drafts_and_read_back(dtype, hq, hkv, d, rotary, interleav
     for i in range(3):
         q, _, _ = sv.step([1, 1, 1, 1], pad=i)
         _q4.compare(sv.decode(q), sv.exact(q, [1] * 4).numpy(), dtype, f"step {i}")
-    if d == 64:  # drafted tokens; some are dropped, and their places taken again
-        for i in range(2):
-            counts = [4, 1, 6, 3]
-            q, _, _ = sv.step(counts)
-            out = torch.empty_like(q)
-            nb.ns_paged_attn_prefill_q4_0(q, _gpu.dev_ints(_span.starts(counts), np.int32), *sv.pools, sv.bt, sv.lens(),
-                                          sv.scale, out, sv.sws)
-            _span.compare(out, sv.exact(q, counts), dtype, f"drafts {i}", q8=True)
-            sv.ctx = sv.ctx - np.array([2, 0, 5, 1])
-            for side in sv.held:
-                for s in range(4):
-                    side[s] = side[s][:sv.ctx[s]]
+    # drafted tokens; some are dropped, and their places taken again
+    for i in range(2):
+        counts = [4, 1, 6, 3]
+        q, _, _ = sv.step(counts)
+        out = torch.empty_like(q)
+        nb.ns_paged_attn_prefill_q4_0(q, _gpu.dev_ints(_span.starts(counts), np.int32), *sv.pools, sv.bt, sv.lens(),
+                                      sv.scale, out, sv.sws)
+        _span.compare(out, sv.exact(q, counts), dtype, f"drafts {i}", q8=True)
+        sv.ctx = sv.ctx - np.array([2, 0, 5, 1])
+        for side in sv.held:
+            for s in range(4):
+                side[s] = side[s][:sv.ctx[s]]
     # read back, as the prefix of a new prompt
     ksl = _span.starts(sv.ctx)
     kr = torch.empty(int(ksl[-1]), hkv, d, dtype=sv.td, device="cuda")
@@ -196,6 +196,42 @@ def test_order_of_copies_append_attention_and_read_back(d, captured):
     assert _q4.status() == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_span_calls_captured_replayed_and_on_another_stream(d):
+    """The rotation of drafted tokens and their attention, twice on one workspace, in a graph and on a stream."""
+    c = Chain(d)
+    c.copies()
+    c.append()
+    start = torch.arange(7, dtype=torch.int32, device="cuda")
+    outs = [torch.zeros_like(c.q) for _ in range(2)]
+
+    def run():
+        c.append()
+        for out in outs:
+            nb.ns_paged_attn_prefill_q4_0(c.q, start, *c.sv.pools, c.sv.bt, c.lens, c.sv.scale, out, c.sv.sws)
+    run()
+    torch.cuda.synchronize()
+    want = outs[0].clone()
+    assert (want != 0).any() and _q4.same_bits(outs[1], want)
+    c.attend()
+    # the decode's output: four roundings to fp16 (V, the weights, and scores of keys there; w dv here), 2^-11 of a
+    # value below 4.5 each, and the two outputs', 2^-10 each below 4
+    assert (want.float() - c.out.float()).abs().max() < 4 * 4.5 * 2 ** -11 + 2 * 2 ** -10
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    side = torch.cuda.Stream()
+    for again in (graph.replay, graph.replay, run):
+        for out in outs:
+            out.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            again()
+        torch.cuda.synchronize()
+        assert _q4.same_bits(outs[0], want) and _q4.same_bits(outs[1], want)
+    assert _q4.status() == 0
+
+
 def test_calls_behind_a_long_walk_wait_for_what_they_share():
     """A prefill whose single-token row outlasts its chunk, then a rotation in place of its output and a
     q4_0 decode that reads that: the results are those with a synchronisation between the calls."""
@@ -280,6 +316,13 @@ def test_long_offsets_in_a_large_pool():
     nb.ns_paged_attn_decode_q4_0(q, *pools, bt, _gpu.dev_ints(lens, np.int32), d ** -0.5, out, nb.alloc_workspace(2, 8, hkv, d))
     ref = torch.cat([_span.attend(q[s:s + 1].cpu(), held[0][seq == s], held[1][seq == s], d ** -0.5) for s in range(2)])
     _q4.compare(out, ref.numpy(), wl.BF16, "far blocks")
+    counts = [5, 1]
+    qs = torch.cat([q_out[65:70], q_out[T - 1:]])
+    out = torch.empty_like(qs)
+    nb.ns_paged_attn_prefill_q4_0(qs, _gpu.dev_ints(_span.starts(counts), np.int32), *pools, bt, _gpu.dev_ints(lens, np.int32),
+                                  d ** -0.5, out, nb.alloc_span_workspace(d))
+    ref = torch.cat([_span.attend(x.cpu(), held[0][seq == s], held[1][seq == s], d ** -0.5) for s, x in enumerate((qs[:5], qs[5:]))])
+    _span.compare(out, ref, wl.BF16, "far blocks, spans", q8=True)
     rows = [torch.empty(T, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
     nb.ns_kv_gather_q4_0(*pools, bt, _gpu.dev_ints(_span.starts(lens), np.int32), *rows)
     for got, want in zip(rows, held):
