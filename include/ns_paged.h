@@ -123,12 +123,17 @@ ns_status ns_kv_append(const void *k, const void *v, const int64_t *slot_mapping
  * Workspace for the attention entry points: split-KV partial results
  * (fp32 running max, running sum and unnormalised output of each piece of a
  * sequence that was cut across workers: about 8.7 MB for head_dim 64, 17 MB
- * for 128), one arrival counter per (sequence, kv head) and a small plan
+ * for 128), one arrival counter per (sequence, kv head) (with more than 8 query
+ * heads a kv head, one per 8 of them) and a small plan
  * record.  Size it with ns_paged_attn_workspace_bytes for the largest
- * num_seqs and the head_dim you will pass.  It must be zero-filled once before
- * first use (ns_paged_attn_workspace_init or cudaMemsetAsync); every call
- * that completes without a device status bit leaves it ready for the next
- * call.  Two calls that share a workspace must not run concurrently.
+ * num_seqs (total_q_tokens of a prefill) and the head_dim you will pass.  It must be
+ * zero-filled once before first use (ns_paged_attn_workspace_init or cudaMemsetAsync);
+ * every call that completes without a device status bit leaves it ready for the next
+ * call, of any number of sequences up to that.  Pass its whole size as
+ * workspace_bytes in every call: the records lie at its end, the counters at its start.
+ * One that serves calls of several num_q_heads, num_kv_heads or head_dim is as
+ * large as the sizes for each of them together.  Two calls that share a workspace
+ * must not run concurrently.
  */
 size_t ns_paged_attn_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                      int head_dim);

@@ -286,7 +286,7 @@ def ns_paged_attn_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads:
 
 def alloc_workspace(num_rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int = 64,
                     device=None) -> torch.Tensor:
-    """A zero-filled workspace for up to ``num_rows`` query rows (sequences when decoding)."""
+    """A zero-filled workspace for calls with these heads of up to ``num_rows`` query rows (sequences when decoding)."""
     n = ns_paged_attn_workspace_bytes(num_rows, num_q_heads, num_kv_heads, head_dim)
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 

@@ -237,9 +237,13 @@ int resident_ctas(int dev, ns_dtype dt, int bs, int g, bool q8, int head_dim)
     return (int)(total > NS_MAX_CTAS ? NS_MAX_CTAS : total);
 }
 
-// Workspace layout (byte offsets), for up to `rows` query rows.
+// Workspace layout (byte offsets) of a call with `rows` query rows: the plan and the arrival
+// counters at the start of the workspace, the records and row arrays at its end.  Counters have
+// to be zero between calls, everything else carries nothing, and a call needs no more of either
+// end than the largest one does: so on a workspace of that one's size the records of a small call lie
+// behind the counters of every other call.
 struct WsLayout {
-    size_t plan, counters, partials, row_seq, row_len, total;
+    size_t plan, counters, partials, row_seq, row_len;
 };
 
 // Groups of more than kMaxGroup query heads run as kv_sub groups of G / kv_sub
@@ -254,15 +258,31 @@ int kv_sub(int num_q_heads, int num_kv_heads)
     return g % sub == 0 ? sub : 0;
 }
 
-WsLayout ws_layout(long long rows, int num_kv_heads, int head_dim)
+size_t counter_bytes(long long rows, int num_kv_heads) { return align256((size_t)rows * num_kv_heads * sizeof(int32_t)); }
+
+size_t row_bytes(long long rows) { return align256((size_t)rows * sizeof(int32_t)); }
+
+size_t record_bytes(int head_dim)
+{
+    return align256((size_t)ns::kMaxWorkers * 2 * ns::slot_floats(head_dim) * sizeof(float));
+}
+
+constexpr size_t kPlanSize = 256;
+
+size_t ws_bytes(long long rows, int num_kv_heads, int head_dim)
+{
+    return kPlanSize + counter_bytes(rows, num_kv_heads) + record_bytes(head_dim) + 2 * row_bytes(rows);
+}
+
+// `bytes`: of the workspace, at least ws_bytes of the call.
+WsLayout ws_layout(size_t bytes, long long rows, int head_dim)
 {
     WsLayout L;
     L.plan = 0;
-    L.counters = 256;
-    L.partials = L.counters + align256((size_t)rows * num_kv_heads * sizeof(int32_t));
-    L.row_seq = L.partials + align256((size_t)ns::kMaxWorkers * 2 * ns::slot_floats(head_dim) * sizeof(float));
-    L.row_len = L.row_seq + align256((size_t)rows * sizeof(int32_t));
-    L.total = L.row_len + align256((size_t)rows * sizeof(int32_t));
+    L.counters = kPlanSize;
+    L.row_len = bytes / 256 * 256 - row_bytes(rows);
+    L.row_seq = L.row_len - row_bytes(rows);
+    L.partials = L.row_seq - record_bytes(head_dim);
     return L;
 }
 
@@ -299,6 +319,7 @@ struct DecodeCall {
     long long num_blocks;
     ns_dtype dtype;
     void *workspace;
+    size_t workspace_bytes;
     const ns_decode_config *cfg;
     const void *k_new, *v_new;
     const int64_t *slot_mapping;
@@ -317,7 +338,7 @@ ns_status run_decode(const DecodeCall &c, int dev)
     if (status == nullptr)
         return NS_ERR_CUDA;
     const int sub = kv_sub(c.num_q_heads, c.num_kv_heads);
-    const WsLayout L = ws_layout(c.rows, c.num_kv_heads * sub, c.head_dim);
+    const WsLayout L = ws_layout(c.workspace_bytes, c.rows, c.head_dim);
     char *ws = static_cast<char *>(c.workspace);
 
     ns::DecodeParams P;
@@ -475,7 +496,7 @@ ns_status decode_q8_0(const void *q, const void *k_new, const void *v_new, const
         return NS_ERR_CUDA;
     DecodeCall c{q, nullptr, nullptr, block_tables, context_lens, nullptr, num_seqs, num_q_heads, num_kv_heads,
                  block_size, scale, out, reinterpret_cast<cudaStream_t>(stream), max_blocks_per_seq, num_blocks,
-                 dtype, workspace, cfg, k_new, v_new, k_new ? slot_mapping : nullptr};
+                 dtype, workspace, workspace_bytes, cfg, k_new, v_new, k_new ? slot_mapping : nullptr};
     c.q8 = true;
     c.head_dim = head_dim;
     c.k_codes = k_codes;
@@ -541,7 +562,7 @@ size_t ns_paged_attn_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
     // as many counters as the q4_0 decode needs too, whose groups need not be cut evenly
     const int group = num_q_heads > 0 ? num_q_heads / num_kv_heads : 1;
     const int sub = std::max(1, (group + ns::kMaxGroup - 1) / ns::kMaxGroup);
-    return ws_layout(num_seqs, num_kv_heads * sub, head_dim == 128 ? 128 : 64).total;
+    return ws_bytes(num_seqs, num_kv_heads * sub, head_dim == 128 ? 128 : 64);
 }
 
 ns_status ns_paged_attn_workspace_init(void *workspace, size_t workspace_bytes, ns_stream_t stream)
@@ -575,7 +596,7 @@ ns_status ns_paged_attn_decode_ex(const void *q, const void *k_pool, const void 
         return NS_ERR_CUDA;
     DecodeCall c{q, k_pool, v_pool, block_tables, context_lens, nullptr, num_seqs, num_q_heads,
                  num_kv_heads, block_size, scale, out, reinterpret_cast<cudaStream_t>(stream),
-                 max_blocks_per_seq, num_blocks, dtype, workspace, cfg, nullptr, nullptr, nullptr};
+                 max_blocks_per_seq, num_blocks, dtype, workspace, workspace_bytes, cfg, nullptr, nullptr, nullptr};
     c.head_dim = head_dim;
     return run_decode(c, dev);
 }
@@ -635,7 +656,7 @@ ns_status ns_kv_append_paged_attn_decode_ex(const void *q, const void *k_new, co
         return NS_ERR_CUDA;
     DecodeCall c{q, k_pool, v_pool, block_tables, context_lens, nullptr, num_seqs, num_q_heads,
                  num_kv_heads, block_size, scale, out, reinterpret_cast<cudaStream_t>(stream),
-                 max_blocks_per_seq, num_blocks, dtype, workspace, cfg, k_new, v_new,
+                 max_blocks_per_seq, num_blocks, dtype, workspace, workspace_bytes, cfg, k_new, v_new,
                  slot_mapping};
     c.head_dim = head_dim;
     return run_decode(c, dev);
@@ -678,7 +699,7 @@ ns_status ns_paged_attn_prefill_ex(const void *q, const int32_t *query_start_loc
     unsigned *status = status_word(dev);
     if (status == nullptr)
         return NS_ERR_CUDA;
-    const WsLayout L = ws_layout(total_q_tokens, num_kv_heads * kv_sub(num_q_heads, num_kv_heads), head_dim);
+    const WsLayout L = ws_layout(workspace_bytes, total_q_tokens, head_dim);
     char *ws = static_cast<char *>(workspace);
     int32_t *row_seq = reinterpret_cast<int32_t *>(ws + L.row_seq);
     int32_t *row_len = reinterpret_cast<int32_t *>(ws + L.row_len);
@@ -701,7 +722,7 @@ ns_status ns_paged_attn_prefill_ex(const void *q, const int32_t *query_start_loc
             return NS_ERR_CUDA;
         DecodeCall c{q, k_pool, v_pool, block_tables, row_len, row_seq, total_q_tokens, num_q_heads,
                      num_kv_heads, block_size, scale, out, st, max_blocks_per_seq, num_blocks, dtype,
-                     workspace, nullptr, nullptr, nullptr, nullptr};
+                     workspace, workspace_bytes, nullptr, nullptr, nullptr, nullptr};
         c.head_dim = head_dim;
         // With more query tokens than spans, some span has two or more and the
         // tensor-core kernel after the walk has work: the walk then packs its
@@ -846,7 +867,7 @@ ns_status ns_paged_attn_decode_q4_0(const void *q, const void *k_codes, const vo
     unsigned *status = status_word(dev);
     if (status == nullptr)
         return NS_ERR_CUDA;
-    const WsLayout L = ws_layout(num_seqs, num_kv_heads * subs, head_dim);
+    const WsLayout L = ws_layout(workspace_bytes, num_seqs, head_dim);
     char *ws = static_cast<char *>(workspace);
     const ns::Q4DecodeArgs a = {q, k_codes, k_scales, v_codes, v_scales, block_tables, context_lens, num_seqs,
                                 num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale,
