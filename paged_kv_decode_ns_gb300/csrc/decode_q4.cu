@@ -318,9 +318,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
     const Q4DecodeArgs &a = P.a;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;  // row and column pair of the products' fragments
-    if (tid < W) {
-        sm.first_pair[tid] = -1;
-        sm.last_pair[tid] = -1;
+    if (lane == 0) {  // by the lane that writes them later: no barrier lies between (up to 32 sequences)
+        sm.first_pair[warp] = -1;
+        sm.last_pair[warp] = -1;
     }
     if (tid < 2)
         sm.to_join[tid] = -1;
