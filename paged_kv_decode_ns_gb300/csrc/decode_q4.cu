@@ -36,6 +36,7 @@ namespace {
 constexpr int kChunk = 32;     // tokens of a step: one a lane
 constexpr int kPairCost = 2;   // chunks that a pair counts besides its own (batch 256 21.9 us; 0: 23.7, 1 and 3: 22.4)
 constexpr float kNone = -3.402823466e38f;
+constexpr float kLeastUnit = 1.17549435e-38f;  // 2^-126
 // m is set so that the largest w dv is just below 2^kLift, and moves when one would pass
 // that by 2^kSlack: fp16 has room up to 2^16 and steps of 2^-24.
 constexpr float kLift = 7.0f, kSlack = 8.0f;
@@ -541,9 +542,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                 q_sum[r] = sum * (-8.f / kCode);
             }
         }
-        // of the two heads of this lane's columns: a unit of the products, and where they start
-        const float2 unit = make_float2(P.scale_log2 * (__shfl_sync(0xffffffffu, q_unit, 8 * t) * kCode),
-                                        P.scale_log2 * (__shfl_sync(0xffffffffu, q_unit, 8 * t + 4) * kCode));
+        // of the two heads of this lane's columns: a unit of the products, and where they start (the
+        // unit stays above 0, which the -infinity of a token that is not there must not meet)
+        const float2 unit = make_float2(fmaxf(P.scale_log2 * (__shfl_sync(0xffffffffu, q_unit, 8 * t) * kCode), kLeastUnit),
+                                        fmaxf(P.scale_log2 * (__shfl_sync(0xffffffffu, q_unit, 8 * t + 4) * kCode), kLeastUnit));
         float2 base[R];
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -956,7 +958,7 @@ cudaError_t launch_decode_q4(const Q4DecodeArgs &a, cudaStream_t stream)
     P.shift = a.block_size == 4 ? 2 : a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
     // a unit of the products has to be positive: q takes the scale's sign
     P.blocks = (uint32_t)std::min<long long>(a.num_blocks, 0x80000000LL);
-    P.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
+    P.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, kLeastUnit);
     P.sign = a.scale < 0.f ? -1.f : 1.f;
     P.counters = a.counters;
     P.records = a.records;
