@@ -662,8 +662,8 @@ ns_status ns_kv_gather_q4_0(const void *k_codes, const void *k_scales, const voi
  * (NS_DEV_BAD_BLOCK_ID).  q is rounded to fp16 for the product, scaled by a power
  * of two first (off by at most 2^-39 of the row's largest element), and so is each
  * softmax weight times its step of V (off by 2^-11 of itself, or 2^-32 of the largest
- * weight times the largest step); scores, sums and outputs are fp32 until the last rounding.  A NaN
- * step reaches the rows that see its token.
+ * weight times the largest step); scores, sums and outputs are fp32 until the last rounding.  Scores
+ * may have any size.  A NaN step reaches the rows that see its token.
  */
 ns_status ns_paged_attn_decode_q4_0(const void *q, const void *k_codes, const void *k_scales,
                                     const void *v_codes, const void *v_scales,

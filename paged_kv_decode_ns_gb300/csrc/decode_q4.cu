@@ -36,9 +36,9 @@ namespace {
 constexpr int kChunk = 32;     // tokens of a step: one a lane
 constexpr int kPairCost = 2;   // chunks that a pair counts besides its own (batch 256 21.9 us; 0: 23.7, 1 and 3: 22.4)
 constexpr float kNone = -3.402823466e38f;
-constexpr float kLeastUnit = 1.17549435e-38f;  // 2^-126
-// m is set so that the largest w dv is just below 2^kLift, and moves when one would pass
-// that by 2^kSlack: fp16 has room up to 2^16 and steps of 2^-24.
+constexpr float kLeastUnit = 1.17549435e-38f, kMostUnit = 1.2676506e30f;  // 2^-126, 2^100
+// The largest w dv is set just below 2^kLift, and again when one would pass that by
+// 2^kSlack: fp16 has room up to 2^16 and steps of 2^-24.
 constexpr float kLift = 7.0f, kSlack = 8.0f;
 
 template <int D>
@@ -145,6 +145,8 @@ __device__ __forceinline__ void less_8(uint32_t (&p)[4])
     }
 }
 constexpr float kCode = 16777216.f, kCodeHigh = 1048576.f;  // 2^24, 2^20
+
+__device__ __forceinline__ float unit_of(float x) { return fminf(fmaxf(x * kCode, kLeastUnit), kMostUnit); }
 
 __device__ __forceinline__ uint32_t larger_f16(uint32_t a, uint32_t b)  // magnitudes, signs of no meaning
 {
@@ -542,10 +544,11 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                 q_sum[r] = sum * (-8.f / kCode);
             }
         }
-        // of the two heads of this lane's columns: a unit of the products, and where they start (the
-        // unit stays above 0, which the -infinity of a token that is not there must not meet)
-        const float2 unit = make_float2(fmaxf(P.scale_log2 * (__shfl_sync(0xffffffffu, q_unit, 8 * t) * kCode), kLeastUnit),
-                                        fmaxf(P.scale_log2 * (__shfl_sync(0xffffffffu, q_unit, 8 * t + 4) * kCode), kLeastUnit));
+        // of the two heads of this lane's columns: a unit of the products, and where they start.  The
+        // unit stays above 0, which the -infinity of a token that is not there must not meet, and at 2^100:
+        // different products are 2^-72 apart at least, so that their scores still differ by 2^28 there.
+        const float2 unit = make_float2(unit_of(P.scale_log2 * __shfl_sync(0xffffffffu, q_unit, 8 * t)),
+                                        unit_of(P.scale_log2 * __shfl_sync(0xffffffffu, q_unit, 8 * t + 4)));
         float2 base[R];
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -559,11 +562,13 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     O[r][u][i] = 0.f;
-        // the references and the limits of the scores, these in units of the products
-        float2 l = make_float2(0.f, 0.f), m = make_float2(kNone, kNone), limit = m;
-        const float2 per_unit = make_float2(__fdividef(1.f, unit.x), __fdividef(1.f, unit.y));
-        int top_e = -1;            // exponent field of the largest V step so far
-        uint32_t step_limit = 0u;  // and the largest fp16 of that exponent
+        // Weights are 2^((z - z0) unit + lift): the reference z0 and the limit of the scores are in units of the
+        // products, and the difference of scores of any size is exact before it is scaled.  (As z unit - m
+        // in one step, scores from 2^24 on met the rounding of m; batch 256 21.3 us then, 21.7 so.)
+        float2 l = make_float2(0.f, 0.f), z0 = make_float2(kNone, kNone), limit = z0;
+        const float2 slack = make_float2(kSlack * __fdividef(1.f, unit.x), kSlack * __fdividef(1.f, unit.y));
+        uint32_t step_limit = 0u;  // the largest fp16 with the exponent of the largest V step so far
+        float lift = 0.f;          // kLift less what those steps are below, in log2
 
         for (int c = p.c; c < p.c1; ++c) {
             copies_wait<ST - 2>();
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
             for (int x = 1; x < 4 * (R / 2); ++x)
                 largest = larger_f16(largest, dv[x / (R / 2) / 2][x / (R / 2) % 2][x % (R / 2)]);
 
-            // ---- the reference moves when a weight times a step would leave fp16's range
+            // ---- the reference moves, or the lift falls, when a weight times a step would leave fp16's range
             const float za = fmaxf(fmaxf(z[0][0].x, z[0][1].x), fmaxf(z[1][0].x, z[1][1].x));
             const float zb = fmaxf(fmaxf(z[0][0].y, z[0][1].y), fmaxf(z[1][0].y, z[1][1].y));
             const uint32_t big = max(largest & 0x7fffu, (largest >> 16) & 0x7fffu);
@@ -644,16 +649,16 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                     top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, o));
                     top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, o));
                 }
+                const int top_e = (int)((step_limit + 1u) >> 10) - 1;  // the field of that exponent, or -1
                 const int e = max(top_e, (int)(__reduce_max_sync(0xffffffffu, big) >> 10));
-                const float rise = top_e < 0 ? 0.f : (float)(e - top_e), size = (float)(e - 14);  // steps are below 2^size
-                top_e = e;
+                const float higher = kLift - (float)(e - 14), fall = higher - lift;  // steps are below 2^(e - 14)
+                lift = higher;
                 step_limit = ((uint32_t)(e + 1) << 10) - 1u;
                 // a head's reference follows its own scores alone, whatever the heads beside it hold
-                const float2 to = make_float2(top.x > limit.x ? fmaxf(m.x + rise, fmaf(top.x, unit.x, size - kLift)) : m.x + rise,
-                                              top.y > limit.y ? fmaxf(m.y + rise, fmaf(top.y, unit.y, size - kLift)) : m.y + rise);
-                const float2 f = make_float2(fast_exp2(m.x - to.x), fast_exp2(m.y - to.y));
-                m = to;
-                limit = fmul2(make_float2(m.x - size + kLift + kSlack, m.y - size + kLift + kSlack), per_unit);
+                const float2 to = make_float2(top.x > limit.x ? top.x : z0.x, top.y > limit.y ? top.y : z0.y);
+                const float2 f = make_float2(fast_exp2(fmaf(z0.x - to.x, unit.x, fall)), fast_exp2(fmaf(z0.y - to.y, unit.y, fall)));
+                z0 = to;
+                limit = fadd2(z0, slack);
                 l = fmul2(l, f);
 #pragma unroll
                 for (int r = 0; r < R; ++r)
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
                 float2 w[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float2 x = ffma2(z[tile][i], unit, make_float2(-m.x, -m.y));
+                    const float2 x = ffma2(fadd2(z[tile][i], make_float2(-z0.x, -z0.y)), unit, make_float2(lift, lift));
                     w[i] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                     l = fadd2(l, w[i]);
                 }
@@ -703,18 +708,21 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
         }
 
         // ---- the piece's end: this lane has elements 4 g .. 4 g + 3 of each group, heads 2 t, 2 t + 1
+        // (the lift out again, exactly: pieces of a pair have lifts of their own)
+        const float drop = __uint_as_float((uint32_t)(127 - (int)lift) << 23);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             l.x += __shfl_xor_sync(0xffffffffu, l.x, o);
             l.y += __shfl_xor_sync(0xffffffffu, l.y, o);
         }
+        l = fmul2(l, make_float2(drop, drop));
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    O[r][u][i] *= i < 2 ? kCode : kCodeHigh;
+                    O[r][u][i] *= (i < 2 ? kCode : kCodeHigh) * drop;
         if (p.whole) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -742,8 +750,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_q4_kernel(const __g
             for (int i = 0; i < 2; ++i) {
                 const int h = 2 * t + i;
                 if (g == 0) {
-                    rec[h] = i == 0 ? m.x : m.y;
-                    rec[8 + h] = i == 0 ? l.x : l.y;
+                    const float sum = i == 0 ? l.x : l.y;
+                    rec[h] = sum != 0.f ? fmaxf(i == 0 ? z0.x * unit.x : z0.y * unit.y, kNone) : kNone;
+                    rec[8 + h] = sum;
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r)

@@ -6,6 +6,7 @@ import torch
 import _gpu
 import _q4
 from _q4 import wl
+from _span import attend as exact_attend
 from paged_kv_decode_ns_gb300 import binding as nb
 
 pytestmark = pytest.mark.gpu
@@ -53,6 +54,54 @@ def test_scores_that_vanish(scale, amp, d):
     assert _q4.status() == 0
     cache.tables[2, 1] = -1
     keep = np.r_[0:16, 32:100]
-    ref[2] = _q4.attend(q[2:3], cache.k[2][keep], cache.v[2][keep], scale).numpy()[0]
+    ref[2] = exact_attend(q[2:3], cache.k[2][keep], cache.v[2][keep], scale).numpy()[0]
     _q4.compare(attend(cache, q, lens, scale, wl.BF16), ref, wl.BF16)
     assert _q4.status() == 1
+
+
+def rows_of(cache, s, L):
+    """fp64 K and V [L, Hkv, D] of a sequence through its table, whose entries may repeat."""
+    p = np.arange(L)
+    at = (cache.tables[s, p // 16], slice(None), p % 16)
+    return (torch.from_numpy(_q4.values(c[at], st[at])) for c, st in ((cache.kc, cache.ks), (cache.vc, cache.vs)))
+
+
+# Scores from 2^24 on.  They are far apart (the chance that the largest two of up to 800 differ by less
+# than 2^-20 of themselves, where fp32 scores could change places, is about 800 2^-20 a row), so that one key, or
+# equal ones, has all the weight, and the output is its row of V to the last rounding.
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,scale,q_amp,amp", [
+    (wl.F16, 0.125, 1e4, 3000.0), (wl.BF16, 0.125, 1e9, 1.0), (wl.BF16, 0.125, 1e20, 1.0), (wl.BF16, 0.125, 1e37, 1.0),
+    (wl.BF16, -1.0, 1e37, 30.0), (wl.F16, 1e9, 1.0, 1.0), (wl.F16, 3e38, 100.0, 1.0), (wl.BF16, 1e30, 1e30, 1.0),
+    (wl.BF16, 1e-30, 1e37, 30.0)])
+def test_scores_of_any_size(dtype, scale, q_amp, amp, d):
+    rng = np.random.default_rng(3)
+    lens = [1, 33, 100, 777]
+    cache = _q4.Cache(rng, lens, 2, 16, d, amp)
+    q = _q4.to16(rng.standard_normal((4, 14, d)).astype(np.float32) * np.float32(q_amp), dtype)
+    ref = _q4.attend_all(q, [(1, n) for n in lens], cache, scale).numpy()
+    _q4.compare(attend(cache, q, lens, scale, dtype), ref, dtype)
+    assert _q4.status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_amp", [1.0, 1e9, 1e37])
+def test_large_scores_that_recur_across_pieces(q_amp, d):
+    """The same keys again and again along a sequence that every CTA has a piece of, its second half
+    among keys whose values are 2^12 larger: the pieces agree on the weights of equal scores."""
+    rng = np.random.default_rng(4)
+    cache = _q4.Cache(rng, [80, 80], 1, 16, d, 1.0)
+    near, far = cache.tables[0].copy(), cache.tables[1].copy()
+    cache.vs[far] = (cache.vs[far].astype(np.float32) * 4096).astype(np.float16)
+    if q_amp > 1:  # no weight there
+        cache.ks[far] = (cache.ks[far].astype(np.float32) / 64).astype(np.float16)
+    cache.tables = np.concatenate((np.resize(near, 200), np.resize(np.concatenate((near, far)), 200)))[None].astype(np.int32)
+    L = 400 * 16
+    q = _q4.to16(rng.standard_normal((1, 8, d)).astype(np.float32) * np.float32(q_amp), wl.BF16)
+    ref = exact_attend(q, *rows_of(cache, 0, L), d ** -0.5).numpy()
+    got = attend(cache, q, [L], d ** -0.5, wl.BF16)
+    if q_amp > 1:
+        _q4.compare(got, ref, wl.BF16)
+    else:  # a rounding of each weight times its step by 2^-11, against values of 2^12 times 5; and the output's
+        assert (np.abs(_gpu.to_f64(got) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -11 * 4096 * 5).all()
+    assert _q4.status() == 0
