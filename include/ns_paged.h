@@ -660,7 +660,7 @@ ns_status ns_kv_gather_q4_0(const void *k_codes, const void *k_scales, const voi
  * negative or beyond the table row counts as 0 or as the row's tokens
  * (NS_DEV_BAD_CONTEXT_LEN); tokens of a block id outside the pool are left out
  * (NS_DEV_BAD_BLOCK_ID).  q is rounded to fp16 for the product, scaled by a power
- * of two first (off by at most 2^-39 of the row's largest element), and so is each
+ * of two first (off by at most 2^-35 of the row's largest element), and so is each
  * softmax weight times its step of V (off by 2^-11 of itself, or 2^-32 of the largest
  * weight times the largest step); scores, sums and outputs are fp32 until the last rounding.  Scores
  * may have any size.  A NaN step reaches the rows that see its token.
@@ -676,8 +676,12 @@ ns_status ns_paged_attn_decode_q4_0(const void *q, const void *k_codes, const vo
 /*
  * ns_paged_attn_prefill_q4_0 -- ns_paged_attn_prefill_q8_0 over a q4_0 pool, with
  * the same block size (16), checks and workspace (ns_span_attn_workspace_bytes of
- * the head_dim), at head_dim 64 and 128.  Scales far below the largest of the sequence and kv
- * head lose bits as there (their values are off by up to 2^-32 of the largest value).
+ * the head_dim), at head_dim 64 and 128.  The same three factors are rounded to fp16 for
+ * the products (2^-11 each: an fp16 call is off by 3.9e-4 of its output, 2.1e-4 of that the
+ * output's own rounding; ns_paged_attn_decode_q4_0 rounds the weights alone): the
+ * dequantised keys and values, and the softmax weights.  Scales far below the largest of the
+ * sequence and kv head lose bits as there (their values are off by up to 2^-32 of the
+ * largest value).
  */
 ns_status ns_paged_attn_prefill_q4_0(const void *q, const int32_t *query_start_loc, const void *k_codes,
                                      const void *k_scales, const void *v_codes, const void *v_scales,
