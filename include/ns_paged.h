@@ -496,7 +496,9 @@ size_t ns_span_attn_workspace_bytes(int head_dim);
  * 2^-32 of that (2^-12 of the output from a million keys).  bf16 values are scaled
  * by powers of two on the way, so that they may have any size: each is off by at
  * most 2^-36 of the largest value of its sequence and kv head (and exact above
- * 2^-28 of it), or by 2^-109.
+ * 2^-28 of it), or by 2^-109.  Scores times log2 e are up to 2^22 in size: from there
+ * on the rounding of a row's running reference reaches its weights, and from 2^23 on one
+ * of them may leave fp16's range and make the row NaN.
  */
 ns_status ns_prompt_attn(const void *q, const void *k, const void *v, const int32_t *query_start_loc,
                          const int32_t *key_start_loc, int num_seqs, int total_q_tokens,
@@ -517,8 +519,8 @@ ns_status ns_prompt_attn(const void *q, const void *k, const void *v, const int3
  * its table row (NS_DEV_BAD_CONTEXT_LEN); a block id outside the pool sets
  * NS_DEV_BAD_BLOCK_ID and its tokens are left out.  The dequantised keys and
  * values and the softmax weights are rounded to fp16 for the products, and so
- * are bf16 queries, each scaled by a power of two first.  Weights are kept as in
- * ns_prompt_attn; scales far below the largest of the sequence and kv head lose
+ * are bf16 queries, each scaled by a power of two first.  Weights are kept and scores
+ * bounded as in ns_prompt_attn; scales far below the largest of the sequence and kv head lose
  * bits (their values are off by up to 2^-29 of the largest value).  An infinite or
  * NaN scale may reach every row of its own span.  workspace: ns_span_attn_workspace_bytes(64).
  */
