@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t d[2] = {have ? scales[pair] : 0u, have ? scales[KT * REG + pair] : 0u};
                     // the tile's largest scale of V, four pairs a lane (those that are there)
                     const int pair4 = 4 * lane;
-                    const int there = (loaded >> (pair4 / REG / 16)) & 1u ? (u.L - j * KT) * REG - pair4 : 0;
+                    const int there = (loaded >> (pair4 / REG / 16)) & 1u ? min(u.L - j * KT, KT) * REG - pair4 : 0;
                     uint4 w4 = lds128(scales + KT * REG + pair4);
                     if (there < 4) {
                         w4.w = 0u;
