@@ -229,9 +229,7 @@ cudaError_t launch_rope_append(const RopeAppendArgs &in, int pool, cudaStream_t 
     const long long room = std::max<long long>(1, (long long)sms * 32 / a.num_tokens);
     const int per = (int)((shares + std::min(shares, room) - 1) / std::min(shares, room));
     int part_steps = per * kLeast;
-    const int parts = (steps + part_steps - 1) / part_steps;
-    if (parts > 65535)
-        return cudaErrorInvalidConfiguration;
+    const int parts = (steps + part_steps - 1) / part_steps;  // at most 32 sms
     void *args[] = {&a, &part_steps};
     return launch_early(kern, dim3((unsigned)((a.num_tokens - 1) / (kThreads / 32) + 1), (unsigned)parts), kThreads, 0, stream, args);
 }
