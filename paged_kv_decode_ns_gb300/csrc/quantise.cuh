@@ -67,18 +67,14 @@ __device__ __forceinline__ void q4_quantize8(const float *x, uint32_t &codes, ui
     }
 }
 
-// Eight q4_0 codes (a word) and their step -> eight elements.  code - 8 is exact in either
-// type that the product is taken in, so fp16(d) * (code - 8) rounds once: a code in the low
-// bits of an fp16 1024 (an fp32 2^23), less that and 8, is code - 8.
-template <typename T>
-__device__ __forceinline__ uint4 q4_elements(uint32_t w, uint16_t d16);
-
-template <>
-__device__ __forceinline__ uint4 q4_elements<F16>(uint32_t w, uint16_t d16)
+// Eight q4_0 codes (a word) times d, as fp16.  code - 8 is exact in either type that the product
+// is taken in, so it rounds once: a code in the low bits of an fp16 1024 (an fp32 2^23), less that and
+// 8, is code - 8.
+__device__ __forceinline__ uint4 q4_halves(uint32_t w, __half2 d)
 {
     const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
     const uint32_t a = __byte_perm(even, odd, 0x5140), b = __byte_perm(even, odd, 0x7362);  // elements 0-3, 4-7
-    const __half2 off = __half2half2(__ushort_as_half(0x6408)), d = __half2half2(__ushort_as_half(d16));  // 1032
+    const __half2 off = __half2half2(__ushort_as_half(0x6408));  // 1032
     uint4 r = make_uint4(__byte_perm(a, 0x64646464u, 0x4140), __byte_perm(a, 0x64646464u, 0x4342),
                          __byte_perm(b, 0x64646464u, 0x4140), __byte_perm(b, 0x64646464u, 0x4342));
     __half2 *h = reinterpret_cast<__half2 *>(&r);
@@ -86,6 +82,16 @@ __device__ __forceinline__ uint4 q4_elements<F16>(uint32_t w, uint16_t d16)
     for (int i = 0; i < 4; ++i)
         h[i] = __hmul2(__hsub2(h[i], off), d);
     return r;
+}
+
+// Eight codes and their step (fp16 bits) -> eight elements.
+template <typename T>
+__device__ __forceinline__ uint4 q4_elements(uint32_t w, uint16_t d16);
+
+template <>
+__device__ __forceinline__ uint4 q4_elements<F16>(uint32_t w, uint16_t d16)
+{
+    return q4_halves(w, __half2half2(__ushort_as_half(d16)));
 }
 
 template <>

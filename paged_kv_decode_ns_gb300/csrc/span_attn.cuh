@@ -60,6 +60,7 @@
 #include <cstddef>
 
 #include "ns_internal.h"
+#include "quantise.cuh"
 #include "tcgen05.cuh"
 
 namespace ns {
@@ -370,21 +371,6 @@ __device__ __forceinline__ uint2 codes_to_f16(uint32_t w, __half2 d)
     __half2 *h = reinterpret_cast<__half2 *>(&r);
     h[0] = __hmul2(__hsub2(h[0], off), d);
     h[1] = __hmul2(__hsub2(h[1], off), d);
-    return r;
-}
-
-// Eight q4_0 codes (a word) -> four fp16 pairs of (code - 8) * d, the product rounded once.
-__device__ __forceinline__ uint4 nibbles_to_f16(uint32_t w, __half2 d)
-{
-    const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
-    const uint32_t a = __byte_perm(even, odd, 0x5140), b = __byte_perm(even, odd, 0x7362);  // elements 0-3, 4-7
-    const __half2 off = __half2half2(__ushort_as_half(0x6408));  // 1032
-    uint4 r = make_uint4(__byte_perm(a, 0x64646464u, 0x4140), __byte_perm(a, 0x64646464u, 0x4342),
-                         __byte_perm(b, 0x64646464u, 0x4140), __byte_perm(b, 0x64646464u, 0x4342));
-    __half2 *h = reinterpret_cast<__half2 *>(&r);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        h[i] = __hmul2(__hsub2(h[i], off), d);
     return r;
 }
 
@@ -903,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    *reinterpret_cast<uint4 *>(row + (((4 * c + i) ^ (key & 7)) << 4)) = nibbles_to_f16(w[i], dd[c]);
+                                    *reinterpret_cast<uint4 *>(row + (((4 * c + i) ^ (key & 7)) << 4)) = q4_halves(w[i], dd[c]);
                             } else {
                                 const __half2 s2 = c < 2 ? dd[0] : dd[1];
                                 const uint2 e0 = codes_to_f16(q.x, s2), e1 = codes_to_f16(q.y, s2),
