@@ -105,3 +105,29 @@ def test_large_scores_that_recur_across_pieces(q_amp, d):
     else:  # a rounding of each weight times its step by 2^-11, against values of 2^12 times 5; and the output's
         assert (np.abs(_gpu.to_f64(got) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -11 * 4096 * 5).all()
     assert _q4.status() == 0
+
+
+@pytest.mark.parametrize("dtype", [wl.F16, wl.BF16])
+@pytest.mark.parametrize("d,amp", [(64, 1.0), (64, 1e-4), (64, 30.0), (64, 3000.0), (128, 1.0), (128, 1e-2)])
+def test_every_element_is_off_by_its_roundings(dtype, d, amp):
+    """Element by element.  With weights p_j: the product of a weight and its step is off by 2^-11 of itself, so a sum
+    by 2^-11 sum p |v|; a score by what an fp32 sum of terms up to 15 |q_i| d and their 8 |q_i| d loses (2^-21 of
+    sum |q_i| 16 d), which moves the weights by as much, in numerator and denominator; sums of 700 terms
+    by 700 2^-24.  Then the output's own half step, or fp16's least one."""
+    rng = np.random.default_rng(8)
+    lens = [700, 40, 3]
+    cache = _q4.Cache(rng, lens, 2, 16, d, amp)
+    q = _q4.to16(rng.standard_normal((3, 14, d)).astype(np.float32), dtype)
+    scale = d ** -0.5 / amp
+    got = _gpu.to_f64(attend(cache, q, lens, scale, dtype))
+    half = torch.finfo(q.dtype).eps / 2
+    for s, n in enumerate(lens):
+        for j in range(14):
+            k, v = cache.k[s][:, j // 7], cache.v[s][:, j // 7]
+            x = q[s, j].double()
+            p = torch.softmax(scale * (k @ x), 0)
+            ref, size = p @ v, p @ v.abs()
+            off = scale * 2.0 ** -21 * 16 * float(x.abs().sum()) * amp  # (a step is 5/8 of that at most)
+            bound = half * ref.abs() + 2.0 ** -25 + (2.0 ** -11 + 2 * off + 700 * 2.0 ** -24) * size
+            err = (torch.from_numpy(got[s, j]) - ref).abs()
+            assert (err <= bound).all(), (s, j, float((err / bound).max()))
