@@ -967,7 +967,7 @@ cudaError_t launch_decode_q4(const Q4DecodeArgs &a, cudaStream_t stream)
     P.shift = a.block_size == 4 ? 2 : a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
     // a unit of the products has to be positive: q takes the scale's sign
     P.blocks = (uint32_t)std::min<long long>(a.num_blocks, 0x80000000LL);
-    P.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, kLeastUnit);
+    P.scale_log2 = std::fabs(a.scale) * 1.4426950408889634f;
     P.sign = a.scale < 0.f ? -1.f : 1.f;
     P.counters = a.counters;
     P.records = a.records;

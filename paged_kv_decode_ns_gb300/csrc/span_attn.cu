@@ -39,7 +39,7 @@ cudaError_t launch_span_attn(const SpanAttnArgs &a, int pool, cudaStream_t strea
     P.a = a;
     P.group = a.num_q_heads / a.num_kv_heads;
     P.qt = span::kRows / P.group;
-    P.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, span::kTinyScale);
+    P.scale_log2 = a.scale == 0.f ? span::kTinyScale : std::fabs(a.scale) * 1.4426950408889634f;
     P.negate = a.scale < 0.f;
     P.headers = static_cast<span::Header *>(a.workspace);
     P.records = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + span::header_bytes());

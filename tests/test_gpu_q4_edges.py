@@ -6,7 +6,7 @@ import torch
 import _gpu
 import _q4
 from _q4 import wl
-from _span import attend as exact_attend
+from _span import attend as exact_attend, compare as span_compare
 from paged_kv_decode_ns_gb300 import binding as nb
 
 pytestmark = pytest.mark.gpu
@@ -131,3 +131,27 @@ def test_every_element_is_off_by_its_roundings(dtype, d, amp):
             bound = half * ref.abs() + 2.0 ** -25 + (2.0 ** -11 + 2 * off + 700 * 2.0 ** -24) * size
             err = (torch.from_numpy(got[s, j]) - ref).abs()
             assert (err <= bound).all(), (s, j, float((err / bound).max()))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("call", ["decode", "spans", "prompts"])
+def test_scales_below_the_normal_numbers(call, d):
+    """Scores of ordinary size from a subnormal scale and large queries (a prompt's products stay below fp32's end)."""
+    rng = np.random.default_rng(9)
+    lens, scale = [1, 33, 400], float(np.float32(5e-40))
+    cache = _q4.Cache(rng, lens, 2, 16, d)
+    q = _q4.to16(rng.standard_normal((3, 14, d)).astype(np.float32) * np.float32(3e38 / (64 if call == "prompts" else 8)), wl.BF16)
+    one, out = _gpu.dev_ints([0, 1, 2, 3], np.int32), torch.full(q.shape, float("nan"), dtype=q.dtype, device="cuda")
+    k, v = cache.k, cache.v
+    if call == "decode":
+        out = attend(cache, q, lens, scale, wl.BF16)
+    elif call == "spans":
+        nb.ns_paged_attn_prefill_q4_0(q.cuda(), one, *cache.dev(), _gpu.dev_ints(lens, np.int32), scale, out,
+                                      nb.alloc_span_workspace(d))
+    else:
+        k, v = ([x.to(torch.bfloat16) for x in y] for y in (k, v))
+        nb.ns_prompt_attn(q.cuda(), torch.cat(k).cuda(), torch.cat(v).cuda(), one, scale, out, nb.alloc_span_workspace(d),
+                          key_start_loc=_gpu.dev_ints(np.cumsum([0] + lens), np.int32))
+    ref = torch.cat([exact_attend(q[s:s + 1], k[s], v[s], scale) for s in range(3)])
+    span_compare(out, ref, wl.BF16, q8=True)
+    assert _q4.status() == 0
