@@ -98,3 +98,21 @@ def test_calls_of_other_sizes_leave_a_workspace_ready(d, dtype, orc):
         torch.cuda.synchronize()
         assert _q4.same_bits(c.out, want[c]), f"{type(c).__name__}, {len(c.out)} rows"
     _gpu.assert_no_device_status()
+
+
+def test_a_workspace_of_both_widths_sizes_together(orc):
+    """head_dim 64 and 128 on one workspace, as large as the sizes for either together."""
+    rng = np.random.default_rng(9)
+    calls = [kind(rng, many, d, wl.F16, orc) for d in (64, 128) for kind in (Over4, Over16) for many in (True, False)]
+    want, sizes = [], [nb.ns_paged_attn_workspace_bytes(MANY, HQ, HKV, d) for d in (64, 128)]
+    for c, d in zip(calls, [64] * 4 + [128] * 4):
+        c.call(nb.alloc_workspace(MANY, HQ, HKV, d))
+        torch.cuda.synchronize()
+        want.append(c.out.clone())
+    ws = torch.zeros(sum(sizes), dtype=torch.uint8, device="cuda")
+    for i in (0, 5, 4, 1, 7, 2, 6, 3, 0, 1, 4, 5, 2, 3, 6, 7):
+        calls[i].out.fill_(float("nan"))
+        calls[i].call(ws)
+        torch.cuda.synchronize()
+        assert _q4.same_bits(calls[i].out, want[i]), f"{type(calls[i]).__name__}, call {i}"
+    _gpu.assert_no_device_status()
